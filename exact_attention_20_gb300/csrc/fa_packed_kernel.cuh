@@ -1,0 +1,717 @@
+// Attention over packed prompts for sm_103a: sequences of different lengths
+// one after another in [T][heads][d] tensors, with grouped heads.
+//
+// For token t of a sequence of L tokens and query head h (KV head h / G)
+//
+//     O[t,h] = sum_j softmax_j(scale q[t,h] . k[j,h/G]) v[j,h/G],
+//
+// j over the sequence's tokens, up to t under the causal mask; L[h,t] is the
+// logsumexp.  The tile pipeline is the one of fa_fwd_kernel.cuh (two 128-row
+// query tiles per CTA, S and O in tensor memory, one softmax warpgroup per
+// tile, two MMA issuers taking turns); what differs is what a tile is and how
+// work is divided:
+//
+// - A query tile holds all G query heads of one KV head for floor(128 / G)
+//   tokens, token after token (row = token * G + head).  The heads of a group
+//   share every K/V tile, so a K/V tile read once serves 256 rows whatever G
+//   is, and a short prompt fills G times as many rows as it has tokens.  G
+//   need not divide 128: the tile's last rows then stay unused.
+// - A work item is two such tiles, 2 floor(128 / G) tokens of one (sequence,
+//   KV head).  The host cuts the concatenated items into ranges of equal
+//   cost, one per CTA, as for the dense forward; an item cut between CTAs is
+//   computed in parts that meet in a workspace.
+// - K/V tiles start at their sequence's first token, wherever that lies in
+//   the packed tensors (the token is an outer TMA coordinate, so any start is
+//   fine).  The last tile runs past the item's visible keys, into later
+//   tokens, the next sequence or rows behind the last one.  Their scores are
+//   replaced by -inf; their V rows are zeroed in shared memory, since
+//   0 * NaN would reach every row.
+#pragma once
+
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+namespace packed {
+
+constexpr int kMaxCtas = 160;         // one CTA per SM
+constexpr int kMaxSeqs = 1024;        // sequences of one launch
+constexpr int kMaxParts = 8;          // parts of one split item
+constexpr int kCountersPerItem = 8;   // per query tile and warp quadrant
+constexpr int kSitePacked = 6;        // status code: a wait gave up
+
+// One part of a split item: its workspace slot, the item's first slot and
+// number of parts (consecutive slots), and the item's counters.  slot < 0:
+// the chunk is the whole item.
+struct Part {
+  int slot, slot0, count, k;
+};
+
+// A CTA's share: n_items consecutive items from (s, h, b), the first from
+// step_begin, the last up to step_end (a step is one 128-key tile).
+struct Range {
+  int s, h, b;
+  int n_items, step_begin, step_end;
+  Part first, last;
+};
+
+struct Params {
+  __nv_bfloat16* o;   // [T][Hq][D]
+  float* lse;         // [Hq][T]
+  int* status;        // device status word (0 = ok)
+  float* part_o;      // workspace: [slot][256 rows] of D fp32, a part's O normalised within it
+  float* part_lse;    // workspace: [slot][256], the part's natural-log logsumexp
+  int* counters;      // workspace: part arrivals, zero when the launch starts
+  int T, Hq, Hkv, G;
+  int tpt;            // tokens of a query tile: floor(128 / G)
+  float qk_scale;     // scale * log2(e)
+  unsigned long long wait_limit_ns;
+  int cu[kMaxSeqs + 1];  // first token of each sequence, and the end of the last
+  Range range[kMaxCtas];
+};
+
+// Key tiles that query tile t of block b visits (0 past the sequence's end).
+template <bool CAUSAL>
+__host__ __device__ __forceinline__ int tiles_for(int b, int t, int len, int tpt) {
+  const int t0 = (2 * b + t) * tpt;
+  if (t0 >= len) return 0;
+  const int last = CAUSAL ? (t0 + tpt < len ? t0 + tpt : len) - 1 : len - 1;
+  return last / kBlockN + 1;
+}
+
+// Steps of an item: the key tiles its longer query tile visits (under the
+// mask the later one, where it has tokens).
+template <bool CAUSAL>
+__host__ __device__ __forceinline__ int item_steps(int b, int len, int tpt) {
+  const int a = tiles_for<CAUSAL>(b, 0, len, tpt), c = tiles_for<CAUSAL>(b, 1, len, tpt);
+  return a > c ? a : c;
+}
+
+// The items of a CTA's range in turn.
+struct Cursor {
+  int s, h, b;
+  int begin, len;  // the sequence's first token and length
+  __device__ __forceinline__ void at(const Params& p) {
+    begin = p.cu[s];
+    len = p.cu[s + 1] - begin;
+  }
+  __device__ __forceinline__ Cursor(const Range& r, const Params& p) : s(r.s), h(r.h), b(r.b) { at(p); }
+  __device__ __forceinline__ void next(const Params& p) {
+    if (++b * 2 * p.tpt < len) return;
+    b = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do {  // sequences without tokens have no items
+      ++s;
+      at(p);
+    } while (len == 0);
+  }
+};
+
+// Key tiles [kb, ke) of one item, and the part it is.
+struct Chunk {
+  int kb, ke, steps;
+  Part part;
+};
+
+template <bool CAUSAL>
+__device__ __forceinline__ Chunk chunk_of(int i, const Cursor& c, const Range& r, const Params& p) {
+  Chunk ch;
+  ch.steps = item_steps<CAUSAL>(c.b, c.len, p.tpt);
+  ch.kb = i == 0 ? r.step_begin : 0;
+  ch.ke = i == r.n_items - 1 ? r.step_end : ch.steps;
+  ch.part = i == 0 ? r.first : r.last;
+  if (ch.kb == 0 && ch.ke == ch.steps) ch.part.slot = -1;
+  return ch;
+}
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Sync& sy, const Params& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t polls = 0;
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((++polls & 31u) == 0u) {
+      if (*sy.abort_flag) return false;
+      if (global_timer_ns() - t0 > p.wait_limit_ns) {
+        *sy.abort_flag = 1;
+        atomicCAS(p.status, 0, kSitePacked);
+        return false;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// TMA producer (one thread)
+// ---------------------------------------------------------------------------
+template <int D, bool CAUSAL>
+__device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                             uint32_t sbase, const Sync& sy, const Params& p) {
+  using C = Cfg<D>;
+  uint32_t q_loads[2] = {0, 0};
+  uint32_t kv_count = 0;
+  const uint64_t pol_q = l2_policy_evict_first();
+  const uint64_t pol_kv = l2_policy_evict_last();
+  const uint32_t q_bytes = static_cast<uint32_t>(p.G * p.tpt) * D * 2;
+  bool ok = true;
+  const Range& r = p.range[blockIdx.x];
+  Cursor c(r, p);
+  for (int i = 0; i < r.n_items && ok; ++i) {
+    if (i > 0) c.next(p);
+    const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
+    for (int t = 0; t < kQTiles; ++t) {
+      if (min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt)) <= ch.kb) continue;  // no key tile of its own here
+      ok = wait_phase(sy.q_empty[t], (q_loads[t] & 1u) ^ 1u, sy, p);
+      if (!ok) break;
+      ++q_loads[t];
+      mbar_arrive_expect_tx(sy.q_full[t], q_bytes);
+      const uint32_t dst = sbase + C::kQOff + t * C::kTileBytes;
+      const int token = c.begin + (2 * c.b + t) * p.tpt;
+#pragma unroll
+      for (int s = 0; s < C::kSlabs; ++s)
+        tma_load_3d_hint(dst + s * kSlabBytes, tmQ, sy.q_full[t], s * 64, c.h * p.G, token, pol_q);
+    }
+    for (int j = ch.kb; j < ch.ke && ok; ++j) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if (!ok) break;
+        const uint32_t slot = kv_count % C::kStages;
+        ok = wait_phase(sy.kv_empty0 + 8 * slot, ((kv_count / C::kStages) & 1u) ^ 1u, sy, p);
+        if (!ok) break;
+        const uint32_t full = sy.kv_full0 + 8 * slot;
+        mbar_arrive_expect_tx(full, C::kTileBytes);
+        const uint32_t dst = sbase + C::kKVOff + slot * C::kTileBytes;
+#pragma unroll
+        for (int s = 0; s < C::kSlabs; ++s)
+          tma_load_3d_hint(dst + s * kSlabBytes, n == 0 ? tmK : tmV, full, s * 64, c.h, c.begin + j * kBlockN, pol_kv);
+        ++kv_count;
+      }
+    }
+  }
+  // Every copy this thread started lands before the CTA exits, also after an abort.
+  const uint32_t first = kv_count > (uint32_t)C::kStages ? kv_count - C::kStages : 0;
+  for (uint32_t n = first; n < kv_count; ++n)
+    mbar_wait_bounded(sy.kv_full0 + 8 * (n % C::kStages), (n / C::kStages) & 1u, p.wait_limit_ns);
+  for (int t = 0; t < kQTiles; ++t)
+    if (q_loads[t] > 0) mbar_wait_bounded(sy.q_full[t], (q_loads[t] - 1) & 1u, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuers (one warp per query tile, strict turns, as in the dense forward)
+// ---------------------------------------------------------------------------
+template <int D, bool CAUSAL>
+__device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, uint32_t tmem, const Sync& sy,
+                                        const Params& p) {
+  using C = Cfg<D>;
+  const uint32_t bar_q_full = t ? sy.q_full[1] : sy.q_full[0];
+  const uint32_t bar_q_empty = t ? sy.q_empty[1] : sy.q_empty[0];
+  const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
+  const uint32_t bar_p_ready = t ? sy.p_ready[1] : sy.p_ready[0];
+  const uint32_t bar_o_done = t ? sy.o_done[1] : sy.o_done[0];
+  const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
+  const uint32_t my_turn = t ? sy.turn[1] : sy.turn[0];
+  const uint32_t next_turn = t ? sy.turn[0] : sy.turn[1];
+  const uint64_t q_desc = sdesc_advance(sdesc_sw128(sbase + C::kQOff, 16, 1024), t * C::kTileBytes);
+  const uint64_t k_desc0 = sdesc_sw128(sbase + C::kKVOff, 16, 1024);
+  const uint64_t v_desc0 = sdesc_sw128(sbase + C::kKVOff, kSlabBytes, 1024);
+  const uint32_t tm_s = tmem + t * 128;
+  const uint32_t tm_o = tmem + 256 + t * 128;
+  uint32_t q_uses = 0, kv_count = 0, pr_par = 0, of_par = 1, turn_par = 0;
+  bool ok = true;
+  auto full = [&](uint32_t c) { return sy.kv_full0 + 8 * (c % C::kStages); };
+  auto empty = [&](uint32_t c) { return sy.kv_empty0 + 8 * (c % C::kStages); };
+  const int lane = threadIdx.x & 31;
+  const bool leader = lane == 0;
+  auto wait_voted = [&](uint32_t bar, uint32_t par) {
+    ok = __all_sync(0xffffffffu, ok && wait_phase(bar, par, sy, p));
+  };
+  // Both issuers wait for every position of the ring, in order: a full
+  // barrier's wait is by parity and tells a fill only from the one before.
+  auto wait_full = [&](uint32_t c) { wait_voted(full(c), (c / C::kStages) & 1u); };
+  auto release_unused = [&](uint32_t c) {  // a K/V tile this query tile skips
+    wait_full(c);
+    if (ok && leader) mbar_arrive(empty(c));
+  };
+  if (t == 1 && leader) mbar_arrive(sy.turn[0]);  // tile 0 takes the first turn
+
+  const Range& r = p.range[blockIdx.x];
+  Cursor cur(r, p);
+  for (int i = 0; i < r.n_items && ok; ++i) {
+    if (i > 0) cur.next(p);
+    const Chunk ch = chunk_of<CAUSAL>(i, cur, r, p);
+    const int kb = ch.kb;
+    const int ne = min(ch.ke, tiles_for<CAUSAL>(cur.b, t, cur.len, p.tpt));  // this tile's key tiles: [kb, ne)
+    // The item's last V tile, where it is in this chunk: its rows from
+    // `visible` on belong to no visible key.  The first issuer that uses the
+    // tile zeroes them (the other is ordered behind it by the turn).
+    const int visible = (CAUSAL ? min((2 * cur.b + 2) * p.tpt, cur.len) : cur.len) - (ch.steps - 1) * kBlockN;
+    const int zero_at =
+        ch.ke == ch.steps && visible < kBlockN &&
+                (t == 0 || tiles_for<CAUSAL>(cur.b, 0, cur.len, p.tpt) < ch.steps)
+            ? ch.steps - 1
+            : -1;
+    if (ne > kb) {
+      wait_voted(bar_q_full, q_uses & 1u);
+      ++q_uses;
+    }
+    // step s issues O_t += P_t(s-1) V_{s-1} (if kb <= s-1 < ne) and S_t(s) (if s < ne)
+    for (int s = kb; s <= ch.ke && ok; ++s) {
+      const bool do_pv = s - 1 >= kb && s - 1 < ne;
+      const bool do_s = s < ne;
+      const uint32_t cv = kv_count + 2 * (s - 1 - kb) + 1;  // V_{s-1}
+      const uint32_t ck = kv_count + 2 * (s - kb);          // K_s
+      if (do_pv) {
+        wait_full(cv);
+        if (s - 1 == zero_at && ok) {
+          uint8_t* tile = smem + C::kKVOff + (cv % C::kStages) * C::kTileBytes;
+          const int rows = kBlockN - visible;
+          for (int n = lane; n < rows * 8 * C::kSlabs; n += 32) {  // whole 128-byte rows, so the swizzle is no matter
+            const int slab = n / (rows * 8), in = n % (rows * 8);
+            *reinterpret_cast<uint4*>(tile + slab * kSlabBytes + visible * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      if (do_s) wait_full(ck);
+      uint64_t dv[C::kPvInstr], dq[C::kQkInstr], dk[C::kQkInstr];
+      {
+        const uint64_t v0 = sdesc_advance(v_desc0, (cv % C::kStages) * C::kTileBytes);
+        const uint64_t k0 = sdesc_advance(k_desc0, (ck % C::kStages) * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < C::kPvInstr; ++kk) dv[kk] = sdesc_advance(v0, kk * 2048);
+#pragma unroll
+        for (int kk = 0; kk < C::kQkInstr; ++kk) {
+          const uint32_t off = (kk / 4) * kSlabBytes + (kk % 4) * 32;
+          dq[kk] = sdesc_advance(q_desc, off);
+          dk[kk] = sdesc_advance(k0, off);
+        }
+      }
+      const uint32_t acc0 = s > kb + 1 ? 1u : 0u;
+      if (do_pv) {
+        if (s == kb + 1) {
+          wait_voted(bar_o_free, of_par);
+          of_par ^= 1u;
+        }
+        wait_voted(bar_p_ready, pr_par);
+        pr_par ^= 1u;
+      }
+      wait_voted(my_turn, turn_par);
+      turn_par ^= 1u;
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (leader) {
+        if (do_pv) {
+          constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, /*b_mn_major=*/true);
+#pragma unroll
+          for (int kk = 0; kk < C::kPvInstr; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+        }
+        if (do_s) {
+          constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, /*b_mn_major=*/false);
+#pragma unroll
+          for (int kk = 0; kk < C::kQkInstr; ++kk) umma_ss(tm_s, dq[kk], dk[kk], idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        mbar_arrive(next_turn);
+        if (do_s) umma_commit(bar_s_full);
+        if (do_pv && !do_s) umma_commit(bar_o_done);
+        if (do_s && s == ne - 1) umma_commit(bar_q_empty);
+        if (do_pv) umma_commit(empty(cv));
+        if (do_s) umma_commit(empty(ck));
+      }
+      __syncwarp();
+      if (!do_pv && s - 1 >= kb) release_unused(cv);
+      if (!do_s && s < ch.ke) release_unused(ck);
+    }
+    kv_count += 2 * (ch.ke - kb);
+  }
+  // Every MMA this thread issued must finish before tensor memory is released.
+  if (leader) umma_commit(sy.drain);
+  __syncwarp();
+  mbar_wait_bounded(sy.drain, 0, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// Parts of split items
+// ---------------------------------------------------------------------------
+// A slot holds one part of an item, 256 rows of D fp32 values in groups of
+// eight columns, each group with its 256 rows one after the other, so that a
+// warp's 32-byte accesses to one group cover 1 KB.
+template <int D>
+__device__ __forceinline__ size_t part_index(int slot, int row, int group) {
+  return static_cast<size_t>(slot) * kItemRows * D + (static_cast<size_t>(group) * kItemRows + row) * 8;
+}
+
+// A warp's 32 rows of a part are in the workspace: counts the arrival, and
+// where it completes the item's parts merges them through their logsumexps
+// (L = ln sum_r exp(L_r), O = sum_r exp(L_r - L) O_r, the largest L_r
+// subtracted first; a part without keys for a row has L_r = -inf and weighs
+// 0).  Parts are added in key order whatever the order of arrival, so results
+// do not depend on timing.
+template <int D>
+__device__ __forceinline__ void arrive_and_merge(const Part& part, int t, int quad, int lane, bool store,
+                                                 __nv_bfloat16* orow, float* lse_dst, const Params& p) {
+  int* ctr = p.counters + part.k * kCountersPerItem + t * 4 + quad;
+  __threadfence();
+  __syncwarp();
+  int old = 0;
+  if (lane == 0) old = atomicAdd(ctr, 1);
+  if (__shfl_sync(0xffffffffu, old, 0) != part.count - 1) return;
+  (void)ld_acquire_gpu(ctr);  // every lane: the other parts' rows were fenced before their arrivals
+  const int r = t * kBlockM + quad * 32 + lane;
+  constexpr float kLog2e = 1.4426950408889634f;
+  float m = -INFINITY;
+  for (int i = 0; i < part.count; ++i) m = fmaxf(m, __ldcg(p.part_lse + static_cast<size_t>(part.slot0 + i) * kItemRows + r));
+  float w[kMaxParts];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts; ++i) {
+    w[i] = 0.f;
+    if (i < part.count) {
+      const float l = __ldcg(p.part_lse + static_cast<size_t>(part.slot0 + i) * kItemRows + r);
+      w[i] = l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e);
+      if (l != l) w[i] = l;  // a row whose scores are NaN stays NaN
+      sum += w[i];
+    }
+  }
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < kMaxParts; ++i) w[i] *= inv;
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    float acc[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+      if (i < part.count && w[i] != 0.f) {  // a part without keys was never written
+        float x[16];
+        ld_global_cg_v8(p.part_o + part_index<D>(part.slot0 + i, r, 2 * c), x);
+        ld_global_cg_v8(p.part_o + part_index<D>(part.slot0 + i, r, 2 * c + 1), x + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = fmaf(w[i], x[e], acc[e]);
+      }
+    }
+    if (store) {
+      uint4* dst = reinterpret_cast<uint4*>(orow + c * 16);
+      dst[0] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                          pack_bf16x2(acc[6], acc[7]));
+      dst[1] = make_uint4(pack_bf16x2(acc[8], acc[9]), pack_bf16x2(acc[10], acc[11]), pack_bf16x2(acc[12], acc[13]),
+                          pack_bf16x2(acc[14], acc[15]));
+    }
+  }
+  if (store) *lse_dst = m + logf(sum);
+}
+
+// ---------------------------------------------------------------------------
+// Softmax / correction / epilogue warpgroup (128 threads, one row each)
+// ---------------------------------------------------------------------------
+template <int D, bool CAUSAL>
+__device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy, const Params& p) {
+  const int lane = threadIdx.x & 31;
+  const int quad = (threadIdx.x >> 5) & 3;  // TMEM lanes 32*quad .. 32*quad+31
+  const int row_in_tile = quad * 32 + lane;
+  const int row_token = row_in_tile / p.G;  // the row's token within the tile
+  const int row_head = row_in_tile - row_token * p.G;
+  const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t tS = tmem + lane_off + t * 128;
+  const uint32_t tO = tmem + lane_off + 256 + t * 128;
+  const float qk = p.qk_scale;
+  const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
+  const uint32_t bar_p_ready = t ? sy.p_ready[1] : sy.p_ready[0];
+  const uint32_t bar_o_done = t ? sy.o_done[1] : sy.o_done[0];
+  const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
+  uint32_t s_par = 0, od_par = 0;
+  bool ok = true;
+
+  const Range& r = p.range[blockIdx.x];
+  Cursor c(r, p);
+  for (int i = 0; i < r.n_items && ok; ++i) {
+    if (i > 0) c.next(p);
+    const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
+    const int t0 = (2 * c.b + t) * p.tpt;  // the tile's first token within the sequence
+    const int ne = min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
+    const int token = t0 + row_token;
+    // rows without a query: past the sequence's end, or past the G * tpt rows of the tile
+    const bool store = row_token < p.tpt && token < c.len;
+    const int head = c.h * p.G + row_head;
+    __nv_bfloat16* orow =
+        store ? p.o + (static_cast<size_t>(c.begin + token) * p.Hq + head) * D : p.o;
+    float* lse_dst = store ? p.lse + static_cast<size_t>(head) * p.T + c.begin + token : p.lse;
+    if (ne <= ch.kb) {
+      // no key tile of this query tile lies in the chunk; a part still reports its rows, as an empty part
+      if (ch.part.slot >= 0) {
+        p.part_lse[static_cast<size_t>(ch.part.slot) * kItemRows + t * kBlockM + row_in_tile] = -INFINITY;
+        arrive_and_merge<D>(ch.part, t, quad, lane, store, orow, lse_dst, p);
+      }
+      continue;
+    }
+    const int seen = CAUSAL ? min(token, c.len - 1) : c.len - 1;  // the row's last visible key
+    const int first_masked = (CAUSAL ? min(t0, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
+    float m_ref = -INFINITY;  // reference maximum, in log2 units; moves on a jump above kRescaleThreshold
+    float l = 0.f;            // running sum of exp2(s*qk - m_ref), for the logsumexp
+    float lq = 0.f;           // the same terms rounded to bf16 (what P.V multiplies), for O
+
+    for (int j = ch.kb; j < ne; ++j) {
+      ok = wait_phase(bar_s_full, s_par, sy, p);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      s_par ^= 1u;
+      tc_fence_after_sync();
+
+      uint32_t s[128];
+      tmem_ld128_wait(tS, s);
+      if (CAUSAL ? j >= first_masked : (j == first_masked && (c.len & (kBlockN - 1)) != 0)) {
+        const int lim = seen - j * kBlockN;
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > lim) s[e] = __float_as_uint(-INFINITY);
+      }
+
+      const uint64_t qk2 = f2_pack(qk, qk);
+      float alpha = 1.f;
+      float sa, sb, lq_tile;
+      // One pass over the tile: exponentials against m_use, P stored to
+      // tensor memory over S, the fp32 and bf16 row sums, and (if asked) the
+      // tile's row maximum from the same values.
+      auto exp_pass = [&](float m_use, bool with_max) -> float {
+        const uint64_t negm2 = f2_pack(-m_use, -m_use);
+        uint64_t sum2 = f2_pack(0.f, 0.f);
+        float lqs[4] = {0.f, 0.f, 0.f, 0.f};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const int e = c4 * 32 + 2 * n;
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), qk2, negm2);
+            float xa, xb;
+            f2_unpack(x, xa, xb);
+            const float a = ex2_approx(xa);
+            const float b = ex2_approx(xb);
+            pk[n] = pack_bf16x2(a, b);
+            sum2 = f2_add(sum2, f2_pack(a, b));
+            add_bf16x2_halves(lqs[(n & 1) * 2], lqs[(n & 1) * 2 + 1], pk[n]);
+            if (with_max) mx[c4] = fmax3(mx[c4], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
+          tmem_st16(tS + c4 * 16, pk);
+        }
+        f2_unpack(sum2, sa, sb);
+        lq_tile = (lqs[0] + lqs[1]) + (lqs[2] + lqs[3]);
+        return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;  // qk > 0: max commutes with the scale
+      };
+      auto row_max = [&]() -> float {
+        float mx[4];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4)
+          mx[q4] = fmax3(__uint_as_float(s[32 * q4]), __uint_as_float(s[32 * q4 + 1]), __uint_as_float(s[32 * q4 + 2]));
+#pragma unroll
+        for (int e = 3; e < 31; e += 2) {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+            mx[q4] = fmax3(mx[q4], __uint_as_float(s[32 * q4 + e]), __uint_as_float(s[32 * q4 + e + 1]));
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) mx[q4] = fmaxf(mx[q4], __uint_as_float(s[32 * q4 + 31]));
+        return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;
+      };
+      if constexpr (CAUSAL) {
+        // the maximum first, then one pass (faster under the mask, with its many first tiles)
+        const float m_tile = row_max();
+        if (m_tile > m_ref + kRescaleThreshold<2>) {
+          alpha = ex2_approx(m_ref - m_tile);  // 0 when m_ref = -inf
+          m_ref = m_tile;
+        }
+        exp_pass(m_ref == -INFINITY ? 0.f : m_ref, false);  // 0: no key of this part visible yet, P = 0
+      } else {
+        // the exponentials against the current reference while the tile's
+        // maximum is found in the same pass; taken again where a row moved
+        if (m_ref == -INFINITY) {
+          m_ref = row_max();
+          alpha = 0.f;
+        }
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          const float m_tile = exp_pass(m_ref == -INFINITY ? 0.f : m_ref, true);
+          const bool move = m_tile > m_ref + kRescaleThreshold<2>;
+          if (!__any_sync(0xffffffffu, move)) break;
+          if (move) {
+            alpha = ex2_approx(m_ref - m_tile);
+            m_ref = m_tile;
+          }
+          tmem_st_wait();  // the repeated pass stores P over this one's
+        }
+      }
+      l = l * alpha + (sa + sb);
+      lq = lq * alpha + lq_tile;
+
+      if (j > ch.kb && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O_t holds the sum up to tile j-1: bring it to the new reference
+        const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+          uint32_t o[64];
+          tmem_ld64_wait(tO + e * 64, o);
+#pragma unroll
+          for (int n = 0; n < 32; ++n) {
+            float lo, hi;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1])), a2), lo, hi);
+            o[2 * n] = __float_as_uint(lo);
+            o[2 * n + 1] = __float_as_uint(hi);
+          }
+          tmem_st32(tO + e * 64, o);
+          tmem_st32(tO + e * 64 + 32, o + 32);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p_ready);  // one arrival per warp
+    }
+    if (!ok) break;
+
+    ok = wait_phase(bar_o_done, od_par, sy, p);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    od_par ^= 1u;
+    tc_fence_after_sync();
+    // a part may hold no visible key of a row (l = 0): its O is 0 and its logsumexp -inf
+    const float inv_l = l == 0.f ? 0.f : 1.f / lq;
+    const uint64_t il2 = f2_pack(inv_l, inv_l);
+    const float lse_row = (m_ref + log2f(l)) * 0.69314718055994531f;
+    const int r_item = t * kBlockM + row_in_tile;
+    // rows of O are 32-byte aligned when O is; the API promises 16
+    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      uint32_t o[32];
+      tmem_ld32_wait(tO + e * 32, o);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        float lo, hi;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1])), il2), lo, hi);
+        o[2 * n] = __float_as_uint(lo);
+        o[2 * n + 1] = __float_as_uint(hi);
+      }
+      if (ch.part.slot >= 0) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) st_global_v8(p.part_o + part_index<D>(ch.part.slot, r_item, e * 4 + n), o + n * 8);
+      } else if (store) {
+        uint32_t w[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) w[n] = pack_bf16x2(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1]));
+        if (wide) {
+          st_global_v8(orow + e * 32, w);
+          st_global_v8(orow + e * 32 + 16, w + 8);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(orow + e * 32);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) dst[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+        }
+      }
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_o_free);  // one arrival per warp
+    if (ch.part.slot < 0) {
+      if (store) *lse_dst = lse_row;
+    } else {
+      p.part_lse[static_cast<size_t>(ch.part.slot) * kItemRows + r_item] = lse_row;
+      arrive_and_merge<D>(ch.part, t, quad, lane, store, orow, lse_dst, p);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Kernel
+// ---------------------------------------------------------------------------
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(kNumThreads, 1)
+fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  Sync sy;
+  {
+    uint32_t b = sbase + C::kBarOff;
+    auto take = [&](int n) {
+      const uint32_t at = b;
+      b += 8 * n;
+      return at;
+    };
+    for (int t = 0; t < 2; ++t) sy.q_full[t] = take(1);
+    for (int t = 0; t < 2; ++t) sy.q_empty[t] = take(1);
+    sy.kv_full0 = take(C::kStages);
+    sy.kv_empty0 = take(C::kStages);
+    for (int t = 0; t < 2; ++t) sy.s_full[t] = take(1);
+    for (int t = 0; t < 2; ++t) sy.p_ready[t] = take(1);
+    for (int t = 0; t < 2; ++t) sy.o_done[t] = take(1);
+    for (int t = 0; t < 2; ++t) sy.o_free[t] = take(1);
+    sy.drain = take(1);
+    for (int t = 0; t < 2; ++t) sy.turn[t] = take(1);
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  sy.abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(sy.q_full[t], 1);
+      mbar_init(sy.q_empty[t], 1);
+      mbar_init(sy.s_full[t], 1);
+      mbar_init(sy.p_ready[t], kBlockM / 32);
+      mbar_init(sy.o_done[t], 1);
+      mbar_init(sy.o_free[t], kBlockM / 32);
+      mbar_init(sy.turn[t], 1);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(sy.kv_full0 + 8 * s, 1);
+      mbar_init(sy.kv_empty0 + 8 * s, 2);  // released by both MMA issuers
+    }
+    mbar_init(sy.drain, 2);
+    *sy.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kRegsAux>();
+    if (warp == kLoadWarp) {
+      if (lane == 0) run_producer<D, CAUSAL>(&tmQ, &tmK, &tmV, sbase, sy, p);
+      __syncwarp();
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      run_mma<D, CAUSAL>(warp - kMmaWarp, smem, sbase, tmem, sy, p);
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    run_softmax<D, CAUSAL>(warp >> 2, tmem, sy, p);
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace packed
+}  // namespace fa

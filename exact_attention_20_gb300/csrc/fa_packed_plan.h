@@ -1,0 +1,111 @@
+// Work division of the packed forward, on the host: the concatenated items of
+// one launch cut into contiguous ranges of about equal cost, one per CTA.
+#pragma once
+
+#include "fa_packed_kernel.cuh"
+
+namespace fa {
+namespace packed {
+
+// What an item costs beyond its steps, in steps: loading Q, the pipeline's
+// start, writing O.
+constexpr int kItemCost = 2;
+// An item is cut only where both sides keep this many steps: a part costs a
+// write and a read of 256 rows in fp32 besides.
+constexpr int kMinPartSteps = 4;
+// With no more items than CTAs, items are cut only while every CTA keeps this
+// many steps.
+constexpr int kMinStepsPerCta = 16;
+
+// Sequences cu[0..n] (n <= kMaxSeqs): fills p.range and returns the grid; the
+// number of workspace slots and of split items go to n_slots and n_split.
+template <bool CAUSAL>
+inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_slots, int& n_split) {
+  n_slots = n_split = 0;
+  const int most = num_ctas < kMaxCtas ? num_ctas : kMaxCtas;
+  long long weight = 0, items = 0;
+  int longest = 0;
+  for (int s = 0; s < n; ++s) {
+    const int len = p.cu[s + 1] - p.cu[s];
+    long long w = 0, k = 0;
+    for (int b = 0; b * 2ll * tpt < len; ++b, ++k) {
+      const int steps = item_steps<CAUSAL>(b, len, tpt);
+      longest = steps > longest ? steps : longest;
+      w += steps + kItemCost;
+    }
+    weight += w * Hkv;
+    items += k * Hkv;
+  }
+  if (items == 0) return 0;
+  long long ctas = items;
+  if (ctas < most) {
+    const long long by_work = weight / kMinStepsPerCta;
+    ctas = by_work > ctas ? by_work : ctas;
+    // an item meets at most kMaxParts ranges
+    const long long by_parts = weight * (kMaxParts - 2) / (longest + kItemCost);
+    if (ctas > items && ctas > by_parts) ctas = by_parts > items ? by_parts : items;
+  }
+  if (ctas > most) ctas = most;
+
+  int grid = 0;             // ranges closed so far
+  bool open = false;        // p.range[grid] has a first chunk
+  long long cut = 1, at = 0;
+  for (int s = 0; s < n; ++s) {
+    const int len = p.cu[s + 1] - p.cu[s];
+    for (int h = 0; h < Hkv; ++h) {
+      for (int b = 0; b * 2ll * tpt < len; ++b) {
+        const int steps = item_steps<CAUSAL>(b, len, tpt);
+        const long long w = steps + kItemCost;
+        // this item's parts: their ranges, patched when their number is known
+        int part_range[kMaxParts];
+        bool part_first[kMaxParts];
+        int parts = 0, done = 0;  // steps of the item already given to a range
+        auto begin = [&](int step) {
+          Range& r = p.range[grid];
+          if (!open) {
+            r = Range{s, h, b, 0, step, 0, Part{-1, 0, 0, 0}, Part{-1, 0, 0, 0}};
+            open = true;
+          }
+          ++r.n_items;
+        };
+        auto take = [&](int to) {  // the open range gets steps [done, to) of this item
+          begin(done);
+          p.range[grid].step_end = to;
+          if (done > 0 || to < steps) {
+            part_range[parts] = grid;
+            part_first[parts] = p.range[grid].n_items == 1;
+            ++parts;
+          }
+          done = to;
+        };
+        for (; cut < ctas && weight * cut / ctas < at + w; ++cut) {
+          const int off = static_cast<int>(weight * cut / ctas - at) - kItemCost / 2;
+          int step = off < 0 ? 0 : off > steps ? steps : off;
+          if (steps < 2 * kMinPartSteps) step = 2 * step < steps ? 0 : steps;
+          if (step - done < kMinPartSteps) step = done;
+          if (steps - step < kMinPartSteps && step > done) step = steps;
+          if (parts >= kMaxParts - 1 && step > done && step < steps) step = done;
+          if (step > done) take(step);
+          if (open && (step > 0 || done == 0)) {  // close the range here
+            ++grid;
+            open = false;
+          }
+        }
+        if (done < steps) take(steps);
+        at += w;
+        if (parts > 0) {
+          for (int i = 0; i < parts; ++i) {
+            Range& r = p.range[part_range[i]];
+            (part_first[i] ? r.first : r.last) = Part{n_slots + i, n_slots, parts, n_split};
+          }
+          n_slots += parts;
+          ++n_split;
+        }
+      }
+    }
+  }
+  return grid + (open ? 1 : 0);
+}
+
+}  // namespace packed
+}  // namespace fa

@@ -1,0 +1,165 @@
+"""GPU tests of the attention over packed prompts against its definition in 64 bits.
+
+Tolerances, from the roundings the operator documents.  With w the exact
+softmax weights, P's rounding to bf16 (relative error at most 2^-8) moves a row
+of O by at most 2^-7 sum_j w_j |v_j - O| <= 2^-7 (w|V| + |O|), since the weights
+are normalised by the sum of the rounded values; O's own rounding adds
+2^-8 |O|.  The fp32 scores, exponentials and sums move the weights by a
+relative error far below 2^-12 at these sizes (score error at most (d + 8)
+2^-24 scale sum|q||k|), taken as 2^-11 (w|V| + |O|).  Over a whole tensor of
+zero-mean values both roundings act as independent errors of at most
+2^-8 / sqrt(3) relative in the root mean square, together below 2^-8 of the
+tensor's norm.  The logsumexp moves by the score error, by len 2^-24 from its
+sum and by a few 2^-24 |LSE| from the logarithm.
+"""
+import math
+
+import pytest
+import torch
+
+from exact_attention_20_gb300 import build as fa_build
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def serve():
+    fa_build.build()
+    from exact_attention_20_gb300 import serve as mod
+    mod.lib()
+    return mod
+
+
+def make(lens, hq, hkv, d, seed=0, tail=0, fused=False):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    T = sum(lens) + tail
+    x = torch.randn((T, (hq + 2 * hkv) * d), generator=g, device=DEV).bfloat16()
+    q, k, v = x.split((hq * d, hkv * d, hkv * d), dim=1)
+    if not fused:
+        q, k, v = (t.contiguous() for t in (q, k, v))
+    return q.view(T, hq, d), k.view(T, hkv, d), v.view(T, hkv, d)
+
+
+def reference(q, k, v, lens, causal, scale):
+    """O, LSE, the row bound w|V| + |O| of every sequence's rows, and the largest scale sum|q||k|, in 64 bits."""
+    T, hq, d = q.shape
+    group = hq // k.shape[1]
+    o = torch.zeros((T, hq, d), dtype=torch.float64, device=DEV)
+    wv = torch.zeros_like(o)
+    lse = torch.zeros((hq, T), dtype=torch.float64, device=DEV)
+    most, at = 0.0, 0
+    for n in lens:
+        if n == 0:
+            continue
+        rows = slice(at, at + n)
+        qs, ks, vs = (t[rows].double().transpose(0, 1) for t in (q, k, v))
+        ks, vs = (t.repeat_interleave(group, 0) for t in (ks, vs))
+        s = qs @ ks.transpose(1, 2) * scale
+        most = max(most, float((qs.abs() @ ks.abs().transpose(1, 2)).max()) * scale)
+        if causal:
+            i = torch.arange(n, device=DEV)
+            hidden = i > i.unsqueeze(1)
+            s = s.masked_fill(hidden, -math.inf)
+        lse[:, rows] = torch.logsumexp(s, -1)
+        w = torch.softmax(s, -1)
+        o[rows] = (w @ vs).transpose(0, 1)
+        wv[rows] = (w @ vs.abs()).transpose(0, 1)
+        at += n
+    return o, lse, wv + o.abs(), most
+
+
+def check(serve, lens, hq, hkv, d, causal, seed=0, tail=0, fused=False):
+    q, k, v = make(lens, hq, hkv, d, seed, tail, fused)
+    scale = d ** -0.5
+    T, n = q.shape[0], sum(lens)
+    o = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((hq, T), 7.0, device=DEV)
+    serve.fa_fwd_packed(q, k, v, o, lse, lens, causal=causal, scale=scale)
+    torch.cuda.synchronize()
+    assert (o[n:] == 7.0).all() and (lse[:, n:] == 7.0).all(), "rows behind the last sequence were written"
+    o64, lse64, bound, most = reference(q, k, v, lens, causal, scale)
+    compare(o[:n], lse[:, :n], o64[:n], lse64[:, :n], bound[:n], most, d, max(lens, default=0))
+
+
+def compare(o, lse, o64, lse64, bound, most, d, longest):
+    err = (o.double() - o64).abs()
+    tol = (2.0 ** -7 + 2.0 ** -11) * bound + 2.0 ** -8 * o64.abs()
+    assert torch.isfinite(o.float()).all()
+    assert (err <= tol).all(), f"max excess {(err - tol).max().item():.3g} at {(err - tol).argmax().item()}"
+    if o64.numel() >= 4096:
+        assert err.norm() <= 2.0 ** -8 * o64.norm(), f"norm-wise {(err.norm() / o64.norm()).item():.3g}"
+    tol = (d + 8) * 2.0 ** -24 * most + (longest + 8) * 2.0 ** -24 + 2.0 ** -21 * lse64.abs()
+    assert ((lse.double() - lse64).abs() <= tol).all(), (lse.double() - lse64).abs().max()
+
+
+LENS = {
+    "one-token": [1],
+    "one-short": [37],
+    "tile-edges": [127, 128, 129, 1, 255, 256, 257],
+    "empty-ones": [0, 5, 0, 0, 300, 0],
+    "many-short": [1, 2, 3, 17, 31, 64, 5, 1, 1, 90] * 6,
+    "long": [1500],
+    "ragged": [700, 3, 1025, 64, 513],
+}
+
+
+@pytest.mark.parametrize("name", LENS)
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (8, 2), (8, 1), (6, 2), (5, 1), (28, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_matches_definition(serve, name, hq, hkv, d, causal):
+    check(serve, LENS[name], hq, hkv, d, causal, seed=len(name))
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 1), (48, 1), (128, 1), (130, 2)])
+def test_large_groups(serve, hq, hkv):
+    # few tokens to a tile: 4, 2, 1 and (65 heads) 1 with unused rows
+    check(serve, [5, 150, 1], hq, hkv, 64, True, seed=2)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_views_of_a_fused_projection_and_rows_behind(serve, d, causal):
+    check(serve, [33, 400, 129], 8, 2, d, causal, seed=3, tail=77, fused=True)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,causal", [
+    ([4096], 4, 1, True),             # few items: keys split over the CTAs
+    ([4096], 2, 2, False),
+    ([6000, 10, 2000], 8, 2, True),   # items cut by the equal ranges
+    ([3333, 3333], 12, 4, False),
+])
+def test_split_items(serve, lens, hq, hkv, causal):
+    import ctypes
+    arr = (ctypes.c_int * len(lens))(*lens)
+    need = ctypes.c_size_t(0)
+    rc = serve.lib().fa_fwd_packed_workspace(arr, len(lens), sum(lens), hq, hkv, 128, int(causal), ctypes.byref(need))
+    assert rc == 0 and need.value > 0, "the call must split items"
+    check(serve, lens, hq, hkv, 128, causal, seed=4)
+
+
+def test_more_sequences_than_one_launch_takes(serve):
+    lens = [(i * 7) % 13 for i in range(2500)]
+    check(serve, lens, 4, 2, 64, True, seed=5)
+
+
+def test_repeatable_bits(serve):
+    lens = [5000, 77, 1200]
+    q, k, v = make(lens, 8, 2, 128, seed=6)
+    first = serve.attention_packed(q, k, v, lens)
+    for _ in range(3):
+        again = serve.attention_packed(q, k, v, lens)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_no_tokens(serve):
+    q, k, v = make([0], 4, 2, 64, tail=3)
+    o = torch.full((3, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((4, 3), 7.0, device=DEV)
+    serve.fa_fwd_packed(q, k, v, o, lse, [])
+    serve.fa_fwd_packed(q, k, v, o, lse, [0, 0])
+    assert (o == 7.0).all() and (lse == 7.0).all()
+    o, lse = serve.attention_packed(q[:0], k[:0], v[:0], [0])
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
