@@ -16,11 +16,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = [os.path.join(PKG, "csrc", n) for n in ("fa_api.cu", "fa_noalloc.cu", "fa_bwd.cu", "fa_fp8.cu", "fa_packed.cu")]
+SOURCES = [os.path.join(PKG, "csrc", n) for n in ("fa_api.cu", "fa_noalloc.cu", "fa_bwd.cu", "fa_fp8.cu", "fa_packed.cu",
+                                                     "fa_kv4.cu")]
 DEPENDS = SOURCES + [
     os.path.join(PKG, "csrc", n)
     for n in ("fa_fwd_kernel.cuh", "fa_bwd_kernel.cuh", "fa_fp8_quant.cuh", "fa_decode.cuh", "sm103_ptx.cuh", "tma_host.h",
-              "fa_internal.h", "fa_packed_kernel.cuh", "fa_packed_plan.h")
+              "fa_internal.h", "fa_packed_kernel.cuh", "fa_packed_plan.h", "fa_kv4.cuh",
+              "fa_kv4_decode.cuh")
 ] + [os.path.join(ROOT, "include", n) for n in ("fa_gb300.h", "fa_gb300_serve.h")]
 
 COMPILE_FLAGS = [
