@@ -154,9 +154,10 @@ DecodePlan decode_plan(int n_seqs, int Lq, int G, int Hkv, int d, int max_pages,
     pl.grid = items;
     return pl;
   }
-  const long long resident = static_cast<long long>(num_sms) * (pl.nt == 1 ? 2 : 1);
+  const long long resident = static_cast<long long>(num_sms) * (pl.nt * d > 256 ? 1 : 2);  // DecodeCfg::kCtasPerSm
   pl.grid = std::min(resident, (items * std::min(tiles, 1ll << 24) + kv::kMinTiles - 1) / kv::kMinTiles);
-  pl.bytes = static_cast<size_t>(2 * pl.grid) * 8 * pl.nt * (d + 2) * 4;
+  // the parts' O, their (m, l), and the cuts
+  pl.bytes = static_cast<size_t>(2 * pl.grid) * 8 * pl.nt * (d + 2) * 4 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
   return pl;
 }
 
@@ -178,7 +179,7 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
   if (!pl.split) return FA_OK;
   // the merge may be set up while the first kernel runs; its CTAs wait for it
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.n_seqs) * p.Hkv * p.row_tiles));
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 8 * NT / kv::kMergeRows);
   cfg.blockDim = dim3(kv::kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -186,7 +187,7 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv::merge_kernel<D>, p, static_cast<int>(pl.grid), 8 * NT) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, kv::merge_kernel<D>, p, 8 * NT) != cudaSuccess)
     return FA_ERR_LAUNCH;
   return FA_OK;
 }
@@ -281,6 +282,7 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * pl.grid * 8 * pl.nt * d);
+  p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * pl.grid * 8 * pl.nt);
   p.errors = errors;
   p.status = view.status;
   p.q_stride = q_stride;
