@@ -147,17 +147,18 @@ DecodePlan decode_plan(int n_seqs, int Lq, int G, int Hkv, int d, int max_pages,
   pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   const long long items = static_cast<long long>(n_seqs) * Hkv * pl.row_tiles;
-  const long long tiles = (static_cast<long long>(max_pages) * page_size + kv::kTile - 1) / kv::kTile;  // of an item, at most
+  const long long units = (static_cast<long long>(max_pages) * page_size + kv::kUnit - 1) / kv::kUnit;  // of an item, at most
   // Items that cannot be longer than a CTA's least share are taken whole.
-  pl.split = tiles > kv::kMinTiles;
+  pl.split = units > kv::kMinUnits;
   if (!pl.split) {
     pl.grid = items;
     return pl;
   }
   const long long resident = static_cast<long long>(num_sms) * (pl.nt * d > 256 ? 1 : 2);  // DecodeCfg::kCtasPerSm
-  pl.grid = std::min(resident, (items * std::min(tiles, 1ll << 24) + kv::kMinTiles - 1) / kv::kMinTiles);
-  // the parts' O, their (m, l), and the cuts
-  pl.bytes = static_cast<size_t>(2 * pl.grid) * 8 * pl.nt * (d + 2) * 4 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
+  pl.grid = std::min(resident, (items * std::min(units, 1ll << 26) + kv::kMinUnits - 1) / kv::kMinUnits);
+  // parts: two of a CTA and one of each warp (O), the CTAs' (m, l), and the cuts
+  const size_t all_rows = static_cast<size_t>(pl.grid) * 8 * pl.nt;
+  pl.bytes = all_rows * (2 + kv::kWarps) * d * 4 + all_rows * 2 * 8 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
   return pl;
 }
 
@@ -280,9 +281,11 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
   p.seq_lens = seq_lens;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  const long long rows = pl.grid * 8 * pl.nt;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * pl.grid * 8 * pl.nt * d);
-  p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * pl.grid * 8 * pl.nt);
+  p.first_o = p.part_o + 2 * rows * d;
+  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kWarps * rows * d);
+  p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * rows);
   p.errors = errors;
   p.status = view.status;
   p.q_stride = q_stride;

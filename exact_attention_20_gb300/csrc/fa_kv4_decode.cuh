@@ -26,13 +26,14 @@
 //   maximum gives 2^8: f16 then loses nothing above 2^-33 of the maximum.
 //   P's rounding to f16 is 2^-11 relative; every sum is fp32.
 //
-// Work: the (sequence, KV head, row tile) items' 256-token tiles, concatenated,
-// are cut into equal ranges, one per CTA, from the lengths on the device.
-// Within a range each of the eight warps takes every eighth unit of 32 tokens
-// through a ring of its own (bulk copies, one unit ahead of the arithmetic
-// and across items), with its own online softmax; the warps' states are
-// combined at the end of an item, and the parts of an item cut between CTAs
-// by merge_kernel.
+// Work: the (sequence, KV head, row tile) items' units of 32 tokens,
+// concatenated, are cut into equal ranges, one per CTA, and a CTA's range into
+// eight, one per warp, from the lengths on the device.  A warp goes through
+// its range alone, with a ring of its own (bulk copies, two units ahead of the
+// arithmetic and across items) and an online softmax per item: an item that
+// lies within the range it writes itself.  Only the range's first and last
+// items may be shared; their states are combined once, at the CTA's end, and
+// what an item has in several CTAs by merge_kernel.
 #pragma once
 
 #include "fa_kv4.cuh"
@@ -43,17 +44,17 @@ namespace kv4 {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 2 * kGroup;       // tokens a warp takes at a time
-constexpr int kTile = kWarps * kUnit;   // tokens of one step of a CTA
-constexpr int kMinTiles = 2;            // tiles a CTA takes at least, where there are that many
+constexpr int kMinUnits = 2 * kWarps;   // units a CTA takes at least, where there are that many
 constexpr float kLift = 8.f;            // log2 of P at a maximum
 constexpr float kMove = 7.f;            // the reference moves on a jump above this many log2 units
 constexpr float kNone = -3.0e38f;       // reference of a row without keys yet
 constexpr int kSiteKv4 = 7;             // status code: a wait gave up
 
-// An item cut by the start of a CTA's range, at its first cut: parts lie with
-// CTAs c0 .. c1, the first in slot slot0, the others in slot 2 c.
+// An item cut by the start of a CTA's range, at its first cut: its parts lie
+// with CTAs c0 .. c1.  A CTA's slot 2c holds its part of the item that began
+// before its range, slot 2c + 1 that of the one that goes on behind it.
 struct Cut {
-  int s, item, c0, c1, slot0;  // s < 0: none
+  int s, item, c0, c1;  // s < 0: none
 };
 
 struct DecodeParams {
@@ -65,6 +66,7 @@ struct DecodeParams {
   float* lse;              // [Hq][n_seqs * Lq]
   float* part_o;           // workspace: [2 grid][rows][D], parts' O, not normalised
   float2* part_ml;         // workspace: [2 grid][rows], (m, l) in log2 units
+  float* first_o;          // workspace: [8 grid][rows][D], a warp's first item's O, not normalised
   Cut* cuts;               // workspace: [grid]
   int* errors;             // or null
   int* status;
@@ -83,29 +85,31 @@ struct DecodeCfg {
   static constexpr int kRows = 8 * NT;
   // O^T takes NT D / 4 registers of a lane.  Up to 64 of them, two CTAs (16
   // warps) fit an SM's registers, with Q in shared memory where it would take
-  // 32 more; a CTA's ring then has two units a warp (147 KB in all, 74 KB at
-  // the least in flight).
+  // 32 more; a CTA's ring then has three units a warp (216 KB an SM, two
+  // thirds of it in flight).
   static constexpr bool kWide = NT * D > 256;
   static constexpr int kCtasPerSm = kWide ? 1 : 2;
   static constexpr bool kSharedQ = NT * D >= 256;
-  static constexpr int kStages = D == 128 && !kWide ? 2 : 4;
-  static constexpr int kPad = 8;  // floats, so that rows of the combine buffer start in other banks
+  static constexpr int kStages = D == 64 ? (kSharedQ ? 4 : 5) : kWide ? 4 : kSharedQ ? 2 : 3;
+  static constexpr int kPad = 8;  // floats, so that rows of a state start in other banks
   static constexpr int kUnitBytes = 2 * group_bytes(D);
-  static constexpr int kRingBytes = kWarps * kStages * kUnitBytes;
-  static constexpr int kCombineAt = kRingBytes;                              // [warp][8 rows][D + pad] fp32
-  static constexpr int kMlAt = kCombineAt + kWarps * 8 * (D + kPad) * 4;     // [warp][rows] (m, l)
-  static constexpr int kQAt = kMlAt + kWarps * kRows * 8;                    // [NT][D / 16][lane] two words, then factors
-  static constexpr int kBarAt = kQAt + (kSharedQ ? NT * (D / 16) * 32 * 8 + kRows * 4 : 0);
+  static constexpr int kWarpRing = kStages * kUnitBytes;                  // at the end it holds the warp's last state:
+  static_assert(kRows * (D + kPad) * 4 <= kWarpRing, "[rows][D + pad] fp32");
+  static constexpr int kMlAt = kWarps * kWarpRing;                        // [warp][first, last][rows] (m, l)
+  static constexpr int kQBytes = kSharedQ ? NT * (D / 16) * 32 * 8 : 0;   // a warp's Q: [NT][D / 16][lane] two words
+  static constexpr int kQAt = kMlAt + kWarps * 2 * kRows * 8;
+  static constexpr int kBarAt = kQAt + kWarps * kQBytes;
   static constexpr int kSmemBytes = kBarAt + kWarps * kStages * 8;
 };
 
-// The items' tiles: a sequence has ceil(len / 256), one at least (so that
+// The items' units: a sequence has ceil(len / 32), one at least (so that
 // every output row has an item to write it).
 __device__ __forceinline__ int tokens_of(int s, const DecodeParams& p) {
   const long long most = min(static_cast<long long>(p.max_pages) << p.page_shift, 0x7fffff00ll);
   return max(0, static_cast<int>(min(static_cast<long long>(p.seq_lens[s]), most)));
 }
-__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+__device__ __forceinline__ int data_units(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int units_of(int len) { return max(1, data_units(len)); }
 
 // Exclusive scan of one value per thread over the block, and the total.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, long long& total) {
@@ -128,7 +132,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, 
   return before + x - v;
 }
 
-// The sequences' tiles, counted for one item of each: this thread's sequences
+// The sequences' units, counted for one item of each: this thread's sequences
 // [lo, hi) with their sum, the sum before them, and the total.
 struct Scan {
   long long mine, before, total;
@@ -138,34 +142,38 @@ struct Scan {
     lo = min(static_cast<int>(threadIdx.x) * per, p.n_seqs);
     hi = min(lo + per, p.n_seqs);
     mine = 0;
-    for (int s = lo; s < hi; ++s) mine += tiles_of(tokens_of(s, p));
+    for (int s = lo; s < hi; ++s) mine += units_of(tokens_of(s, p));
     before = block_scan(mine, s_sums, total);
   }
 };
 
-// A CTA's place in the concatenated items: the segment (tiles of one item) it
+// A warp's place in the concatenated items: the segment (units of one item) it
 // is at.  Only changed between segments.
 struct Walk {
-  int s, item;        // sequence, item within it (head * row_tiles + row tile)
-  int len, tiles;     // the sequence's
-  int t0, count;      // the segment's tiles: [t0, t0 + count)
-  int left;           // tiles from t0 to the end of the CTA's range; 0: done
-  __device__ __forceinline__ void set() { count = min(tiles - t0, left); }
+  int s, item;     // sequence, item within it (head * row_tiles + row tile)
+  int len, units;  // the sequence's
+  int u0, count;   // the segment's units: [u0, u0 + count)
+  int left;        // units from u0 to the end of the warp's range; 0: done
+  __device__ __forceinline__ void set() { count = min(units - u0, left); }
   __device__ __forceinline__ void next(const DecodeParams& p) {
     left -= count;
-    t0 = 0;
+    u0 = 0;
     if (left <= 0) return;
     if (++item == p.Hkv * p.row_tiles) {
       item = 0;
       ++s;
       len = tokens_of(s, p);
-      tiles = tiles_of(len);
+      units = units_of(len);
     }
     set();
   }
-  // the segment's units of 32 tokens: [first, end)
-  __device__ __forceinline__ int first_unit() const { return t0 * kWarps; }
-  __device__ __forceinline__ int end_unit() const { return min((t0 + count) * kWarps, (len + kUnit - 1) / kUnit); }
+  __device__ __forceinline__ int end() const { return min(u0 + count, data_units(len)); }  // of the units that hold tokens
+};
+
+// Where a warp's loads are: a segment and its next unit.
+struct LoadCursor {
+  Walk w;
+  int u;
 };
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -186,6 +194,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Row r (within the item's row tile) of item w: its place in O and LSE.
+struct RowPlace {
+  bool store;
+  long long token;
+  int head;
+};
+__device__ __forceinline__ RowPlace row_place(int s, int item, int r_in_tile, int rows, const DecodeParams& p) {
+  const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
+  const int r = rt * rows + r_in_tile;
+  const int i = r / p.G;
+  return RowPlace{r < p.Lq * p.G, static_cast<long long>(s) * p.Lq + i, h * p.G + r - i * p.G};
 }
 
 // Query rows to f16 fragments: lane (g, t) of row tile nt holds row 8 nt + g,
@@ -252,38 +273,77 @@ struct State {
     }
   }
 
-  // The item's query rows.  With Q in shared memory the whole CTA calls this
-  // at the same point, after a barrier behind the last use of the item before.
-  __device__ __forceinline__ void load_q(const Walk& w, const DecodeParams& p, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+  // The item's query rows (`words`: the warp's shared memory for them; every
+  // lane reads its own words only).
+  __device__ __forceinline__ void load_q(const Walk& w, const DecodeParams& p, uint2* words) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
     const int row0 = w.item % p.row_tiles * 8 * NT;
-    if constexpr (kSharedQ) {
-      uint2* words = reinterpret_cast<uint2*>(smem + DecodeCfg<D, NT>::kQAt);
-      float* factors = reinterpret_cast<float*>(words + NT * (D / 16) * 32);
-      if (warp < NT) {
+    q_shared = words + lane;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float factor;
+      if constexpr (kSharedQ) {
         uint32_t x[D / 16][2];
-        float factor;
-        load_q_rows<D>(warp, row0, w, p, x, factor);
+        load_q_rows<D>(nt, row0, w, p, x, factor);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) words[(warp * (D / 16) + i) * 32 + lane] = make_uint2(x[i][0], x[i][1]);
-        if (t == 0) factors[warp * 8 + (lane >> 2)] = factor;
-      }
-      __syncthreads();
-      q_shared = words + lane;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f[nt][0] = factors[nt * 8 + 2 * t];
-        f[nt][1] = factors[nt * 8 + 2 * t + 1];
-      }
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float factor;
+        for (int i = 0; i < D / 16; ++i) words[(nt * (D / 16) + i) * 32 + lane] = make_uint2(x[i][0], x[i][1]);
+      } else {
         load_q_rows<D>(nt, row0, w, p, q[nt], factor);
-        f[nt][0] = __shfl_sync(0xffffffffu, factor, 8 * t);  // lanes 4 r hold row r's
-        f[nt][1] = __shfl_sync(0xffffffffu, factor, 8 * t + 4);
       }
+      f[nt][0] = __shfl_sync(0xffffffffu, factor, 8 * t);  // lanes 4 r hold row r's
+      f[nt][1] = __shfl_sync(0xffffffffu, factor, 8 * t + 4);
     }
+  }
+
+  // l summed over the lanes that hold a row's keys.
+  __device__ __forceinline__ void sum_l() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+      }
+  }
+
+  // The state of a shared item, to [rows][stride] fp32 and [rows] (m, l).
+  __device__ __forceinline__ void save(float* o, int stride, float2* ml) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2)
+          *reinterpret_cast<float4*>(o + r * stride + (D / 8) * g + 2 * j) =
+              make_float4(acc[nt][j][e], acc[nt][j][2 + e], acc[nt][j + 1][e], acc[nt][j + 1][2 + e]);
+        if (g == 0) ml[r] = make_float2(m[nt][e], l[nt][e]);
+      }
+  }
+
+  // The whole of an item: O = O_acc v_scale / l in bf16, L = (m + log2 l) ln 2.
+  __device__ __forceinline__ void write(const Walk& w, const DecodeParams& p) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const RowPlace rp = row_place(w.s, w.item, nt * 8 + 2 * t + e, 8 * NT, p);
+        if (!rp.store) continue;
+        const float inv = l[nt][e] == 0.f ? 0.f : p.v_scale / l[nt][e];
+        uint4* dst = reinterpret_cast<uint4*>(p.o + (rp.token * p.Hq + rp.head) * D + (D / 8) * g);
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 4)
+          dst[j / 4] = make_uint4(pack_bf16x2(acc[nt][j][e] * inv, acc[nt][j][2 + e] * inv),
+                                  pack_bf16x2(acc[nt][j + 1][e] * inv, acc[nt][j + 1][2 + e] * inv),
+                                  pack_bf16x2(acc[nt][j + 2][e] * inv, acc[nt][j + 2][2 + e] * inv),
+                                  pack_bf16x2(acc[nt][j + 3][e] * inv, acc[nt][j + 3][2 + e] * inv));
+        if (g == 0)
+          p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] =
+              (m[nt][e] + log2f(l[nt][e])) * 0.69314718055994531f;
+      }
   }
 
   // S^T of one group of 16 keys at `st`.  Row g of a product is key
@@ -342,11 +402,11 @@ struct State {
     }
   }
 
-  // O^T += V^T P^T of one group.  tail: keys from `valid` on (counted within
-  // the group) lie past the sequence's end, and what is there may be NaN,
-  // which 0 * NaN would spread.
-  __device__ __forceinline__ void values(const uint8_t* st, const uint32_t* b0, const uint32_t* b1, bool tail, int pos,
-                                         const Walk& w, const DecodeParams& p) {
+  // O^T += V^T P^T of one group.  masked: keys may lie past the sequence's
+  // end, or (skip) none of the group is to be looked at; the scales there may
+  // be NaN, which 0 * NaN would spread (codes are always finite).
+  __device__ __forceinline__ void values(const uint8_t* st, const uint32_t* b0, const uint32_t* b1, bool masked,
+                                         uint32_t skip, int pos, const Walk& w, const DecodeParams& p) {
     constexpr int kHalf = D / 2, kBlocks = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint8_t* va = st + codes_at(D, 1) + t * kHalf + g * (D / 16);
@@ -354,11 +414,11 @@ struct State {
     uint32_t s[4];
 #pragma unroll
     for (int n = 0; n < 4; ++n) s[n] = sc[4 * n * kBlocks];
-    if (tail) {
+    if (masked) {
       uint32_t nan = 0;  // bit n: this lane's block of key t + 4n is NaN
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        if (pos + t + 4 * n >= w.len) s[n] = 0u;
+        if (skip != 0 || pos + t + 4 * n >= w.len) s[n] = 0u;
         nan |= ((s[n] & 0x7fu) == 0x7fu ? 1u : 0u) << n;
       }
       if (__any_sync(0xffffffffu, nan != 0)) {
@@ -437,7 +497,8 @@ struct State {
     float c[NG][NT][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) scores(st + n * group_bytes(D), c[n]);
-    if (tail || skip != 0) {
+    const bool masked = tail || skip != 0;
+    if (masked) {
       const int row0 = w.item % p.row_tiles * 8 * NT;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -508,24 +569,10 @@ struct State {
         b0[nt] = transpose8x8(pack_f16x2(p0, p1));
         b1[nt] = transpose8x8(pack_f16x2(p2, p3));
       }
-      if ((skip >> n) & 1u) continue;  // a skipped group's bytes are not a group's
-      values(st + n * group_bytes(D), b0, b1, tail, pos + n * kGroup, w, p);
+      values(st + n * group_bytes(D), b0, b1, masked, (skip >> n) & 1u, pos + n * kGroup, w, p);
     }
   }
 };
-
-// Row r (within the item's row tile) of item w: its place in O and LSE.
-struct RowPlace {
-  bool store;
-  long long token;
-  int head;
-};
-__device__ __forceinline__ RowPlace row_place(int s, int item, int r_in_tile, int rows, const DecodeParams& p) {
-  const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
-  const int r = rt * rows + r_in_tile;
-  const int i = r / p.G;
-  return RowPlace{r < p.Lq * p.G, static_cast<long long>(s) * p.Lq + i, h * p.G + r - i * p.G};
-}
 
 // O = O_acc v_scale / l as bf16 and L = (m + log2 l) ln 2 of four elements of a row.
 __device__ __forceinline__ void write_row(const RowPlace& rp, int D, int d4, float4 O, float M, float L,
@@ -537,216 +584,250 @@ __device__ __forceinline__ void write_row(const RowPlace& rp, int D, int d4, flo
     p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
+// A warp's shared items: its range's first (where that is not its last too) and last.
+struct Shared {
+  int s, item, u0, count, units;  // the item's units [u0, u0 + count) of `units`; count = 0: none
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode_kernel(const DecodeParams p) {
   using C = DecodeCfg<D, NT>;
   constexpr int kRows = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_sums[kWarps];
-  __shared__ Walk s_walk;
+  __shared__ Walk s_walk[kWarps];
+  __shared__ LoadCursor s_load[kWarps];
+  __shared__ Shared s_shared[kWarps][2];
+  __shared__ int s_entry[2 * kWarps], s_group[2 * kWarps + 1], s_groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint8_t* ring = smem + warp * C::kStages * C::kUnitBytes;
+  uint8_t* ring = smem + warp * C::kWarpRing;
   const uint32_t ring_u32 = smem_u32(ring);
   const uint32_t bar0 = smem_u32(smem + C::kBarAt) + warp * C::kStages * 8;
   if (lane == 0) {
     for (int st = 0; st < C::kStages; ++st) mbar_init(bar0 + 8 * st, 1);
     fence_barrier_init();
+    s_walk[warp].left = 0;
+    s_shared[warp][0].count = s_shared[warp][1].count = 0;
   }
 
-  // This CTA's range of the concatenated items' tiles.
+  // This CTA's range of the concatenated items' units, and its warps'.
   const int items = p.Hkv * p.row_tiles;  // of a sequence
   if (p.split) {
-    const Scan sc(p, s_sums);
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].s = -1;
+    const Scan sc(p, s_sums);  // a barrier, too
     const long long all = sc.total * items;
-    const long long ctas = min(static_cast<long long>(gridDim.x), (all + kMinTiles - 1) / kMinTiles);
+    const long long ctas = min(static_cast<long long>(gridDim.x), (all + kMinUnits - 1) / kMinUnits);
     const long long c = blockIdx.x;
     const long long begin = c < ctas ? all * c / ctas : all;
-    const long long end = c < ctas ? all * (c + 1) / ctas : all;
-    if (threadIdx.x == 0) {
-      s_walk.left = 0;
-      p.cuts[c].s = -1;
-    }
-    __syncthreads();
-    // the thread whose sequences hold tile `begin`
-    if (begin < end && begin >= sc.before * items && begin < (sc.before + sc.mine) * items) {
-      long long at = sc.before * items;
+    const int n = c < ctas ? static_cast<int>(min(all * (c + 1) / ctas - begin, 0x7fffffffll)) : 0;
+    const long long lo = sc.before * items, hi = (sc.before + sc.mine) * items;
+    if (begin < hi && begin + n > lo) {  // this thread's sequences hold some of it
+      long long at = lo;
+      int x = 0;  // the next warp's range to be found
       for (int s = sc.lo; s < sc.hi; ++s) {
-        const int len = tokens_of(s, p), n = tiles_of(len);
-        if (begin < at + static_cast<long long>(n) * items) {
-          const int item = static_cast<int>((begin - at) / n);
-          const long long a = at + static_cast<long long>(item) * n;  // the item's first tile
-          Walk w{s, item, len, n, static_cast<int>(begin - a), 0, static_cast<int>(min(end - begin, 0x7fffffffll))};
+        const int len = tokens_of(s, p), units = units_of(len);
+        const long long after = at + static_cast<long long>(units) * items;
+        for (; x < kWarps; ++x) {
+          const int from = static_cast<int>(static_cast<long long>(n) * x / kWarps);
+          const int left = static_cast<int>(static_cast<long long>(n) * (x + 1) / kWarps) - from;
+          const long long b = begin + from;  // the range's first unit
+          if (b >= after) break;
+          if (b < at || left == 0) continue;
+          const int item = static_cast<int>((b - at) / units);
+          const long long a = at + static_cast<long long>(item) * units;  // the item's first unit
+          Walk w{s, item, len, units, static_cast<int>(b - a), 0, left};
           w.set();
-          s_walk = w;
-          const long long prev = all * (c - 1) / ctas;  // where the range before this one starts
-          if (begin > a && prev <= a) {  // the item's first cut
+          s_walk[x] = w;
+          if (b == begin && b > a && all * (c - 1) / ctas <= a) {  // the item's first cut by a CTA's range
             long long c1 = c;
-            while (all * (c1 + 1) / ctas < a + n) ++c1;
-            p.cuts[c] = Cut{s, item, static_cast<int>(c - 1), static_cast<int>(c1),
-                            static_cast<int>(2 * (c - 1) + (prev == a ? 0 : 1))};
+            while (all * (c1 + 1) / ctas < a + units) ++c1;
+            p.cuts[c] = Cut{s, item, static_cast<int>(c - 1), static_cast<int>(c1)};
           }
-          break;
         }
-        at += static_cast<long long>(n) * items;
+        at = after;
       }
     }
-  } else if (threadIdx.x == 0) {
+  } else if (lane == 0) {
     // short items: CTA i takes item i whole
-    const int s = blockIdx.x / items, len = tokens_of(s, p), n = tiles_of(len);
-    s_walk = Walk{s, static_cast<int>(blockIdx.x) - s * items, len, n, 0, n, n};
+    const int s = blockIdx.x / items, len = tokens_of(s, p), units = units_of(len);
+    const int from = units * warp / kWarps, left = units * (warp + 1) / kWarps - from;
+    s_walk[warp] = Walk{s, static_cast<int>(blockIdx.x) - s * items, len, units, from, left, left};
   }
   __syncthreads();
-  Walk w = s_walk;
+  Walk w = s_walk[warp];
   if (p.errors && blockIdx.x == 0) {
     for (int s = threadIdx.x; s < p.n_seqs; s += kThreads)
       if (p.seq_lens[s] != tokens_of(s, p)) atomicOr(p.errors, kErrPosition);
   }
 
-  // The load cursor runs ahead of the arithmetic, through the same units; the
-  // page ids of the unit it is at are already on their way.
-  Walk lw = w;
-  int lu = 0, l_end = 0;        // the next unit to load, the end of its segment
-  const int* l_table = nullptr;
-  long long l_head = 0;         // the item's KV head within a page, in bytes
-  int page0 = -1, page1 = -1;   // its groups' pages
+  // The loads run ahead of the arithmetic, through the same units.  Up to 32
+  // units of a segment are looked up together, one by each lane, which later
+  // issues its unit's copies; the cursor is only touched then.
+  if (lane == 0) s_load[warp] = LoadCursor{w, w.u0};
+  __syncwarp();
   const int group_shift = p.page_shift - 4;  // log2 of a page's groups
-  const int group_mask = (1 << group_shift) - 1;
   const long long page_bytes = (static_cast<long long>(row_bytes(D)) << p.page_shift) * p.Hkv;
-  auto enter = [&]() {  // to the first segment from lw on that has a unit for this warp
-    while (lw.left > 0) {
-      lu = lw.first_unit() + warp;
-      l_end = lw.end_unit();
-      if (lu < l_end) {
-        l_table = p.page_table + static_cast<long long>(lw.s) * p.max_pages;
-        l_head = (static_cast<long long>(row_bytes(D)) << p.page_shift) * (lw.item / p.row_tiles);
-        return;
-      }
-      lw.next(p);
+  const uint8_t *src0 = nullptr, *src1 = nullptr;  // this lane's unit: its groups
+  uint32_t bad0 = 0, bad1 = 0;                     // lanes whose first, second group is not loaded
+  int batch = 0, next = 0;                         // units looked up, and issued of those
+  auto look_up = [&]() {
+    LoadCursor c = s_load[warp];
+    batch = next = 0;
+    while (c.w.left > 0 && c.u >= c.w.end()) {  // to the next segment that holds tokens
+      c.w.next(p);
+      c.u = c.w.u0;
     }
+    if (c.w.left > 0) {
+      batch = min(32, c.w.end() - c.u);
+      const int group = 2 * (c.u + lane);
+      int page0 = -1, page1 = -1;
+      const bool second = (group + 1) * kGroup < c.w.len;  // else it may lie past the sequence's last page
+      if (lane < batch) {
+        const int* table = p.page_table + static_cast<long long>(c.w.s) * p.max_pages;
+        page0 = __ldg(table + (group >> group_shift));
+        page1 = group_shift > 0 ? page0 : second ? __ldg(table + group + 1) : -1;
+      }
+      const bool ok0 = static_cast<uint32_t>(page0) < static_cast<uint32_t>(p.num_pages);
+      const bool ok1 = static_cast<uint32_t>(page1) < static_cast<uint32_t>(p.num_pages);
+      const uint8_t* head = p.cache + (static_cast<long long>(row_bytes(D)) << p.page_shift) * (c.w.item / p.row_tiles);
+      src0 = head + page0 * page_bytes + (group & ((1 << group_shift) - 1)) * group_bytes(D);
+      src1 = group_shift > 0 ? src0 + group_bytes(D) : head + page1 * page_bytes;
+      bad0 = __ballot_sync(0xffffffffu, lane < batch && !ok0);
+      bad1 = __ballot_sync(0xffffffffu, lane < batch && !ok1);
+      if (p.errors && lane < batch && (!ok0 || (!ok1 && second))) atomicOr(p.errors, kErrPage);
+      c.u += batch;
+    }
+    __syncwarp();
+    if (lane == 0) s_load[warp] = c;
+    __syncwarp();
   };
-  auto look_up = [&]() {  // the unit's pages; its second group may lie past the sequence's last page
-    if (lw.left <= 0) return;
-    page0 = __ldg(l_table + (2 * lu >> group_shift));
-    page1 = page0;
-    if (group_shift == 0) page1 = (2 * lu + 1) * kGroup < lw.len ? __ldg(l_table + 2 * lu + 1) : -2;
-  };
-  enter();
-  look_up();
-  uint32_t loads = 0;  // units asked for
-  uint32_t skips = 0;  // two bits per stage: groups that were not loaded
+  uint32_t loads = 0;     // units asked for
+  uint32_t load_at = 0;   // the stage the next one goes to
+  uint32_t skips = 0;     // two bits per stage: groups that were not loaded
   auto issue = [&]() {
-    if (lw.left <= 0) return;
-    const uint32_t st = loads % C::kStages, dst = ring_u32 + st * C::kUnitBytes, bar = bar0 + 8 * st;
-    const bool ok0 = static_cast<uint32_t>(page0) < static_cast<uint32_t>(p.num_pages);
-    const bool ok1 = static_cast<uint32_t>(page1) < static_cast<uint32_t>(p.num_pages);
-    skips = (skips & ~(3u << (2 * st))) | ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << (2 * st);
-    if (lane == 0) {
-      const uint8_t* src = p.cache + page0 * page_bytes + l_head + (2 * lu & group_mask) * group_bytes(D);
-      if (group_shift > 0) {  // both groups lie together
-        if (ok0) {
-          mbar_arrive_expect_tx(bar, C::kUnitBytes);
-          bulk_load(dst, src, C::kUnitBytes, bar);
-        } else {
-          mbar_arrive(bar);
-        }
-      } else {
-        mbar_arrive_expect_tx(bar, ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)) * group_bytes(D));
-        if (ok0) bulk_load(dst, src, group_bytes(D), bar);
-        if (ok1) bulk_load(dst + group_bytes(D), p.cache + page1 * page_bytes + l_head, group_bytes(D), bar);
+    if (next == batch) {
+      look_up();
+      if (batch == 0) return;
+    }
+    const uint32_t st = load_at, dst = ring_u32 + st * C::kUnitBytes, bar = bar0 + 8 * st;
+    if ((bad0 | bad1 | skips) == 0 && group_shift > 0) {  // the usual case: both groups lie together
+      if (lane == next) {
+        mbar_arrive_expect_tx(bar, C::kUnitBytes);
+        bulk_load(dst, src0, C::kUnitBytes, bar);
       }
-      if (p.errors && (!ok0 || (!ok1 && page1 != -2))) atomicOr(p.errors, kErrPage);
+    } else {
+      const uint32_t no0 = (bad0 >> next) & 1u, no1 = (bad1 >> next) & 1u;
+      skips = (skips & ~(3u << (2 * st))) | (no0 | no1 << 1) << (2 * st);
+      if (lane == next) {
+        mbar_arrive_expect_tx(bar, (2 - no0 - no1) * group_bytes(D));
+        if (no0 == 0) bulk_load(dst, src0, group_bytes(D), bar);
+        if (no1 == 0) bulk_load(dst + group_bytes(D), src1, group_bytes(D), bar);
+      }
     }
+    load_at = st + 1 == C::kStages ? 0 : st + 1;
+    ++next;
     ++loads;
-    lu += kWarps;
-    if (lu >= l_end) {
-      lw.next(p);
-      enter();
-    }
-    look_up();
   };
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  float* comb = reinterpret_cast<float*>(smem + C::kCombineAt);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlAt);
-  uint32_t used = 0;  // units taken from the ring
-  bool dead = false;  // a wait gave up
-  int slot = 2 * blockIdx.x;
+  float* first_o = p.first_o + (static_cast<long long>(blockIdx.x) * kWarps + warp) * kRows * D;
+  uint32_t used = 0;            // units taken from the ring
+  uint32_t at = 0, parity = 0;  // the stage of the next one, and its phase
+  bool dead = false;            // a wait gave up
   State<D, NT> state;
-  for (; w.left > 0; w.next(p), slot = 2 * blockIdx.x + 1) {
+#pragma unroll 1
+  for (bool first = true; w.left > 0; w.next(p), first = false) {
     state.reset();
-    state.load_q(w, p, smem);
-    const int end = w.end_unit();
+    state.load_q(w, p, reinterpret_cast<uint2*>(smem + C::kQAt + warp * C::kQBytes));
+    const int end = w.end();
     const int tail_from = w.len - p.Lq + 1;  // a unit that reaches past it is masked
-    for (int u = w.first_unit() + warp; u < end && !dead; u += kWarps) {
-      const uint32_t st = used % C::kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * st, (used / C::kStages) & 1, p.wait_limit_ns))) {
+#pragma unroll 1
+    for (int u = w.u0; u < end && !dead; ++u) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * at, parity, p.wait_limit_ns))) {
         dead = true;
         if (lane == 0) atomicCAS(p.status, 0, kSiteKv4);
         break;
       }
-      state.unit(ring + st * C::kUnitBytes, u * kUnit, (u + 1) * kUnit > tail_from, (skips >> (2 * st)) & 3u, w, p);
+      state.unit(ring + at * C::kUnitBytes, u * kUnit, (u + 1) * kUnit > tail_from, (skips >> (2 * at)) & 3u, w, p);
       __syncwarp();  // every lane has read the stage
       ++used;
+      if (++at == C::kStages) at = 0, parity ^= 1u;
       issue();
     }
-    // The warps' states: M = max m_w, O = sum O_w 2^(m_w - M), l likewise (a
-    // warp without keys has m = kNone, l = 0 and O = 0).
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = state.l[nt][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) s_ml[warp * kRows + nt * 8 + 2 * t + e] = make_float2(state.m[nt][e], l);
-      }
-    const bool whole = w.count == w.tiles;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        float* dst = comb + (warp * 8 + 2 * t) * (D + C::kPad) + (D / 8) * g + 2 * j;
-        *reinterpret_cast<float2*>(dst) = make_float2(state.acc[nt][j][0], state.acc[nt][j][2]);
-        *reinterpret_cast<float2*>(dst + D + C::kPad) = make_float2(state.acc[nt][j][1], state.acc[nt][j][3]);
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int idx = threadIdx.x; idx < 8 * D / 4; idx += kThreads) {
-        const int r = idx / (D / 4), d4 = idx % (D / 4) * 4;
-        float M = kNone;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) M = fmaxf(M, s_ml[x * kRows + nt * 8 + r].x);
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          const float2 ml = s_ml[x * kRows + nt * 8 + r];
-          const float f = exp2f(ml.x - M);
-          const float4 a = *reinterpret_cast<const float4*>(comb + (x * 8 + r) * (D + C::kPad) + d4);
-          L = fmaf(ml.y, f, L);
-          O.x = fmaf(a.x, f, O.x);
-          O.y = fmaf(a.y, f, O.y);
-          O.z = fmaf(a.z, f, O.z);
-          O.w = fmaf(a.w, f, O.w);
-        }
-        if (whole) {
-          const RowPlace rp = row_place(w.s, w.item, nt * 8 + r, kRows, p);
-          if (rp.store) write_row(rp, D, d4, O, M, L, p);
-        } else {
-          const long long row = static_cast<long long>(slot) * kRows + nt * 8 + r;
-          *reinterpret_cast<float4*>(p.part_o + row * D + d4) = O;
-          if (d4 == 0) p.part_ml[row] = make_float2(M, L);
-        }
-      }
-      __syncthreads();
+    state.sum_l();
+    if (w.count == w.units) {
+      state.write(w, p);
+      continue;
     }
+    // a shared item: the range's last goes where the ring was (nothing is on
+    // its way there any more), its first to the workspace
+    const int which = w.count == w.left ? 1 : 0;
+    if (lane == 0) s_shared[warp][which] = Shared{w.s, w.item, w.u0, w.count, w.units};
+    if (which == 1 && !dead)
+      state.save(reinterpret_cast<float*>(ring), D + C::kPad, s_ml + (warp * 2 + 1) * kRows);
+    else if (which == 0)
+      state.save(first_o, D, s_ml + warp * 2 * kRows);
   }
   // Copies still in flight land before the CTA exits (only after a wait gave up).
   for (; used < loads; ++used) mbar_wait_bounded(bar0 + 8 * (used % C::kStages), (used / C::kStages) & 1, p.wait_limit_ns);
+  __syncthreads();
+
+  // The shared items: entries (warp, first / last) in order, an item's are
+  // neighbours; the first warp lists them and where each item's start.
+  if (warp == 0) {
+    const Shared x = lane < 2 * kWarps ? s_shared[lane >> 1][lane & 1] : Shared{0, 0, 0, 0, 0};
+    const uint32_t used_mask = __ballot_sync(0xffffffffu, x.count > 0);
+    const uint32_t below = used_mask & ((1u << lane) - 1u);
+    const int before = below ? 31 - __clz(below) : lane;  // the entry before this one
+    const int s_before = __shfl_sync(0xffffffffu, x.s, before), item_before = __shfl_sync(0xffffffffu, x.item, before);
+    const bool starts = x.count > 0 && (below == 0 || s_before != x.s || item_before != x.item);
+    const uint32_t starts_mask = __ballot_sync(0xffffffffu, starts);
+    if (x.count > 0) s_entry[__popc(below)] = lane;
+    if (starts) s_group[__popc(starts_mask & ((1u << lane) - 1u))] = __popc(below);
+    if (lane == 0) {
+      s_groups = __popc(starts_mask);
+      s_group[__popc(starts_mask)] = __popc(used_mask);
+    }
+  }
+  __syncthreads();
+  // M = max m_e, O = sum O_e 2^(m_e - M), l likewise (a state without keys has
+  // m = kNone, l = 0 and O = 0).
+  const int total = s_groups * kRows * (D / 4);
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < total; idx += kThreads) {
+    const int group = idx / (kRows * (D / 4)), r = idx / (D / 4) % kRows, d4 = idx % (D / 4) * 4;
+    const int e0 = s_group[group], e1 = s_group[group + 1];
+    float M = kNone;
+    int count = 0;
+    for (int i = e0; i < e1; ++i) {
+      M = fmaxf(M, s_ml[s_entry[i] * kRows + r].x);
+      count += s_shared[s_entry[i] >> 1][s_entry[i] & 1].count;
+    }
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (int i = e0; i < e1; ++i) {
+      const int e = s_entry[i];
+      const float2 ml = s_ml[e * kRows + r];
+      const float f = ex2_approx(ml.x - M);
+      const float4 a = e & 1 ? *reinterpret_cast<const float4*>(smem + (e >> 1) * C::kWarpRing + (r * (D + C::kPad) + d4) * 4)
+                             : *reinterpret_cast<const float4*>(
+                                   p.first_o + ((static_cast<long long>(blockIdx.x) * kWarps + (e >> 1)) * kRows + r) * D + d4);
+      L = fmaf(ml.y, f, L);
+      O = make_float4(fmaf(a.x, f, O.x), fmaf(a.y, f, O.y), fmaf(a.z, f, O.z), fmaf(a.w, f, O.w));
+    }
+    const Shared& x = s_shared[s_entry[e0] >> 1][s_entry[e0] & 1];
+    if (count == x.units) {
+      const RowPlace rp = row_place(x.s, x.item, r, kRows, p);
+      if (rp.store) write_row(rp, D, d4, O, M, L, p);
+    } else {
+      const long long row = (2ll * blockIdx.x + (x.u0 > 0 ? 0 : 1)) * kRows + r;
+      *reinterpret_cast<float4*>(p.part_o + row * D + d4) = O;
+      if (d4 == 0) p.part_ml[row] = make_float2(M, L);
+    }
+  }
 }
 
 constexpr int kMergeRows = 2;  // rows of a CTA of merge_kernel
@@ -765,7 +846,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const DecodeParams p, i
   if (cut.s < 0) return;
   const int lane = threadIdx.x % kLanes, rr = threadIdx.x / kLanes % kMergeRows, side = threadIdx.x / (kLanes * kMergeRows);
   const int r = blockIdx.y * kMergeRows + rr;
-  auto row_of = [&](int c) { return static_cast<long long>(c == cut.c0 ? cut.slot0 : 2 * c) * rows + r; };
+  auto row_of = [&](int c) { return (2ll * c + (c == cut.c0 ? 1 : 0)) * rows + r; };
   float M = kNone, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAhead = 4;  // parts loaded together
