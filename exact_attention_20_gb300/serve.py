@@ -13,9 +13,10 @@ one.  The tensors' device need not be the current one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
+import operator
 
 import torch
 
@@ -60,33 +61,41 @@ def _checked(rc: int) -> None:
 
 
 class _Target:
-    """The device and stream of one call: ``with _Target(...) as handle`` makes them current."""
+    """The device and stream of one call: ``with _Target(...) as handle`` makes them current.
+
+    Without a stream the call runs on the device's current one, where the usual
+    case, tensors on the current device, needs no change of either.
+    """
+
+    __slots__ = ("context", "handle", "stream", "other")
 
     def __init__(self, device, stream):
         if device.type != "cuda":
             raise ValueError("tensors must be on a CUDA device")
-        self.device, self.other = device, None
+        self.context = self.stream = self.other = None
         if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-            self.context = (contextlib.nullcontext() if device.index == torch.cuda.current_device()
-                            else torch.cuda.device(device))
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
-                          else torch.cuda.default_stream(device))
-            if stream.device != device:
-                raise ValueError(f"stream must be on {device}, got {stream.device}")
-            caller = torch.cuda.current_stream(device)
-            self.stream, self.context = stream, torch.cuda.stream(stream)
-            if caller != stream:
-                self.other = caller
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            if torch._C._cuda_getDevice() != device.index:
+                self.context = torch.cuda.device(device)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}, got {stream.device}")
+        caller = torch.cuda.current_stream(device)
+        self.handle, self.context = stream.cuda_stream, torch.cuda.stream(stream)
+        if caller != stream:
+            self.stream, self.other = stream, caller
 
     def __enter__(self) -> int:
-        self.context.__enter__()
-        return self.stream.cuda_stream
+        if self.context is not None:
+            self.context.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        return self.context.__exit__(*exc)
+        if self.context is not None:
+            return self.context.__exit__(*exc)
 
     def uses(self, *tensors) -> None:
         """Keeps the tensors' memory from being reused before this call's work is done."""
@@ -102,43 +111,78 @@ class _Target:
         return tensors
 
 
-def _check_tokens(name, t, heads, d, device, dtype=torch.bfloat16, tokens=None) -> int:
-    """Checks a [T, heads, d] tensor whose tokens may be strided; returns the token stride in elements."""
+def _check(name, t, dtype, shape, device) -> None:
+    """fa._check, with the usual case decided in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        fa._check(name, t, dtype, shape, device)
+
+
+def _check_tokens(name, t, heads, d, device, tokens) -> int:
+    """Checks a bf16 [T, heads, d] tensor whose tokens may be strided; returns the token stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (tokens is not None and t.shape[0] != tokens):
-        want = ("T" if tokens is None else tokens, heads, d)
-        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (tokens, heads, d):
+        raise ValueError(f"{name} must have shape {(tokens, heads, d)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape[0] <= 1:  # one token's stride says nothing
-        if t.shape[0] == 1 and not t[0].is_contiguous():
-            raise ValueError(f"{name} must have the heads of a token contiguous")
+    token, head, element = t.stride()
+    if tokens == 0:
         return heads * d
-    if (heads > 1 and t.stride(1) != d) or t.stride(2) != 1:
+    if (heads > 1 and head != d) or element != 1:
         raise ValueError(f"{name} must have the heads of a token contiguous")
-    return t.stride(0)
+    return token if tokens > 1 else heads * d  # one token's stride says nothing
 
 
-def _scale(scale, d) -> float:
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+def _lengths(seq_lens, T):
+    """The lengths as a C array, and their number; checked here, since ctypes would wrap what an int does not hold."""
+    lens = [operator.index(x) for x in (seq_lens.tolist() if isinstance(seq_lens, torch.Tensor) else seq_lens)]
+    n, total = len(lens), sum(lens)
+    if n and min(lens) < 0:
+        raise ValueError("sequence lengths must not be negative")
+    if total > T:
+        raise ValueError(f"the sequences hold {total} tokens, the tensors {T}")
+    return (_I * n)(*lens), n
 
 
-def _lengths(seq_lens):
-    lens = [int(n) for n in (seq_lens.tolist() if isinstance(seq_lens, torch.Tensor) else seq_lens)]
-    if any(n < 0 or n > 1 << 30 for n in lens):
-        raise ValueError("sequence lengths must lie between 0 and 2^30")
-    return (ctypes.c_int * max(1, len(lens)))(*lens), len(lens), sum(lens)
-
-
-def _packed_shapes(q, k):
+def _packed(q, k, v, o, lse, seq_lens, causal, scale, stream):
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
         raise TypeError("q and k must be torch.Tensors")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, Hq, d] and k [T, Hkv, d]")
-    return q.shape[0], q.shape[1], k.shape[1], q.shape[2]
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    dev = q.device
+    target = _Target(dev, stream) if dev.type == "cuda" else None
+    strides = (_check_tokens("q", q, Hq, d, dev, T), _check_tokens("k", k, Hkv, d, dev, T),
+               _check_tokens("v", v, Hkv, d, dev, T))
+    lens, n = _lengths(seq_lens, T)
+    if o is not None:
+        _check("o", o, torch.bfloat16, (T, Hq, d), dev)
+        _check("lse", lse, torch.float32, (Hq, T), dev)
+    if target is None:
+        raise ValueError("tensors must be on a CUDA device")
+    c = lib()
+    causal = 1 if causal else 0
+    with target as handle:
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), lens, n, T, Hq, Hkv, d, *strides,
+                causal, 1.0 / math.sqrt(d) if scale is None else scale)
+        # most calls split no item and need no workspace; the others are told so, with nothing launched
+        rc = c.fa_fwd_packed(*args, None, 0, handle)
+        if rc == fa.FA_ERR_SCRATCH:
+            need = _Z(0)
+            _checked(c.fa_fwd_packed_workspace(lens, n, T, Hq, Hkv, d, causal, ctypes.byref(need)))
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+            rc = c.fa_fwd_packed(*args, ws.data_ptr(), need.value, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    target.uses(q, k, v)
+    return target, o, lse
 
 
 def fa_fwd_packed(q, k, v, o, lse, seq_lens, causal: bool = True, scale: float | None = None,
@@ -152,25 +196,10 @@ def fa_fwd_packed(q, k, v, o, lse, seq_lens, causal: bool = True, scale: float |
     follows the ones before it.  Query head h reads KV head h // (Hq // Hkv).
     Rows of tokens behind the last sequence are left as they were.
     """
-    T, Hq, Hkv, d = _packed_shapes(q, k)
-    dev = q.device
-    strides = [_check_tokens("q", q, Hq, d, dev), _check_tokens("k", k, Hkv, d, dev, tokens=T),
-               _check_tokens("v", v, Hkv, d, dev, tokens=T)]
-    fa._check("o", o, torch.bfloat16, (T, Hq, d), dev)
-    fa._check("lse", lse, torch.float32, (Hq, T), dev)
-    lens, n, total = _lengths(seq_lens)
-    if total > T:
-        raise ValueError(f"the sequences hold {total} tokens, the tensors {T}")
-    c = lib()
-    target = _Target(dev, stream)
-    need = ctypes.c_size_t(0)
-    with target as handle:
-        _checked(c.fa_fwd_packed_workspace(lens, n, T, Hq, Hkv, d, int(bool(causal)), ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        _checked(c.fa_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), lens, n, T,
-                                 Hq, Hkv, d, *strides, int(bool(causal)), _scale(scale, d),
-                                 None if ws is None else ws.data_ptr(), need.value, handle))
-    target.uses(q, k, v, o, lse)
+    if o is None or lse is None:
+        raise TypeError("o and lse must be torch.Tensors")
+    target, _, _ = _packed(q, k, v, o, lse, seq_lens, causal, scale, stream)
+    target.uses(o, lse)
 
 
 def attention_packed(q, k, v, seq_lens, causal: bool = True, scale: float | None = None, stream=None):
@@ -178,12 +207,7 @@ def attention_packed(q, k, v, seq_lens, causal: bool = True, scale: float | None
 
     Rows of tokens behind the last sequence hold nothing of use.
     """
-    T, Hq, _, d = _packed_shapes(q, k)
-    target = _Target(q.device, stream)
-    with target:
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    fa_fwd_packed(q, k, v, o, lse, seq_lens, causal=causal, scale=scale, stream=stream)
+    target, o, lse = _packed(q, k, v, None, None, seq_lens, causal, scale, stream)
     return target.gives(o, lse)
 
 
@@ -209,12 +233,14 @@ def kv4_cache(num_pages: int, n_kv_heads: int, d: int, page_size: int = 64, devi
 class _Cache:
     """A cache with its tables, checked: the arguments its entry points share."""
 
+    __slots__ = ("device", "pages", "heads", "page_size", "n", "max_pages", "tensors", "errors")
+
     def __init__(self, cache, page_table, seq_lens, d, errors):
-        if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.dtype != torch.uint8:
+        if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.dtype is not torch.uint8:
             raise TypeError("cache must be a uint8 tensor [pages, KV heads, bytes]")
         if not cache.is_contiguous():
             raise ValueError("cache must be contiguous")
-        self.device = cache.device
+        dev = self.device = cache.device
         self.pages, self.heads, page_bytes = cache.shape
         self.page_size, rest = divmod(page_bytes, kv4_row_bytes(d))
         if rest:
@@ -222,12 +248,13 @@ class _Cache:
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be an int32 tensor [sequences, pages]")
         self.n, self.max_pages = page_table.shape
-        fa._check("page_table", page_table, torch.int32, page_table.shape, self.device)
-        fa._check("seq_lens", seq_lens, torch.int32, (self.n,), self.device)
-        if errors is not None:
-            fa._check("errors", errors, torch.int32, (1,), self.device)
-        self.tensors = [t for t in (cache, page_table, seq_lens, errors) if t is not None]
-        self.errors = None if errors is None else errors.data_ptr()
+        _check("page_table", page_table, torch.int32, page_table.shape, dev)
+        _check("seq_lens", seq_lens, torch.int32, (self.n,), dev)
+        if errors is None:
+            self.tensors, self.errors = (cache, page_table, seq_lens), None
+        else:
+            _check("errors", errors, torch.int32, (1,), dev)
+            self.tensors, self.errors = (cache, page_table, seq_lens, errors), errors.data_ptr()
 
 
 def kv4_store(cache, k, v, page_table, seq_lens, cu_seqlens, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -246,15 +273,34 @@ def kv4_store(cache, k, v, page_table, seq_lens, cu_seqlens, k_scale: float = 1.
         raise ValueError("k must be a bf16 tensor [T, KV heads, d]")
     T, heads, d = k.shape
     c = _Cache(cache, page_table, seq_lens, d, errors)
-    strides = [_check_tokens("k", k, c.heads, d, c.device), _check_tokens("v", v, c.heads, d, c.device, tokens=T)]
-    fa._check("cu_seqlens", cu_seqlens, torch.int32, (c.n + 1,), c.device)
+    strides = _check_tokens("k", k, c.heads, d, c.device, T), _check_tokens("v", v, c.heads, d, c.device, T)
+    _check("cu_seqlens", cu_seqlens, torch.int32, (c.n + 1,), c.device)
     target = _Target(c.device, stream)
     with target as handle:
         _checked(lib().fa_kv4_store(k.data_ptr(), v.data_ptr(), cache.data_ptr(), page_table.data_ptr(),
                                     seq_lens.data_ptr(), cu_seqlens.data_ptr(), T, c.n, c.max_pages, c.pages,
-                                    c.page_size, c.heads, d, *strides, float(k_scale), float(v_scale), c.errors,
+                                    c.page_size, c.heads, d, *strides, k_scale, v_scale, c.errors,
                                     handle))
     target.uses(k, v, cu_seqlens, *c.tensors)
+
+
+def _load(cache, page_table, seq_lens, cu_seqlens, k, v, n_tokens, d, k_scale, v_scale, errors, stream):
+    c = _Cache(cache, page_table, seq_lens, d, errors)
+    dev, shape = c.device, (n_tokens, c.heads, d)
+    _check("cu_seqlens", cu_seqlens, torch.int32, (c.n + 1,), dev)
+    if k is not None:
+        _check("k", k, torch.bfloat16, shape, dev)
+        _check("v", v, torch.bfloat16, shape, dev)
+    target = _Target(dev, stream)
+    with target as handle:
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _checked(lib().fa_kv4_load(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                   cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), n_tokens, c.n, c.max_pages,
+                                   c.pages, c.page_size, c.heads, d, k_scale, v_scale, c.errors, handle))
+    target.uses(cu_seqlens, *c.tensors)
+    return target, k, v
 
 
 def fa_kv4_load(cache, page_table, seq_lens, cu_seqlens, k, v, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -267,17 +313,9 @@ def fa_kv4_load(cache, page_table, seq_lens, cu_seqlens, k, v, k_scale: float = 
     """
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a bf16 tensor [T, KV heads, d]")
-    T, _, d = k.shape
-    c = _Cache(cache, page_table, seq_lens, d, errors)
-    fa._check("k", k, torch.bfloat16, (T, c.heads, d), c.device)
-    fa._check("v", v, torch.bfloat16, (T, c.heads, d), c.device)
-    fa._check("cu_seqlens", cu_seqlens, torch.int32, (c.n + 1,), c.device)
-    target = _Target(c.device, stream)
-    with target as handle:
-        _checked(lib().fa_kv4_load(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                                   cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), T, c.n, c.max_pages, c.pages,
-                                   c.page_size, c.heads, d, float(k_scale), float(v_scale), c.errors, handle))
-    target.uses(k, v, cu_seqlens, *c.tensors)
+    target, _, _ = _load(cache, page_table, seq_lens, cu_seqlens, k, v, k.shape[0], k.shape[2], k_scale, v_scale, errors,
+                         stream)
+    target.uses(k, v)
 
 
 def kv4_load(cache, page_table, seq_lens, cu_seqlens, n_tokens: int, d: int, k_scale: float = 1.0,
@@ -286,15 +324,44 @@ def kv4_load(cache, page_table, seq_lens, cu_seqlens, n_tokens: int, d: int, k_s
 
     Rows outside all sequences hold nothing of use.
     """
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
-        raise TypeError("cache must be a uint8 tensor [pages, KV heads, bytes]")
-    target = _Target(cache.device, stream)
-    with target:
-        k = torch.empty((n_tokens, cache.shape[1], d), dtype=torch.bfloat16, device=cache.device)
-        v = torch.empty_like(k)
-    fa_kv4_load(cache, page_table, seq_lens, cu_seqlens, k, v, k_scale=k_scale, v_scale=v_scale, errors=errors,
-                stream=stream)
+    target, k, v = _load(cache, page_table, seq_lens, cu_seqlens, None, None, n_tokens, d, k_scale, v_scale, errors,
+                         stream)
     return target.gives(k, v)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(device_index, n, n_queries, Hq, heads, d, max_pages, page_size) -> int:
+    """fa_kv4_attention_workspace for these sizes (on the current device, which device_index names)."""
+    need = _Z(0)
+    _checked(lib().fa_kv4_attention_workspace(n, n_queries, Hq, heads, d, max_pages, page_size, ctypes.byref(need)))
+    return need.value
+
+
+def _kv4_attention(q, cache, page_table, seq_lens, o, lse, n_queries, scale, k_scale, v_scale, errors, stream):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a bf16 tensor [T, Hq, d]")
+    T, Hq, d = q.shape
+    c = _Cache(cache, page_table, seq_lens, d, errors)
+    dev = c.device
+    if n_queries < 1:
+        raise ValueError("n_queries must be at least 1")
+    stride = _check_tokens("q", q, Hq, d, dev, c.n * n_queries)
+    if o is not None:
+        _check("o", o, torch.bfloat16, (T, Hq, d), dev)
+        _check("lse", lse, torch.float32, (Hq, T), dev)
+    target = _Target(dev, stream)
+    with target as handle:
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        need = _attention_workspace(dev.index, c.n, n_queries, Hq, c.heads, d, c.max_pages, c.page_size)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _checked(lib().fa_kv4_attention(q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                        o.data_ptr(), lse.data_ptr(), c.n, n_queries, Hq, c.heads, d, c.max_pages,
+                                        c.pages, c.page_size, stride, 1.0 / math.sqrt(d) if scale is None else scale,
+                                        k_scale, v_scale, c.errors, None if ws is None else ws.data_ptr(), need, handle))
+    target.uses(q, *c.tensors)
+    return target, o, lse
 
 
 def fa_kv4_attention(q, cache, page_table, seq_lens, o, lse, n_queries: int = 1, scale: float | None = None,
@@ -307,39 +374,16 @@ def fa_kv4_attention(q, cache, page_table, seq_lens, o, lse, n_queries: int = 1,
     the positions up to its own; one that sees none gets O = 0, LSE = -inf.
     o: bf16 like q, lse: fp32 [Hq, sequences * n_queries], contiguous.
     """
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a bf16 tensor [T, Hq, d]")
-    T, Hq, d = q.shape
-    c = _Cache(cache, page_table, seq_lens, d, errors)
-    if n_queries < 1:
-        raise ValueError("n_queries must be at least 1")
-    stride = _check_tokens("q", q, Hq, d, c.device, tokens=c.n * n_queries)
-    fa._check("o", o, torch.bfloat16, (T, Hq, d), c.device)
-    fa._check("lse", lse, torch.float32, (Hq, T), c.device)
-    target = _Target(c.device, stream)
-    need = ctypes.c_size_t(0)
-    handle_lib = lib()
-    with target as handle:
-        _checked(handle_lib.fa_kv4_attention_workspace(c.n, n_queries, Hq, c.heads, d, c.max_pages, c.page_size,
-                                                       ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=c.device) if need.value else None
-        _checked(handle_lib.fa_kv4_attention(q.data_ptr(), cache.data_ptr(), page_table.data_ptr(),
-                                             seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), c.n, n_queries, Hq,
-                                             c.heads, d, c.max_pages, c.pages, c.page_size, stride, _scale(scale, d),
-                                             float(k_scale), float(v_scale), c.errors,
-                                             None if ws is None else ws.data_ptr(), need.value, handle))
-    target.uses(q, o, lse, *c.tensors)
+    if o is None or lse is None:
+        raise TypeError("o and lse must be torch.Tensors")
+    target, _, _ = _kv4_attention(q, cache, page_table, seq_lens, o, lse, n_queries, scale, k_scale, v_scale, errors,
+                                  stream)
+    target.uses(o, lse)
 
 
 def kv4_attention(q, cache, page_table, seq_lens, n_queries: int = 1, scale: float | None = None,
                   k_scale: float = 1.0, v_scale: float = 1.0, errors=None, stream=None):
     """Allocating form of fa_kv4_attention: returns (O, LSE)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a bf16 tensor [T, Hq, d]")
-    target = _Target(q.device, stream)
-    with target:
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    fa_kv4_attention(q, cache, page_table, seq_lens, o, lse, n_queries=n_queries, scale=scale, k_scale=k_scale,
-                     v_scale=v_scale, errors=errors, stream=stream)
+    target, o, lse = _kv4_attention(q, cache, page_table, seq_lens, None, None, n_queries, scale, k_scale, v_scale,
+                                    errors, stream)
     return target.gives(o, lse)

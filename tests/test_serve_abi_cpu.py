@@ -180,12 +180,18 @@ def test_valid_calls_without_a_device_fail_loudly(serve, fa):
 
 def test_binding_checks(serve):
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        serve.attention_packed(x, x, x, [4])  # not on a GPU
+    with pytest.raises(ValueError, match="CUDA"):
+        serve.attention_packed(x, x, x, [4])
     with pytest.raises(TypeError):
         serve.fa_fwd_packed(x.float(), x, x, x, torch.zeros(2, 4), [4])
     with pytest.raises(ValueError):
         serve.fa_fwd_packed(x, x, x[:3], x, torch.zeros(2, 4), [4])
+    for lens, error in (([5], ValueError), ([-1, 5], ValueError), ([2 ** 32 + 4], ValueError),
+                        ([2 ** 32 + 4, -2 ** 32], ValueError), ([2.5], TypeError), (torch.tensor([1.0]), TypeError)):
+        with pytest.raises(error):
+            serve.attention_packed(x, x, x, lens)
+    with pytest.raises(TypeError):
+        serve.fa_fwd_packed(x, x, x, None, None, [4])
     with pytest.raises(ValueError):
         serve.kv4_row_bytes(96)
     cache = torch.zeros((2, 2, 16 * 72), dtype=torch.uint8)
