@@ -60,7 +60,7 @@ template <int D, bool CAUSAL>
 int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const pk::Params& p, int grid, int dev,
            cudaStream_t stream) {
   auto kernel = pk::fa_packed_kernel<D, CAUSAL>;
-  constexpr int smem = fa::Cfg<D>::kSmemBytes;
+  constexpr int smem = pk::PackedCfg<D>::kSmemBytes;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     bool& set = g_attr[dev][D == 128][CAUSAL];

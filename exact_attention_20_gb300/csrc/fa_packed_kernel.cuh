@@ -39,6 +39,34 @@ constexpr int kMaxParts = 8;          // parts of one split item
 constexpr int kCountersPerItem = 8;   // per query tile and warp quadrant
 constexpr int kSitePacked = 6;        // status code: a wait gave up
 
+// Shared memory: Q tiles, the K/V ring, and (d = 128) 4 KB a softmax warp to
+// bring output rows into whole 128-byte lines.  At d = 128 that takes the place of
+// the dense forward's fifth ring stage, which costs prompts of any length
+// less than 1 %, while lane-by-lane rows (32 lines touched by each store) held
+// an item up by 1.0 us of its 1.9 us per step plus 3 us.
+template <int D>
+struct PackedCfg {
+  static constexpr int kSlabs = Cfg<D>::kSlabs, kTileBytes = Cfg<D>::kTileBytes;
+  static constexpr int kQkInstr = Cfg<D>::kQkInstr, kPvInstr = Cfg<D>::kPvInstr;
+  static constexpr int kStages = D == 128 ? 4 : 9;
+  static constexpr int kQOff = 0;
+  static constexpr int kKVOff = kQTiles * kTileBytes;
+  static constexpr int kOutOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kWarpOut = 32 * 128;
+  static constexpr int kBarOff = kOutOff + (D == 128 ? 8 * kWarpOut : 0);
+  static constexpr int kNumBars = 2 * 2 + 2 * kStages + 2 * 4 + 1 + 2;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kCursorOff = kMiscOff + 16;         // [softmax warp] where it is
+  static constexpr int kSmemBytes = kCursorOff + 8 * 32 + 1024;  // + alignment slack
+  static_assert(kSmemBytes <= 232448, "227 KB");
+};
+
+// The kernel's shared memory, from the first 1024-byte boundary on.
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ uint8_t smem_raw[];
+  return smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+}
+
 // One part of a split item: its workspace slot, the item's first slot and
 // number of parts (consecutive slots), and the item's counters.  slot < 0:
 // the chunk is the whole item.
@@ -94,6 +122,7 @@ struct Cursor {
     begin = p.cu[s];
     len = p.cu[s + 1] - begin;
   }
+  Cursor() = default;
   __device__ __forceinline__ Cursor(const Range& r, const Params& p) : s(r.s), h(r.h), b(r.b) { at(p); }
   __device__ __forceinline__ void next(const Params& p) {
     if (++b * 2 * p.tpt < len) return;
@@ -107,10 +136,10 @@ struct Cursor {
   }
 };
 
-// Key tiles [kb, ke) of one item, and the part it is.
+// Key tiles [kb, ke) of one item with `steps`; all of them, or a part.
 struct Chunk {
   int kb, ke, steps;
-  Part part;
+  __device__ __forceinline__ bool whole() const { return kb == 0 && ke == steps; }
 };
 
 template <bool CAUSAL>
@@ -119,8 +148,6 @@ __device__ __forceinline__ Chunk chunk_of(int i, const Cursor& c, const Range& r
   ch.steps = item_steps<CAUSAL>(c.b, c.len, p.tpt);
   ch.kb = i == 0 ? r.step_begin : 0;
   ch.ke = i == r.n_items - 1 ? r.step_end : ch.steps;
-  ch.part = i == 0 ? r.first : r.last;
-  if (ch.kb == 0 && ch.ke == ch.steps) ch.part.slot = -1;
   return ch;
 }
 
@@ -147,7 +174,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 template <int D, bool CAUSAL>
 __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                              uint32_t sbase, const Sync& sy, const Params& p) {
-  using C = Cfg<D>;
+  using C = PackedCfg<D>;
   uint32_t q_loads[2] = {0, 0};
   uint32_t kv_count = 0;
   const uint64_t pol_q = l2_policy_evict_first();
@@ -202,7 +229,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
 template <int D, bool CAUSAL>
 __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, uint32_t tmem, const Sync& sy,
                                         const Params& p) {
-  using C = Cfg<D>;
+  using C = PackedCfg<D>;
   const uint32_t bar_q_full = t ? sy.q_full[1] : sy.q_full[0];
   const uint32_t bar_q_empty = t ? sy.q_empty[1] : sy.q_empty[0];
   const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
@@ -341,77 +368,108 @@ __device__ __forceinline__ size_t part_index(int slot, int row, int group) {
   return static_cast<size_t>(slot) * kItemRows * D + (static_cast<size_t>(group) * kItemRows + row) * 8;
 }
 
-// A warp's 32 rows of a part are in the workspace: counts the arrival, and
-// where it completes the item's parts merges them through their logsumexps
-// (L = ln sum_r exp(L_r), O = sum_r exp(L_r - L) O_r, the largest L_r
-// subtracted first; a part without keys for a row has L_r = -inf and weighs
-// 0).  Parts are added in key order whatever the order of arrival, so results
-// do not depend on timing.
+// What this warp has of a split item: its state as the end of a chunk left it.
+constexpr int kStored = 0;  // in the workspace, like the others
+constexpr int kInTmem = 1;  // in tensor memory
+constexpr int kEmpty = 2;   // no key tile: nothing anywhere
+struct Own {
+  int where;    // the same in every lane
+  float lse;    // natural-log logsumexp of the part, -inf without keys
+  float inv_l;  // the accumulator's factor
+  uint32_t tO;  // the accumulator
+};
+
+// Merges one warp's 32 rows of a split item through the parts' logsumexps:
+// L = ln sum_r exp(L_r), O = sum_r exp(L_r - L) O_r, the largest L_r
+// subtracted first; a part without keys for a row has L_r = -inf and weighs 0.
+// Every other part's rows are in the workspace.  Parts are added in key
+// order, so the result does not depend on who merges.
 template <int D>
-__device__ __forceinline__ void arrive_and_merge(const Part& part, int t, int quad, int lane, bool store,
-                                                 __nv_bfloat16* orow, float* lse_dst, const Params& p) {
-  int* ctr = p.counters + part.k * kCountersPerItem + t * 4 + quad;
-  __threadfence();
-  __syncwarp();
-  int old = 0;
-  if (lane == 0) old = atomicAdd(ctr, 1);
-  if (__shfl_sync(0xffffffffu, old, 0) != part.count - 1) return;
-  (void)ld_acquire_gpu(ctr);  // every lane: the other parts' rows were fenced before their arrivals
-  const int r = t * kBlockM + quad * 32 + lane;
+__device__ __forceinline__ void merge_rows(const Part part, const Own own, int r, bool store, __nv_bfloat16* orow,
+                                        float* lse_dst, const float* part_o, const float* part_lse) {
   constexpr float kLog2e = 1.4426950408889634f;
+  const int mine = own.where == kStored ? -1 : part.slot - part.slot0;
+  const float* lse_in = part_lse + static_cast<size_t>(part.slot0) * kItemRows + r;
+  auto lse_of = [&](int i) { return i == mine ? own.lse : __ldcg(lse_in + i * kItemRows); };
+  // -inf: no key (m may be -inf too); a row whose scores are NaN stays NaN
+  auto weight = [&](float l, float m) { return l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e); };
   float m = -INFINITY;
-  for (int i = 0; i < part.count; ++i) m = fmaxf(m, __ldcg(p.part_lse + static_cast<size_t>(part.slot0 + i) * kItemRows + r));
-  float w[kMaxParts];
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxParts; ++i) {
-    w[i] = 0.f;
-    if (i < part.count) {
-      const float l = __ldcg(p.part_lse + static_cast<size_t>(part.slot0 + i) * kItemRows + r);
-      w[i] = l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e);
-      if (l != l) w[i] = l;  // a row whose scores are NaN stays NaN
-      sum += w[i];
-    }
-  }
-  const float inv = 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < kMaxParts; ++i) w[i] *= inv;
 #pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
-    float acc[16];
+  for (int i = 0; i < part.count; ++i) m = fmaxf(m, lse_of(i));
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < part.count; ++i) sum += weight(lse_of(i), m);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float acc[32];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < part.count; ++i) {
+      if (i == mine && own.where == kEmpty) continue;
+      const float w = weight(lse_of(i), m) * inv;
+      float x[32];
+      if (i == mine) {
+        uint32_t o[32];
+        tmem_ld32_wait(own.tO + c * 32, o);
 #pragma unroll
-    for (int i = 0; i < kMaxParts; ++i) {
-      if (i < part.count && w[i] != 0.f) {  // a part without keys was never written
-        float x[16];
-        ld_global_cg_v8(p.part_o + part_index<D>(part.slot0 + i, r, 2 * c), x);
-        ld_global_cg_v8(p.part_o + part_index<D>(part.slot0 + i, r, 2 * c + 1), x + 8);
+        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * own.inv_l;
+      } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = fmaf(w[i], x[e], acc[e]);
+        for (int n = 0; n < 4; ++n) ld_global_cg_v8(part_o + part_index<D>(part.slot0 + i, r, 4 * c + n), x + 8 * n);
+      }
+      if (w != 0.f) {  // an empty part's rows were never written
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = fmaf(w, x[e], acc[e]);
       }
     }
     if (store) {
-      uint4* dst = reinterpret_cast<uint4*>(orow + c * 16);
-      dst[0] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                          pack_bf16x2(acc[6], acc[7]));
-      dst[1] = make_uint4(pack_bf16x2(acc[8], acc[9]), pack_bf16x2(acc[10], acc[11]), pack_bf16x2(acc[12], acc[13]),
-                          pack_bf16x2(acc[14], acc[15]));
+      uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        dst[n] = make_uint4(pack_bf16x2(acc[8 * n], acc[8 * n + 1]), pack_bf16x2(acc[8 * n + 2], acc[8 * n + 3]),
+                            pack_bf16x2(acc[8 * n + 4], acc[8 * n + 5]), pack_bf16x2(acc[8 * n + 6], acc[8 * n + 7]));
     }
   }
   if (store) *lse_dst = m + logf(sum);
 }
+
+// The warp's arrival for a part whose rows are in the workspace: true for the
+// warp that completes the item, which then merges it.
+__device__ __forceinline__ bool part_arrive(int* ctr, int count, int lane) {
+  __threadfence();
+  __syncwarp();
+  int old = 0;
+  if (lane == 0) old = atomicAdd(ctr, 1);
+  if (__shfl_sync(0xffffffffu, old, 0) != count - 1) return false;
+  (void)ld_acquire_gpu(ctr);  // every lane: the other parts' rows were fenced before their arrivals
+  return true;
+}
+
+// A row's place in O and LSE; rows without a query (past the sequence's end,
+// or past the G * tpt rows of a tile) are not stored.
+struct Row {
+  bool store;
+  __nv_bfloat16* o;
+  float* lse;
+  __device__ __forceinline__ Row(int begin, int len, int h, int t0, int row_in_tile, int D, const Params& p) {
+    const int in_tile = row_in_tile / p.G, token = t0 + in_tile, head = h * p.G + row_in_tile - in_tile * p.G;
+    store = in_tile < p.tpt && token < len;
+    o = store ? p.o + (static_cast<size_t>(begin + token) * p.Hq + head) * D : p.o;
+    lse = store ? p.lse + static_cast<size_t>(head) * p.T + begin + token : p.lse;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Softmax / correction / epilogue warpgroup (128 threads, one row each)
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL>
 __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy, const Params& p) {
+  using C = PackedCfg<D>;
   const int lane = threadIdx.x & 31;
   const int quad = (threadIdx.x >> 5) & 3;  // TMEM lanes 32*quad .. 32*quad+31
   const int row_in_tile = quad * 32 + lane;
-  const int row_token = row_in_tile / p.G;  // the row's token within the tile
-  const int row_head = row_in_tile - row_token * p.G;
   const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t tS = tmem + lane_off + t * 128;
   const uint32_t tO = tmem + lane_off + 256 + t * 128;
@@ -422,36 +480,49 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
   const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
   uint32_t s_par = 0, od_par = 0;
   bool ok = true;
-
+  // Where the warp is, in shared memory: 128 scores of a row and what the loop
+  // over key tiles needs beside them fill the registers.
+  struct Place {
+    Cursor c;
+    Chunk ch;
+  };
+  static_assert(sizeof(Place) <= 32, "its slot");
+  Place* place = reinterpret_cast<Place*>(shared_base() + C::kCursorOff) + (threadIdx.x >> 5);
   const Range& r = p.range[blockIdx.x];
-  Cursor c(r, p);
   for (int i = 0; i < r.n_items && ok; ++i) {
-    if (i > 0) c.next(p);
-    const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
-    const int t0 = (2 * c.b + t) * p.tpt;  // the tile's first token within the sequence
-    const int ne = min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
-    const int token = t0 + row_token;
-    // rows without a query: past the sequence's end, or past the G * tpt rows of the tile
-    const bool store = row_token < p.tpt && token < c.len;
-    const int head = c.h * p.G + row_head;
-    __nv_bfloat16* orow =
-        store ? p.o + (static_cast<size_t>(c.begin + token) * p.Hq + head) * D : p.o;
-    float* lse_dst = store ? p.lse + static_cast<size_t>(head) * p.T + c.begin + token : p.lse;
-    if (ne <= ch.kb) {
-      // no key tile of this query tile lies in the chunk; a part still reports its rows, as an empty part
-      if (ch.part.slot >= 0) {
-        p.part_lse[static_cast<size_t>(ch.part.slot) * kItemRows + t * kBlockM + row_in_tile] = -INFINITY;
-        arrive_and_merge<D>(ch.part, t, quad, lane, store, orow, lse_dst, p);
-      }
-      continue;
+    int t0, ne, kb;
+    bool empty;
+    int seen, first_masked;
+    {
+      Cursor c = i == 0 ? Cursor(r, p) : place->c;
+      if (i > 0) c.next(p);
+      const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
+      __syncwarp();
+      if (lane == 0) *place = Place{c, ch};
+      __syncwarp();
+      t0 = (2 * c.b + t) * p.tpt;  // the tile's first token within the sequence
+      kb = ch.kb;
+      ne = min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
+      // a part may have no key tile of this query tile; it still reports its rows, as an empty part
+      empty = ne <= kb;
+      seen = CAUSAL ? min(t0 + row_in_tile / p.G, c.len - 1) : c.len - 1;             // the row's last visible key
+      first_masked = (CAUSAL ? min(t0, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
+      if (!CAUSAL && (c.len & (kBlockN - 1)) == 0) first_masked = ne;
     }
-    const int seen = CAUSAL ? min(token, c.len - 1) : c.len - 1;  // the row's last visible key
-    const int first_masked = (CAUSAL ? min(t0, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
+    if (i == 1 && r.first.slot >= 0) {
+      // The range's first chunk was a part and has stored its rows; its arrival
+      // is made here, while this chunk's first scores are on their way.
+      if (part_arrive(p.counters + r.first.k * kCountersPerItem + t * 4 + quad, r.first.count, lane)) {
+        const Row row(p.cu[r.s], p.cu[r.s + 1] - p.cu[r.s], r.h, (2 * r.b + t) * p.tpt, row_in_tile, D, p);
+        merge_rows<D>(r.first, Own{kStored, 0.f, 0.f, 0u}, t * kBlockM + row_in_tile, row.store, row.o, row.lse,
+                      p.part_o, p.part_lse);
+      }
+    }
     float m_ref = -INFINITY;  // reference maximum, in log2 units; moves on a jump above kRescaleThreshold
     float l = 0.f;            // running sum of exp2(s*qk - m_ref), for the logsumexp
     float lq = 0.f;           // the same terms rounded to bf16 (what P.V multiplies), for O
 
-    for (int j = ch.kb; j < ne; ++j) {
+    for (int j = kb; j < ne; ++j) {
       ok = wait_phase(bar_s_full, s_par, sy, p);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -460,7 +531,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
 
       uint32_t s[128];
       tmem_ld128_wait(tS, s);
-      if (CAUSAL ? j >= first_masked : (j == first_masked && (c.len & (kBlockN - 1)) != 0)) {
+      if (j >= first_masked) {
         const int lim = seen - j * kBlockN;
 #pragma unroll
         for (int e = 0; e < 128; ++e)
@@ -545,7 +616,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       l = l * alpha + (sa + sb);
       lq = lq * alpha + lq_tile;
 
-      if (j > ch.kb && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if (j > kb && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O_t holds the sum up to tile j-1: bring it to the new reference
         const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll
@@ -570,54 +641,105 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
     }
     if (!ok) break;
 
-    ok = wait_phase(bar_o_done, od_par, sy, p);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    od_par ^= 1u;
-    tc_fence_after_sync();
-    // a part may hold no visible key of a row (l = 0): its O is 0 and its logsumexp -inf
-    const float inv_l = l == 0.f ? 0.f : 1.f / lq;
-    const uint64_t il2 = f2_pack(inv_l, inv_l);
-    const float lse_row = (m_ref + log2f(l)) * 0.69314718055994531f;
-    const int r_item = t * kBlockM + row_in_tile;
-    // rows of O are 32-byte aligned when O is; the API promises 16
-    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+    Own own{kEmpty, -INFINITY, 0.f, tO};
+    if (!empty) {
+      ok = wait_phase(bar_o_done, od_par, sy, p);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      od_par ^= 1u;
+      tc_fence_after_sync();
+      // a part may hold no visible key of a row (l = 0): its O is 0 and its logsumexp -inf
+      own = Own{kInTmem, (m_ref + log2f(l)) * 0.69314718055994531f, l == 0.f ? 0.f : 1.f / lq, tO};
+    }
+    const bool whole = place->ch.whole();
+    if (whole && empty) continue;
+    const Cursor c = place->c;
+    const Row row(c.begin, c.len, c.h, (2 * c.b + t) * p.tpt, row_in_tile, D, p);
+    if (!whole) {
+      const Part part = i == 0 ? r.first : r.last;
+      const int r_item = t * kBlockM + row_in_tile;  // row within the item, and its slot
+      // The end of a chunk that is a part: where every other part is in already
+      // (as a rule for the range's last chunk, whose item's other parts were
+      // other CTAs' first work), the warp merges from where its rows are;
+      // else it stores them and arrives.
+      int* ctr = p.counters + part.k * kCountersPerItem + t * 4 + quad;
+      bool merge = (i > 0 || r.n_items == 1) && __all_sync(0xffffffffu, ld_acquire_gpu(ctr) == part.count - 1);
+      if (!merge) {
+        if (own.where == kInTmem) {
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      uint32_t o[32];
-      tmem_ld32_wait(tO + e * 32, o);
+          for (int e = 0; e < D / 32; ++e) {
+            uint32_t o[32];
+            tmem_ld32_wait(tO + e * 32, o);
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        float lo, hi;
-        f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1])), il2), lo, hi);
-        o[2 * n] = __float_as_uint(lo);
-        o[2 * n + 1] = __float_as_uint(hi);
+            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * own.inv_l);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) st_global_v8(p.part_o + part_index<D>(part.slot, r_item, e * 4 + n), o + n * 8);
+          }
+        }
+        p.part_lse[static_cast<size_t>(part.slot) * kItemRows + r_item] = own.lse;
+        own.where = kStored;
+        if (i > 0 || r.n_items == 1) merge = part_arrive(ctr, part.count, lane);  // else: with the next chunk
       }
-      if (ch.part.slot >= 0) {
+      if (merge) merge_rows<D>(part, own, r_item, row.store, row.o, row.lse, p.part_o, p.part_lse);
+    } else {
+      const uint64_t il2 = f2_pack(own.inv_l, own.inv_l);
+      auto to_bf16 = [&](const uint32_t* o) {  // two elements of the row
+        float lo, hi;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(o[0]), __uint_as_float(o[1])), il2), lo, hi);
+        return pack_bf16x2(lo, hi);
+      };
+      if constexpr (D == 128) {
+        // The warp's 32 rows, 64 columns at a time: each lane writes its row's
+        // 128 bytes to shared memory (16-byte pieces swizzled by row), then
+        // eight lanes store a row's line, four rows an instruction.
+        uint8_t* out = shared_base() + C::kOutOff + (threadIdx.x >> 5) * C::kWarpOut;
+        const uint32_t stores = __ballot_sync(0xffffffffu, row.store);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) st_global_v8(p.part_o + part_index<D>(ch.part.slot, r_item, e * 4 + n), o + n * 8);
-      } else if (store) {
-        uint32_t w[16];
+        for (int e = 0; e < D / 64; ++e) {
 #pragma unroll
-        for (int n = 0; n < 16; ++n) w[n] = pack_bf16x2(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1]));
-        if (wide) {
-          st_global_v8(orow + e * 32, w);
-          st_global_v8(orow + e * 32 + 16, w + 8);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(orow + e * 32);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            tmem_ld32_wait(tO + e * 64 + h * 32, o);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) dst[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+            for (int n = 0; n < 4; ++n)
+              *reinterpret_cast<uint4*>(out + lane * 128 + (((h * 4 + n) ^ (lane & 7)) * 16)) =
+                  make_uint4(to_bf16(o + 8 * n), to_bf16(o + 8 * n + 2), to_bf16(o + 8 * n + 4), to_bf16(o + 8 * n + 6));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int from = (lane >> 3) + 4 * x, piece = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(out + from * 128 + ((piece ^ (from & 7)) * 16));
+            const unsigned long long dst = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row.o), from);
+            if ((stores >> from) & 1u) *reinterpret_cast<uint4*>(dst + (e * 64 + piece * 8) * 2) = v;
+          }
+          __syncwarp();
+        }
+      } else {
+        // 128-byte rows: each lane its own, which measured faster here
+        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;  // the API promises 16
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          uint32_t o[32], w[16];
+          tmem_ld32_wait(tO + e * 32, o);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) w[n] = to_bf16(o + 2 * n);
+          if (row.store && wide) {
+            st_global_v8(row.o + e * 32, w);
+            st_global_v8(row.o + e * 32 + 16, w + 8);
+          } else if (row.store) {
+            uint4* dst = reinterpret_cast<uint4*>(row.o + e * 32);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) dst[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+          }
         }
       }
+      if (row.store) *row.lse = own.lse;
     }
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_o_free);  // one arrival per warp
-    if (ch.part.slot < 0) {
-      if (store) *lse_dst = lse_row;
-    } else {
-      p.part_lse[static_cast<size_t>(ch.part.slot) * kItemRows + r_item] = lse_row;
-      arrive_and_merge<D>(ch.part, t, quad, lane, store, orow, lse_dst, p);
+    if (!empty) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_o_free);  // one arrival per warp
     }
   }
 }
@@ -629,10 +751,8 @@ template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kNumThreads, 1)
 fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
-  using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  using C = PackedCfg<D>;
+  uint8_t* smem = shared_base();
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

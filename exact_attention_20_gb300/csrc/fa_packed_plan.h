@@ -12,7 +12,7 @@ namespace packed {
 constexpr int kItemCost = 2;
 // An item is cut only where both sides keep this many steps: a part costs a
 // write and a read of 256 rows in fp32 besides.
-constexpr int kMinPartSteps = 4;
+constexpr int kMinPartSteps = 8;
 // With no more items than CTAs, items are cut only while every CTA keeps this
 // many steps.
 constexpr int kMinStepsPerCta = 16;
