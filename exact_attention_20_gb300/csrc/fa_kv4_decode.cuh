@@ -45,6 +45,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 2 * kGroup;       // tokens a warp takes at a time
 constexpr int kMinUnits = 2 * kWarps;   // units a CTA takes at least, where there are that many
+// Ranges are equal in cost: an item costs its units and this many more (Q, the
+// page ids, the state's start and end: 1.5 us, as long as a unit takes a warp).
+constexpr int kItemUnits = 1;
 constexpr float kLift = 8.f;            // log2 of P at a maximum
 constexpr float kMove = 7.f;            // the reference moves on a jump above this many log2 units
 constexpr float kNone = -3.0e38f;       // reference of a row without keys yet
@@ -110,6 +113,7 @@ __device__ __forceinline__ int tokens_of(int s, const DecodeParams& p) {
 }
 __device__ __forceinline__ int data_units(int len) { return (len + kUnit - 1) / kUnit; }
 __device__ __forceinline__ int units_of(int len) { return max(1, data_units(len)); }
+__device__ __forceinline__ int cost_of(int len) { return units_of(len) + kItemUnits; }
 
 // Exclusive scan of one value per thread over the block, and the total.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, long long& total) {
@@ -132,7 +136,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, 
   return before + x - v;
 }
 
-// The sequences' units, counted for one item of each: this thread's sequences
+// The sequences' costs, counted for one item of each: this thread's sequences
 // [lo, hi) with their sum, the sum before them, and the total.
 struct Scan {
   long long mine, before, total;
@@ -142,7 +146,7 @@ struct Scan {
     lo = min(static_cast<int>(threadIdx.x) * per, p.n_seqs);
     hi = min(lo + per, p.n_seqs);
     mine = 0;
-    for (int s = lo; s < hi; ++s) mine += units_of(tokens_of(s, p));
+    for (int s = lo; s < hi; ++s) mine += cost_of(tokens_of(s, p));
     before = block_scan(mine, s_sums, total);
   }
 };
@@ -152,12 +156,17 @@ struct Scan {
 struct Walk {
   int s, item;     // sequence, item within it (head * row_tiles + row tile)
   int len, units;  // the sequence's
-  int u0, count;   // the segment's units: [u0, u0 + count)
-  int left;        // units from u0 to the end of the warp's range; 0: done
-  __device__ __forceinline__ void set() { count = min(units - u0, left); }
+  int u0, count;   // the segment's units: [u0, u0 + count); none where the range ends within the item's own cost
+  int take;        // the segment's cost
+  int left;        // cost from here to the end of the warp's range; 0: done
+  // from `at` of the item's cost on
+  __device__ __forceinline__ void set(int at) {
+    take = min(units + kItemUnits - at, left);
+    u0 = max(0, at - kItemUnits);
+    count = max(0, at + take - kItemUnits - u0);
+  }
   __device__ __forceinline__ void next(const DecodeParams& p) {
-    left -= count;
-    u0 = 0;
+    left -= take;
     if (left <= 0) return;
     if (++item == p.Hkv * p.row_tiles) {
       item = 0;
@@ -165,7 +174,7 @@ struct Walk {
       len = tokens_of(s, p);
       units = units_of(len);
     }
-    set();
+    set(0);
   }
   __device__ __forceinline__ int end() const { return min(u0 + count, data_units(len)); }  // of the units that hold tokens
 };
@@ -584,10 +593,84 @@ __device__ __forceinline__ void write_row(const RowPlace& rp, int D, int d4, flo
     p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
+// Where a CTA's range starts: a sequence, and the cost of its items before it.
+struct From {
+  int s;
+  long long at;
+};
+
 // A warp's shared items: its range's first (where that is not its last too) and last.
 struct Shared {
   int s, item, u0, count, units;  // the item's units [u0, u0 + count) of `units`; count = 0: none
 };
+
+// The combination of a CTA's shared items: M = max m_e, O = sum O_e 2^(m_e - M),
+// l likewise (a state without keys has m = kNone, l = 0 and O = 0), for the
+// item of entries list[0 .. n): rows row0, row0 + kSide, ... (kSteps of them),
+// elements d4 .. d4+3.  Of the entries only the last may be a warp's first
+// item, in the workspace: its loads go out for all rows before the others are
+// added up.
+template <int D, int NT, int kSteps>
+__device__ __forceinline__ void combine(const int* list, int n, int row0, int d4, const uint8_t* smem,
+                                        const Shared (*shared)[2], const DecodeParams& p) {
+  using C = DecodeCfg<D, NT>;
+  constexpr int kRows = C::kRows, kSide = 32 / (D / 4);
+  const float2* s_ml = reinterpret_cast<const float2*>(smem + C::kMlAt);
+  const int last = list[n - 1];
+  const bool stored = (last & 1) == 0;  // the last entry is in the workspace
+  const int in_smem = stored ? n - 1 : n;
+  float4 o[kSteps];
+  float M[kSteps], L[kSteps];
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    M[i] = kNone;
+    L[i] = 0.f;
+    o[i] = stored ? *reinterpret_cast<const float4*>(
+                        p.first_o + ((static_cast<long long>(blockIdx.x) * kWarps + (last >> 1)) * kRows + row0 + i * kSide) * D + d4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int x = 0; x < n; ++x) {
+    const int e = list[x];
+    count += shared[e >> 1][e & 1].count;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) M[i] = fmaxf(M[i], s_ml[e * kRows + row0 + i * kSide].x);
+  }
+  if (stored) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float2 ml = s_ml[last * kRows + row0 + i * kSide];
+      const float f = ex2_approx(ml.x - M[i]);
+      L[i] = ml.y * f;
+      o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+    }
+  }
+  for (int x = 0; x < in_smem; ++x) {
+    const int e = list[x];
+    const float* from = reinterpret_cast<const float*>(smem + (e >> 1) * C::kWarpRing);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float2 ml = s_ml[e * kRows + row0 + i * kSide];
+      const float f = ex2_approx(ml.x - M[i]);
+      const float4 a = *reinterpret_cast<const float4*>(from + (row0 + i * kSide) * (D + C::kPad) + d4);
+      L[i] = fmaf(ml.y, f, L[i]);
+      o[i] = make_float4(fmaf(a.x, f, o[i].x), fmaf(a.y, f, o[i].y), fmaf(a.z, f, o[i].z), fmaf(a.w, f, o[i].w));
+    }
+  }
+  const Shared x = shared[list[0] >> 1][list[0] & 1];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = row0 + i * kSide;
+    if (count == x.units) {
+      const RowPlace rp = row_place(x.s, x.item, r, kRows, p);
+      if (rp.store) write_row(rp, D, d4, o[i], M[i], L[i], p);
+    } else {
+      const long long row = (2ll * blockIdx.x + (x.u0 > 0 ? 0 : 1)) * kRows + r;
+      *reinterpret_cast<float4*>(p.part_o + row * D + d4) = o[i];
+      if (d4 == 0) p.part_ml[row] = make_float2(M[i], L[i]);
+    }
+  }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode_kernel(const DecodeParams p) {
@@ -595,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
   constexpr int kRows = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_sums[kWarps];
-  __shared__ Walk s_walk[kWarps];
+  __shared__ From s_from;
   __shared__ LoadCursor s_load[kWarps];
   __shared__ Shared s_shared[kWarps][2];
   __shared__ int s_entry[2 * kWarps], s_group[2 * kWarps + 1], s_groups;
@@ -606,12 +689,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
   if (lane == 0) {
     for (int st = 0; st < C::kStages; ++st) mbar_init(bar0 + 8 * st, 1);
     fence_barrier_init();
-    s_walk[warp].left = 0;
     s_shared[warp][0].count = s_shared[warp][1].count = 0;
   }
 
-  // This CTA's range of the concatenated items' units, and its warps'.
+  // This CTA's range of the concatenated items' cost, and from it this warp's.
   const int items = p.Hkv * p.row_tiles;  // of a sequence
+  Walk w;
+  w.left = 0;
   if (p.split) {
     if (threadIdx.x == 0) p.cuts[blockIdx.x].s = -1;
     const Scan sc(p, s_sums);  // a barrier, too
@@ -621,40 +705,51 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
     const long long begin = c < ctas ? all * c / ctas : all;
     const int n = c < ctas ? static_cast<int>(min(all * (c + 1) / ctas - begin, 0x7fffffffll)) : 0;
     const long long lo = sc.before * items, hi = (sc.before + sc.mine) * items;
-    if (begin < hi && begin + n > lo) {  // this thread's sequences hold some of it
+    if (begin >= lo && begin < hi) {  // this thread's sequences hold the range's start
       long long at = lo;
-      int x = 0;  // the next warp's range to be found
-      for (int s = sc.lo; s < sc.hi; ++s) {
-        const int len = tokens_of(s, p), units = units_of(len);
-        const long long after = at + static_cast<long long>(units) * items;
-        for (; x < kWarps; ++x) {
-          const int from = static_cast<int>(static_cast<long long>(n) * x / kWarps);
-          const int left = static_cast<int>(static_cast<long long>(n) * (x + 1) / kWarps) - from;
-          const long long b = begin + from;  // the range's first unit
-          if (b >= after) break;
-          if (b < at || left == 0) continue;
-          const int item = static_cast<int>((b - at) / units);
-          const long long a = at + static_cast<long long>(item) * units;  // the item's first unit
-          Walk w{s, item, len, units, static_cast<int>(b - a), 0, left};
-          w.set();
-          s_walk[x] = w;
-          if (b == begin && b > a && all * (c - 1) / ctas <= a) {  // the item's first cut by a CTA's range
-            long long c1 = c;
-            while (all * (c1 + 1) / ctas < a + units) ++c1;
-            p.cuts[c] = Cut{s, item, static_cast<int>(c - 1), static_cast<int>(c1)};
-          }
-        }
+      int s = sc.lo;
+      for (;; ++s) {
+        const long long after = at + static_cast<long long>(cost_of(tokens_of(s, p))) * items;
+        if (begin < after) break;
         at = after;
       }
+      s_from = From{s, begin - at};
     }
-  } else if (lane == 0) {
+    __syncthreads();
+    // this warp's share, from that sequence on
+    const int from = static_cast<int>(static_cast<long long>(n) * warp / kWarps);
+    w.left = static_cast<int>(static_cast<long long>(n) * (warp + 1) / kWarps) - from;
+    if (w.left > 0) {
+      w.s = s_from.s;
+      long long at = s_from.at + from;  // counted from the sequence's start
+      int cost;
+      for (;; ++w.s) {
+        w.len = tokens_of(w.s, p);
+        w.units = units_of(w.len);
+        cost = w.units + kItemUnits;
+        if (at < static_cast<long long>(cost) * items) break;
+        at -= static_cast<long long>(cost) * items;
+      }
+      w.item = at < 0x7fffffffll ? static_cast<int>(at) / cost : static_cast<int>(at / cost);
+      const int in_item = static_cast<int>(at - static_cast<long long>(w.item) * cost);
+      w.set(in_item);
+      if (warp == 0 && lane == 0 && w.u0 > 0) {
+        // the range starts within an item: is this the item's first cut?
+        const long long a = begin - in_item;  // its start
+        if (all * (c - 1) / ctas <= a + kItemUnits)
+          p.cuts[c] = Cut{w.s, w.item, static_cast<int>(c - 1), static_cast<int>(((a + cost) * ctas + all - 1) / all - 1)};
+      }
+    }
+  } else {
     // short items: CTA i takes item i whole
-    const int s = blockIdx.x / items, len = tokens_of(s, p), units = units_of(len);
-    const int from = units * warp / kWarps, left = units * (warp + 1) / kWarps - from;
-    s_walk[warp] = Walk{s, static_cast<int>(blockIdx.x) - s * items, len, units, from, left, left};
+    w.s = blockIdx.x / items;
+    w.item = static_cast<int>(blockIdx.x) - w.s * items;
+    w.len = tokens_of(w.s, p);
+    w.units = units_of(w.len);
+    const int from = w.units * warp / kWarps;
+    w.left = w.units * (warp + 1) / kWarps - from;
+    w.set(from + kItemUnits);
   }
-  __syncthreads();
-  Walk w = s_walk[warp];
   if (p.errors && blockIdx.x == 0) {
     for (int s = threadIdx.x; s < p.n_seqs; s += kThreads)
       if (p.seq_lens[s] != tokens_of(s, p)) atomicOr(p.errors, kErrPosition);
@@ -739,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
   bool dead = false;            // a wait gave up
   State<D, NT> state;
 #pragma unroll 1
-  for (bool first = true; w.left > 0; w.next(p), first = false) {
+  for (; w.left > 0; w.next(p)) {
+    if (w.count == 0) continue;  // the range ends with an item's own cost
     state.reset();
     state.load_q(w, p, reinterpret_cast<uint2*>(smem + C::kQAt + warp * C::kQBytes));
     const int end = w.end();
@@ -764,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
     }
     // a shared item: the range's last goes where the ring was (nothing is on
     // its way there any more), its first to the workspace
-    const int which = w.count == w.left ? 1 : 0;
+    const int which = w.take == w.left ? 1 : 0;
     if (lane == 0) s_shared[warp][which] = Shared{w.s, w.item, w.u0, w.count, w.units};
     if (which == 1 && !dead)
       state.save(reinterpret_cast<float*>(ring), D + C::kPad, s_ml + (warp * 2 + 1) * kRows);
@@ -793,39 +889,20 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
     }
   }
   __syncthreads();
-  // M = max m_e, O = sum O_e 2^(m_e - M), l likewise (a state without keys has
-  // m = kNone, l = 0 and O = 0).
-  const int total = s_groups * kRows * (D / 4);
+  // Eight rows of an item to a warp, or a warp's lanes' worth where there are few items.
+  constexpr int kLanes = D / 4, kSide = 32 / kLanes, kSteps = 8 / kSide;  // lanes of a row, rows side by side
+  const int r0 = lane / kLanes, d4 = lane % kLanes * 4;
+  if (s_groups * NT >= kWarps) {
 #pragma unroll 1
-  for (int idx = threadIdx.x; idx < total; idx += kThreads) {
-    const int group = idx / (kRows * (D / 4)), r = idx / (D / 4) % kRows, d4 = idx % (D / 4) * 4;
-    const int e0 = s_group[group], e1 = s_group[group + 1];
-    float M = kNone;
-    int count = 0;
-    for (int i = e0; i < e1; ++i) {
-      M = fmaxf(M, s_ml[s_entry[i] * kRows + r].x);
-      count += s_shared[s_entry[i] >> 1][s_entry[i] & 1].count;
+    for (int idx = warp; idx < s_groups * NT; idx += kWarps) {
+      const int group = idx / NT, first = s_group[group];
+      combine<D, NT, kSteps>(s_entry + first, s_group[group + 1] - first, idx % NT * 8 + r0, d4, smem, s_shared, p);
     }
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    for (int i = e0; i < e1; ++i) {
-      const int e = s_entry[i];
-      const float2 ml = s_ml[e * kRows + r];
-      const float f = ex2_approx(ml.x - M);
-      const float4 a = e & 1 ? *reinterpret_cast<const float4*>(smem + (e >> 1) * C::kWarpRing + (r * (D + C::kPad) + d4) * 4)
-                             : *reinterpret_cast<const float4*>(
-                                   p.first_o + ((static_cast<long long>(blockIdx.x) * kWarps + (e >> 1)) * kRows + r) * D + d4);
-      L = fmaf(ml.y, f, L);
-      O = make_float4(fmaf(a.x, f, O.x), fmaf(a.y, f, O.y), fmaf(a.z, f, O.z), fmaf(a.w, f, O.w));
-    }
-    const Shared& x = s_shared[s_entry[e0] >> 1][s_entry[e0] & 1];
-    if (count == x.units) {
-      const RowPlace rp = row_place(x.s, x.item, r, kRows, p);
-      if (rp.store) write_row(rp, D, d4, O, M, L, p);
-    } else {
-      const long long row = (2ll * blockIdx.x + (x.u0 > 0 ? 0 : 1)) * kRows + r;
-      *reinterpret_cast<float4*>(p.part_o + row * D + d4) = O;
-      if (d4 == 0) p.part_ml[row] = make_float2(M, L);
+  } else {
+#pragma unroll 1
+    for (int idx = warp; idx < s_groups * NT * kSteps; idx += kWarps) {
+      const int group = idx / (NT * kSteps), first = s_group[group];
+      combine<D, NT, 1>(s_entry + first, s_group[group + 1] - first, idx % (NT * kSteps) * kSide + r0, d4, smem, s_shared, p);
     }
   }
 }
@@ -849,7 +926,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const DecodeParams p, i
   auto row_of = [&](int c) { return (2ll * c + (c == cut.c0 ? 1 : 0)) * rows + r; };
   float M = kNone, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 4;  // parts loaded together
+  constexpr int kAhead = 8;  // parts loaded together
   for (int c = cut.c0 + side; c <= cut.c1; c += kSide * kAhead) {
     float2 ml[kAhead];
     float4 o[kAhead];
