@@ -154,11 +154,10 @@ DecodePlan decode_plan(int n_seqs, int Lq, int G, int Hkv, int d, int max_pages,
     pl.grid = items;
     return pl;
   }
-  const long long resident = static_cast<long long>(num_sms) * (pl.nt * d > 256 ? 1 : 2);  // DecodeCfg::kCtasPerSm
-  pl.grid = std::min(resident, (items * std::min(units, 1ll << 26) + kv::kMinUnits - 1) / kv::kMinUnits);
+  pl.grid = std::min(static_cast<long long>(num_sms), (items * std::min(units, 1ll << 26) + kv::kMinUnits - 1) / kv::kMinUnits);
   // parts: two of a CTA and one of each warp (O), the CTAs' (m, l), and the cuts
   const size_t all_rows = static_cast<size_t>(pl.grid) * 8 * pl.nt;
-  pl.bytes = all_rows * (2 + kv::kWarps) * d * 4 + all_rows * 2 * 8 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
+  pl.bytes = all_rows * (2 + kv::kMaxWarps) * d * 4 + all_rows * 2 * 8 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
   return pl;
 }
 
@@ -175,13 +174,13 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
       set = true;
     }
   }
-  kernel<<<static_cast<int>(pl.grid), kv::kThreads, smem, stream>>>(p);
+  kernel<<<static_cast<int>(pl.grid), kv::DecodeCfg<D, NT>::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   if (!pl.split) return FA_OK;
   // the merge may be set up while the first kernel runs; its CTAs wait for it
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 8 * NT / kv::kMergeRows);
-  cfg.blockDim = dim3(kv::kThreads);
+  cfg.blockDim = dim3(kv::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -284,7 +283,7 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
   const long long rows = pl.grid * 8 * pl.nt;
   p.part_o = static_cast<float*>(workspace);
   p.first_o = p.part_o + 2 * rows * d;
-  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kWarps * rows * d);
+  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kMaxWarps * rows * d);
   p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * rows);
   p.errors = errors;
   p.status = view.status;

@@ -27,8 +27,8 @@
 //   P's rounding to f16 is 2^-11 relative; every sum is fp32.
 //
 // Work: the (sequence, KV head, row tile) items' units of 32 tokens,
-// concatenated, are cut into equal ranges, one per CTA, and a CTA's range into
-// eight, one per warp, from the lengths on the device.  A warp goes through
+// concatenated, are cut into ranges of equal cost, one per CTA, and a CTA's
+// range into one per warp, from the lengths on the device.  A warp goes through
 // its range alone, with a ring of its own (bulk copies, two units ahead of the
 // arithmetic and across items) and an online softmax per item: an item that
 // lies within the range it writes itself.  Only the range's first and last
@@ -41,13 +41,13 @@
 namespace fa {
 namespace kv4 {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kMaxWarps = 16;
 constexpr int kUnit = 2 * kGroup;       // tokens a warp takes at a time
-constexpr int kMinUnits = 2 * kWarps;   // units a CTA takes at least, where there are that many
+constexpr int kMinUnits = 16;           // units a CTA takes at least, where there are that many
 // Ranges are equal in cost: an item costs its units and this many more (Q, the
-// page ids, the state's start and end: 1.5 us, as long as a unit takes a warp).
-constexpr int kItemUnits = 1;
+// page ids, the state's start and end).  96 contexts of 320 to 16000 tokens
+// took 82.8, 81.0, 79.6 and 80.0 us with 1, 2, 3 and 4.
+constexpr int kItemUnits = 3;
 constexpr float kLift = 8.f;            // log2 of P at a maximum
 constexpr float kMove = 7.f;            // the reference moves on a jump above this many log2 units
 constexpr float kNone = -3.0e38f;       // reference of a row without keys yet
@@ -69,7 +69,7 @@ struct DecodeParams {
   float* lse;              // [Hq][n_seqs * Lq]
   float* part_o;           // workspace: [2 grid][rows][D], parts' O, not normalised
   float2* part_ml;         // workspace: [2 grid][rows], (m, l) in log2 units
-  float* first_o;          // workspace: [8 grid][rows][D], a warp's first item's O, not normalised
+  float* first_o;          // workspace: [warps][rows][D], a warp's first item's O, not normalised
   Cut* cuts;               // workspace: [grid]
   int* errors;             // or null
   int* status;
@@ -86,12 +86,14 @@ struct DecodeParams {
 template <int D, int NT>
 struct DecodeCfg {
   static constexpr int kRows = 8 * NT;
-  // O^T takes NT D / 4 registers of a lane.  Up to 64 of them, two CTAs (16
-  // warps) fit an SM's registers, with Q in shared memory where it would take
-  // 32 more; a CTA's ring then has three units a warp (216 KB an SM, two
-  // thirds of it in flight).
+  // One CTA an SM (two of eight warps, whose ends an SM's preference for its
+  // older warps draws 10 us apart, took 84 us where this takes 80).  O^T takes
+  // NT D / 4 registers of a lane: up to 64 of them leave room for 16 warps,
+  // with Q in shared memory where it would take 32 more; the ring has three
+  // units a warp then (216 KB, two thirds of it in flight).
   static constexpr bool kWide = NT * D > 256;
-  static constexpr int kCtasPerSm = kWide ? 1 : 2;
+  static constexpr int kWarps = kWide ? 8 : kMaxWarps;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr bool kSharedQ = NT * D >= 256;
   static constexpr int kStages = D == 64 ? (kSharedQ ? 4 : 5) : kWide ? 4 : kSharedQ ? 2 : 3;
   static constexpr int kPad = 8;  // floats, so that rows of a state start in other banks
@@ -129,7 +131,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, 
   long long before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kMaxWarps; ++w) {
+    if (w * 32 >= static_cast<int>(blockDim.x)) break;
     if (w < warp) before += s_sums[w];
     total += s_sums[w];
   }
@@ -142,7 +145,7 @@ struct Scan {
   long long mine, before, total;
   int lo, hi;
   __device__ __forceinline__ Scan(const DecodeParams& p, long long* s_sums) {
-    const int per = (p.n_seqs + kThreads - 1) / kThreads;
+    const int threads = static_cast<int>(blockDim.x), per = (p.n_seqs + threads - 1) / threads;
     lo = min(static_cast<int>(threadIdx.x) * per, p.n_seqs);
     hi = min(lo + per, p.n_seqs);
     mine = 0;
@@ -605,79 +608,70 @@ struct Shared {
 };
 
 // The combination of a CTA's shared items: M = max m_e, O = sum O_e 2^(m_e - M),
-// l likewise (a state without keys has m = kNone, l = 0 and O = 0), for the
-// item of entries list[0 .. n): rows row0, row0 + kSide, ... (kSteps of them),
-// elements d4 .. d4+3.  Of the entries only the last may be a warp's first
-// item, in the workspace: its loads go out for all rows before the others are
-// added up.
-template <int D, int NT, int kSteps>
-__device__ __forceinline__ void combine(const int* list, int n, int row0, int d4, const uint8_t* smem,
+// l likewise (a state without keys has m = kNone, l = 0 and O = 0).  A warp
+// takes 32 / (D / 4) rows of an item at a time, elements d4 .. d4+3 to a lane.
+// Of an item's entries only the last may be a warp's first item, in the
+// workspace; its load goes out a step ahead.  The loops are not unrolled: this
+// runs once a launch, from a cold instruction cache.
+template <int D, int NT>
+__device__ __forceinline__ void combine(const int* entries, const int* starts, int groups, const uint8_t* smem,
                                         const Shared (*shared)[2], const DecodeParams& p) {
   using C = DecodeCfg<D, NT>;
-  constexpr int kRows = C::kRows, kSide = 32 / (D / 4);
+  constexpr int kRows = C::kRows, kWarps = C::kWarps, kLanes = D / 4, kSide = 32 / kLanes, kSteps = kRows / kSide;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = lane / kLanes, d4 = lane % kLanes * 4;
   const float2* s_ml = reinterpret_cast<const float2*>(smem + C::kMlAt);
-  const int last = list[n - 1];
-  const bool stored = (last & 1) == 0;  // the last entry is in the workspace
-  const int in_smem = stored ? n - 1 : n;
-  float4 o[kSteps];
-  float M[kSteps], L[kSteps];
-  int count = 0;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    M[i] = kNone;
-    L[i] = 0.f;
-    o[i] = stored ? *reinterpret_cast<const float4*>(
-                        p.first_o + ((static_cast<long long>(blockIdx.x) * kWarps + (last >> 1)) * kRows + row0 + i * kSide) * D + d4)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int x = 0; x < n; ++x) {
-    const int e = list[x];
-    count += shared[e >> 1][e & 1].count;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) M[i] = fmaxf(M[i], s_ml[e * kRows + row0 + i * kSide].x);
-  }
-  if (stored) {
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const float2 ml = s_ml[last * kRows + row0 + i * kSide];
-      const float f = ex2_approx(ml.x - M[i]);
-      L[i] = ml.y * f;
-      o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+  const float* first_o = p.first_o + static_cast<long long>(blockIdx.x) * kWarps * kRows * D + d4;
+  auto fetch = [&](int idx) {  // the last entry's elements, where they are in the workspace
+    if (idx >= groups * kSteps) return make_float4(0.f, 0.f, 0.f, 0.f);
+    const int last = entries[starts[idx / kSteps + 1] - 1];
+    if (last & 1) return make_float4(0.f, 0.f, 0.f, 0.f);
+    return *reinterpret_cast<const float4*>(first_o + ((last >> 1) * kRows + idx % kSteps * kSide + r0) * D);
+  };
+  float4 ahead = fetch(warp);
+#pragma unroll 1
+  for (int idx = warp; idx < groups * kSteps; idx += kWarps) {
+    const int group = idx / kSteps, r = idx % kSteps * kSide + r0;
+    const int e0 = starts[group], e1 = starts[group + 1];
+    const float4 stored = ahead;
+    ahead = fetch(idx + kWarps);
+    float M = kNone, L = 0.f;
+    int count = 0;
+#pragma unroll 4
+    for (int x = e0; x < e1; ++x) {
+      const int e = entries[x];
+      count += shared[e >> 1][e & 1].count;
+      M = fmaxf(M, s_ml[e * kRows + r].x);
     }
-  }
-  for (int x = 0; x < in_smem; ++x) {
-    const int e = list[x];
-    const float* from = reinterpret_cast<const float*>(smem + (e >> 1) * C::kWarpRing);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const float2 ml = s_ml[e * kRows + row0 + i * kSide];
-      const float f = ex2_approx(ml.x - M[i]);
-      const float4 a = *reinterpret_cast<const float4*>(from + (row0 + i * kSide) * (D + C::kPad) + d4);
-      L[i] = fmaf(ml.y, f, L[i]);
-      o[i] = make_float4(fmaf(a.x, f, o[i].x), fmaf(a.y, f, o[i].y), fmaf(a.z, f, o[i].z), fmaf(a.w, f, o[i].w));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = e0; x < e1; ++x) {
+      const int e = entries[x];
+      const float2 ml = s_ml[e * kRows + r];
+      const float f = ex2_approx(ml.x - M);
+      const float4 a = e & 1 ? *reinterpret_cast<const float4*>(smem + (e >> 1) * C::kWarpRing + (r * (D + C::kPad) + d4) * 4)
+                             : stored;
+      L = fmaf(ml.y, f, L);
+      o = make_float4(fmaf(a.x, f, o.x), fmaf(a.y, f, o.y), fmaf(a.z, f, o.z), fmaf(a.w, f, o.w));
     }
-  }
-  const Shared x = shared[list[0] >> 1][list[0] & 1];
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = row0 + i * kSide;
+    const Shared& x = shared[entries[e0] >> 1][entries[e0] & 1];
     if (count == x.units) {
       const RowPlace rp = row_place(x.s, x.item, r, kRows, p);
-      if (rp.store) write_row(rp, D, d4, o[i], M[i], L[i], p);
+      if (rp.store) write_row(rp, D, d4, o, M, L, p);
     } else {
       const long long row = (2ll * blockIdx.x + (x.u0 > 0 ? 0 : 1)) * kRows + r;
-      *reinterpret_cast<float4*>(p.part_o + row * D + d4) = o[i];
-      if (d4 == 0) p.part_ml[row] = make_float2(M[i], L[i]);
+      *reinterpret_cast<float4*>(p.part_o + row * D + d4) = o;
+      if (d4 == 0) p.part_ml[row] = make_float2(M, L);
     }
   }
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(const DecodeParams p) {
   using C = DecodeCfg<D, NT>;
-  constexpr int kRows = C::kRows;
+  constexpr int kRows = C::kRows, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_sums[kWarps];
+  __shared__ long long s_sums[kMaxWarps];
   __shared__ From s_from;
   __shared__ LoadCursor s_load[kWarps];
   __shared__ Shared s_shared[kWarps][2];
@@ -733,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
       w.item = at < 0x7fffffffll ? static_cast<int>(at) / cost : static_cast<int>(at / cost);
       const int in_item = static_cast<int>(at - static_cast<long long>(w.item) * cost);
       w.set(in_item);
-      if (warp == 0 && lane == 0 && w.u0 > 0) {
-        // the range starts within an item: is this the item's first cut?
+      if (from == 0 && lane == 0 && w.u0 > 0) {
+        // the CTA's range starts within an item: is this the item's first cut?
         const long long a = begin - in_item;  // its start
         if (all * (c - 1) / ctas <= a + kItemUnits)
           p.cuts[c] = Cut{w.s, w.item, static_cast<int>(c - 1), static_cast<int>(((a + cost) * ctas + all - 1) / all - 1)};
@@ -889,33 +883,19 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NT>::kCtasPerSm) decode
     }
   }
   __syncthreads();
-  // Eight rows of an item to a warp, or a warp's lanes' worth where there are few items.
-  constexpr int kLanes = D / 4, kSide = 32 / kLanes, kSteps = 8 / kSide;  // lanes of a row, rows side by side
-  const int r0 = lane / kLanes, d4 = lane % kLanes * 4;
-  if (s_groups * NT >= kWarps) {
-#pragma unroll 1
-    for (int idx = warp; idx < s_groups * NT; idx += kWarps) {
-      const int group = idx / NT, first = s_group[group];
-      combine<D, NT, kSteps>(s_entry + first, s_group[group + 1] - first, idx % NT * 8 + r0, d4, smem, s_shared, p);
-    }
-  } else {
-#pragma unroll 1
-    for (int idx = warp; idx < s_groups * NT * kSteps; idx += kWarps) {
-      const int group = idx / (NT * kSteps), first = s_group[group];
-      combine<D, NT, 1>(s_entry + first, s_group[group + 1] - first, idx % (NT * kSteps) * kSide + r0, d4, smem, s_shared, p);
-    }
-  }
+  combine<D, NT>(s_entry, s_group, s_groups, smem, s_shared, p);
 }
 
 constexpr int kMergeRows = 2;  // rows of a CTA of merge_kernel
+constexpr int kMergeThreads = 256;
 
 // Block (c, y): rows 2y, 2y+1 of the item that the start of CTA c's range cuts
 // first, if it does: its parts' states are merged as the warps' were.  D / 4
 // threads take a row's part, several parts side by side.
 template <int D>
-__global__ void __launch_bounds__(kThreads) merge_kernel(const DecodeParams p, int rows) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const DecodeParams p, int rows) {
   constexpr int kLanes = D / 4;                               // threads of one row
-  constexpr int kSide = kThreads / (kMergeRows * kLanes);     // parts side by side
+  constexpr int kSide = kMergeThreads / (kMergeRows * kLanes);     // parts side by side
   __shared__ float4 s_o[kSide][kMergeRows][kLanes];
   __shared__ float2 s_ml[kSide][kMergeRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has finished and its writes are here
@@ -926,7 +906,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const DecodeParams p, i
   auto row_of = [&](int c) { return (2ll * c + (c == cut.c0 ? 1 : 0)) * rows + r; };
   float M = kNone, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 8;  // parts loaded together
+  constexpr int kAhead = 4;  // parts loaded together
   for (int c = cut.c0 + side; c <= cut.c1; c += kSide * kAhead) {
     float2 ml[kAhead];
     float4 o[kAhead];
