@@ -155,6 +155,12 @@ int fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* l
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.status = view.status;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
   p.T = T;
   p.Hq = Hq;
   p.Hkv = Hkv;

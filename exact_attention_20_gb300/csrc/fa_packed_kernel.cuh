@@ -24,8 +24,9 @@
 //   the packed tensors (the token is an outer TMA coordinate, so any start is
 //   fine).  The last tile runs past the item's visible keys, into later
 //   tokens, the next sequence or rows behind the last one.  Their scores are
-//   replaced by -inf; their V rows are zeroed in shared memory, since
-//   0 * NaN would reach every row.
+//   replaced by -inf; P is 0 there, but 0 * NaN is NaN: the V rows past the
+//   item's last visible key are zeroed in shared memory, and a row that comes
+//   out NaN under the mask is looked at again (mend_rows).
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -89,6 +90,8 @@ struct Params {
   float* part_o;      // workspace: [slot][256 rows] of D fp32, a part's O normalised within it
   float* part_lse;    // workspace: [slot][256], the part's natural-log logsumexp
   int* counters;      // workspace: part arrivals, zero when the launch starts
+  const __nv_bfloat16 *q, *k, *v;  // for mend_rows alone; token strides below
+  long long q_stride, k_stride, v_stride;
   int T, Hq, Hkv, G;
   int tpt;            // tokens of a query tile: floor(128 / G)
   float qk_scale;     // scale * log2(e)
@@ -368,6 +371,19 @@ __device__ __forceinline__ size_t part_index(int slot, int row, int group) {
   return static_cast<size_t>(slot) * kItemRows * D + (static_cast<size_t>(group) * kItemRows + row) * 8;
 }
 
+// The larger of two values (fp32 bits, or two bf16), NaN where either is.
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+  return __float_as_uint(r);
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ bool is_nan(uint32_t x) { return (x & 0x7fffffffu) > 0x7f800000u; }
+
 // What this warp has of a split item: its state as the end of a chunk left it.
 constexpr int kStored = 0;  // in the workspace, like the others
 constexpr int kInTmem = 1;  // in tensor memory
@@ -383,9 +399,10 @@ struct Own {
 // L = ln sum_r exp(L_r), O = sum_r exp(L_r - L) O_r, the largest L_r
 // subtracted first; a part without keys for a row has L_r = -inf and weighs 0.
 // Every other part's rows are in the workspace.  Parts are added in key
-// order, so the result does not depend on who merges.
+// order, so the result does not depend on who merges.  Returns NaN (fp32 bits)
+// where an element of the own part in tensor memory is.
 template <int D>
-__device__ __forceinline__ void merge_rows(const Part part, const Own own, int r, bool store, __nv_bfloat16* orow,
+__device__ __forceinline__ uint32_t merge_rows(const Part part, const Own own, int r, bool store, __nv_bfloat16* orow,
                                         float* lse_dst, const float* part_o, const float* part_lse) {
   constexpr float kLog2e = 1.4426950408889634f;
   const int mine = own.where == kStored ? -1 : part.slot - part.slot0;
@@ -400,6 +417,7 @@ __device__ __forceinline__ void merge_rows(const Part part, const Own own, int r
 #pragma unroll 1
   for (int i = 0; i < part.count; ++i) sum += weight(lse_of(i), m);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t top = 0;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     float acc[32];
@@ -414,7 +432,10 @@ __device__ __forceinline__ void merge_rows(const Part part, const Own own, int r
         uint32_t o[32];
         tmem_ld32_wait(own.tO + c * 32, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * own.inv_l;
+        for (int e = 0; e < 32; ++e) {
+          top = max_nan(top, o[e]);
+          x[e] = __uint_as_float(o[e]) * own.inv_l;
+        }
       } else {
 #pragma unroll
         for (int n = 0; n < 4; ++n) ld_global_cg_v8(part_o + part_index<D>(part.slot0 + i, r, 4 * c + n), x + 8 * n);
@@ -433,6 +454,7 @@ __device__ __forceinline__ void merge_rows(const Part part, const Own own, int r
     }
   }
   if (store) *lse_dst = m + logf(sum);
+  return top;
 }
 
 // The warp's arrival for a part whose rows are in the workspace: true for the
@@ -460,6 +482,80 @@ struct Row {
     lse = store ? p.lse + static_cast<size_t>(head) * p.T + begin + token : p.lse;
   }
 };
+
+// Where a chunk's rows are stored: bf16 rows of O, or fp32 rows of a part.
+struct Mend {
+  __nv_bfloat16* o;  // the row in O, or null
+  float* part;       // the row's first group in the workspace, groups kItemRows * 8 apart
+  float m_ref, inv_l;
+};
+
+// Rows with NaN among their columns, stored by their warp: a NaN that comes
+// from keys that the row does not see (0 * NaN or 0 * infinity in the product
+// with P) is replaced by what the visible keys give.  A column needs that
+// where V is not finite at a key behind the row's token within the chunk's
+// tiles; its sum over the chunk's visible keys is then taken anew, key by key,
+// the warp together on one row.  Only values that are not finite lead here, so
+// it is a call: inlined it cost 24 ragged prompts 3 us of 150.
+template <int D>
+__device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0, const Cursor c, const Chunk ch,
+                                       const Mend mine, const Params& p) {
+  constexpr int kPer = D / 32;  // columns of a lane
+  const int behind = min(min(2 * (c.b + 1) * p.tpt, c.len), ch.ke * kBlockN);  // V rows from here on were zeroed or not read
+  auto load = [&](const __nv_bfloat16* row, float* x) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = __bfloat162float(row[lane * kPer + e]);
+  };
+  __syncwarp();
+  while (rows != 0) {
+    const int src = __ffs(rows) - 1;
+    rows &= rows - 1;
+    const int in_tile = (quad * 32 + src) / p.G, token = t0 + in_tile;
+    const int head = c.h * p.G + quad * 32 + src - in_tile * p.G;
+    const __nv_bfloat16* v = p.v + static_cast<long long>(c.begin) * p.v_stride + c.h * D;
+    bool need[kPer] = {};
+    for (int key = max(token + 1, ch.kb * kBlockN); key < behind; ++key) {
+      float x[kPer];
+      load(v + key * p.v_stride, x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) need[e] |= !(fabsf(x[e]) < INFINITY);
+    }
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) any |= need[e];
+    const float m_ref = __shfl_sync(0xffffffffu, mine.m_ref, src), inv_l = __shfl_sync(0xffffffffu, mine.inv_l, src);
+    const unsigned long long o = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.o), src);
+    const unsigned long long part = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.part), src);
+    if (!__any_sync(0xffffffffu, any)) continue;
+    float q[kPer], acc[kPer];
+    load(p.q + (c.begin + token) * p.q_stride + static_cast<long long>(head) * D, q);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    const __nv_bfloat16* k = p.k + static_cast<long long>(c.begin) * p.k_stride + c.h * D;
+    const int to = min(token + 1, ch.ke * kBlockN);
+#pragma unroll 4
+    for (int key = ch.kb * kBlockN; key < to; ++key) {
+      float x[kPer], y[kPer], dot = 0.f;
+      load(k + key * p.k_stride, x);
+      load(v + key * p.v_stride, y);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) dot = fmaf(q[e], x[e], dot);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      const float w = exp2f(fmaf(dot, p.qk_scale, -m_ref));
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, y[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = lane * kPer + e;
+      if (!need[e]) continue;
+      if (o != 0) reinterpret_cast<__nv_bfloat16*>(o)[col] = __float2bfloat16_rn(acc[e] * inv_l);
+      else reinterpret_cast<float*>(part)[col / 8 * kItemRows * 8 + col % 8] = acc[e] * inv_l;
+    }
+  }
+  __syncwarp();
+}
 
 // ---------------------------------------------------------------------------
 // Softmax / correction / epilogue warpgroup (128 threads, one row each)
@@ -655,6 +751,8 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
     if (whole && empty) continue;
     const Cursor c = place->c;
     const Row row(c.begin, c.len, c.h, (2 * c.b + t) * p.tpt, row_in_tile, D, p);
+    // whether the chunk's last V tiles held keys that some of the item's rows do not see
+    const bool masked = CAUSAL && !empty && place->ch.ke > 2 * c.b * p.tpt / kBlockN;
     if (!whole) {
       const Part part = i == 0 ? r.first : r.last;
       const int r_item = t * kBlockM + row_in_tile;  // row within the item, and its slot
@@ -664,24 +762,43 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       // else it stores them and arrives.
       int* ctr = p.counters + part.k * kCountersPerItem + t * 4 + quad;
       bool merge = (i > 0 || r.n_items == 1) && __all_sync(0xffffffffu, ld_acquire_gpu(ctr) == part.count - 1);
-      if (!merge) {
-        if (own.where == kInTmem) {
+      bool store = !merge;
+#pragma unroll 1
+      for (;;) {
+        if (store) {
+          if (own.where == kInTmem) {
+            uint32_t top = 0;  // NaN where an element of the row is
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            uint32_t o[32];
-            tmem_ld32_wait(tO + e * 32, o);
+            for (int e = 0; e < D / 32; ++e) {
+              uint32_t o[32];
+              tmem_ld32_wait(tO + e * 32, o);
 #pragma unroll
-            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * own.inv_l);
+              for (int n = 0; n < 32; ++n) {
+                top = max_nan(top, o[n]);
+                o[n] = __float_as_uint(__uint_as_float(o[n]) * own.inv_l);
+              }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) st_global_v8(p.part_o + part_index<D>(part.slot, r_item, e * 4 + n), o + n * 8);
+              for (int n = 0; n < 4; ++n) st_global_v8(p.part_o + part_index<D>(part.slot, r_item, e * 4 + n), o + n * 8);
+            }
+            const uint32_t rows = __ballot_sync(0xffffffffu, row.store && is_nan(top));
+            if (masked && rows != 0)
+              mend_rows<D>(rows, lane, quad, (2 * c.b + t) * p.tpt, c, place->ch,
+                           Mend{nullptr, p.part_o + part_index<D>(part.slot, r_item, 0), m_ref, own.inv_l}, p);
           }
+          p.part_lse[static_cast<size_t>(part.slot) * kItemRows + r_item] = own.lse;
+          own.where = kStored;
+          // merged already, but for NaN rows; or arrive (in the range's first chunk: with the next one)
+          if (!merge && (i > 0 || r.n_items == 1)) merge = part_arrive(ctr, part.count, lane);
         }
-        p.part_lse[static_cast<size_t>(part.slot) * kItemRows + r_item] = own.lse;
-        own.where = kStored;
-        if (i > 0 || r.n_items == 1) merge = part_arrive(ctr, part.count, lane);  // else: with the next chunk
+        if (!merge) break;
+        __syncwarp();
+        const uint32_t top = merge_rows<D>(part, own, r_item, row.store, row.o, row.lse, p.part_o, p.part_lse);
+        // a NaN row is mended in the workspace, and merged again
+        store = masked && own.where == kInTmem && __any_sync(0xffffffffu, row.store && is_nan(top));
+        if (!store) break;
       }
-      if (merge) merge_rows<D>(part, own, r_item, row.store, row.o, row.lse, p.part_o, p.part_lse);
     } else {
+      uint32_t top = 0;  // NaN where an element of the row is
       const uint64_t il2 = f2_pack(own.inv_l, own.inv_l);
       auto to_bf16 = [&](const uint32_t* o) {  // two elements of the row
         float lo, hi;
@@ -701,9 +818,12 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
             uint32_t o[32];
             tmem_ld32_wait(tO + e * 64 + h * 32, o);
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              *reinterpret_cast<uint4*>(out + lane * 128 + (((h * 4 + n) ^ (lane & 7)) * 16)) =
-                  make_uint4(to_bf16(o + 8 * n), to_bf16(o + 8 * n + 2), to_bf16(o + 8 * n + 4), to_bf16(o + 8 * n + 6));
+            for (int n = 0; n < 4; ++n) {
+              const uint4 w = make_uint4(to_bf16(o + 8 * n), to_bf16(o + 8 * n + 2), to_bf16(o + 8 * n + 4),
+                                         to_bf16(o + 8 * n + 6));
+              if (CAUSAL) top = max_nan_bf16x2(top, max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w)));
+              *reinterpret_cast<uint4*>(out + lane * 128 + (((h * 4 + n) ^ (lane & 7)) * 16)) = w;
+            }
           }
           __syncwarp();
 #pragma unroll
@@ -724,6 +844,11 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
           tmem_ld32_wait(tO + e * 32, o);
 #pragma unroll
           for (int n = 0; n < 16; ++n) w[n] = to_bf16(o + 2 * n);
+          if constexpr (CAUSAL) {
+#pragma unroll
+            for (int n = 0; n < 16; n += 4)
+              top = max_nan_bf16x2(top, max_nan_bf16x2(max_nan_bf16x2(w[n], w[n + 1]), max_nan_bf16x2(w[n + 2], w[n + 3])));
+          }
           if (row.store && wide) {
             st_global_v8(row.o + e * 32, w);
             st_global_v8(row.o + e * 32 + 16, w + 8);
@@ -735,6 +860,11 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
         }
       }
       if (row.store) *row.lse = own.lse;
+      if (CAUSAL) {
+        const uint32_t rows = __ballot_sync(0xffffffffu, row.store && ((top & 0x7fffu) > 0x7f80u || (top & 0x7fff0000u) > 0x7f800000u));
+        if (rows != 0)
+          mend_rows<D>(rows, lane, quad, (2 * c.b + t) * p.tpt, c, place->ch, Mend{row.o, nullptr, m_ref, own.inv_l}, p);
+      }
     }
     if (!empty) {
       tc_fence_before_sync();

@@ -52,9 +52,9 @@ extern "C" {
  *   scale   : as for fa_fwd.
  *
  * A row whose visible scores are all -inf gets O = 0 and LSE = -inf.  P is
- * rounded to bf16 before P.V, every sum is fp32, O is rounded once.  Whatever
- * lies in the tensors outside a sequence, NaN and infinities included, does
- * not reach its results.  One launch per 1024 sequences, with a memset of the
+ * rounded to bf16 before P.V, every sum is fp32, O is rounded once.  What a
+ * row does not see, other sequences and (causal) later tokens, does not reach
+ * it even where that holds NaN or infinities.  One launch per 1024 sequences, with a memset of the
  * workspace's counters before it where items are split between CTAs.
  * Results do not depend on timing: two calls give the same bits.
  *

@@ -163,3 +163,75 @@ def test_no_tokens(serve):
     assert (o == 7.0).all() and (lse == 7.0).all()
     o, lse = serve.attention_packed(q[:0], k[:0], v[:0], [0])
     assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+
+
+def exact_rows(q, k, v, n, causal, scale):
+    """One sequence, row by row from the keys it sees alone, in 64 bits: O [n, hq, d] (NaN and infinities as they come)."""
+    group = q.shape[1] // k.shape[1]
+    kd, vd = (t.double().repeat_interleave(group, 1) for t in (k, v))
+    o = torch.zeros((n, q.shape[1], q.shape[2]), dtype=torch.float64, device=DEV)
+    lse = torch.zeros((q.shape[1], n), dtype=torch.float64, device=DEV)
+    for i in range(n):
+        seen = i + 1 if causal else n
+        s = torch.einsum("hd,mhd->hm", q[i].double(), kd[:seen]) * scale
+        lse[:, i] = torch.logsumexp(s, -1)
+        o[i] = torch.einsum("hm,mhd->hd", torch.softmax(s, -1), vd[:seen])
+    return o, lse
+
+
+def same_but_for_rounding(o, o64):
+    """Non-finite where the reference is, of the same kind; elsewhere within the rounding (see above, with w|V| <= 4)."""
+    assert torch.equal(torch.isnan(o.float()), torch.isnan(o64))
+    assert torch.equal(torch.isposinf(o.float()), torch.isposinf(o64))
+    assert torch.equal(torch.isneginf(o.float()), torch.isneginf(o64))
+    fin = torch.isfinite(o64)
+    tol = (2.0 ** -7 + 2.0 ** -11) * (4 + o64[fin].abs()) + 2.0 ** -8 * o64[fin].abs()
+    assert ((o.double() - o64)[fin].abs() <= tol).all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2), (3, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(serve, hq, hkv, d, causal):
+    lens = [300, 70, 129, 40]
+    q, k, v = make(lens, hq, hkv, d, seed=7, tail=100)
+    v, k = v.clone(), k.clone()
+    at = [0, 300, 370, 499, 539]
+    v[at[0] + 299, 0, 3] = math.nan       # the last token's row alone sees it
+    v[at[0] + 130, 0, 5] = math.inf
+    v[at[0] + 131, 0, 5] = -math.inf      # from here on NaN in that column
+    v[at[0] + 255, 0, d - 1] = -math.inf  # an edge of tiles
+    v[at[0] + 0, 0, 7] = math.nan         # every row
+    v[at[1]:at[2]] = math.nan             # a whole sequence, its neighbours untouched
+    k[at[2] + 64, 0, 0] = math.nan        # a key: the rows that see it are NaN throughout
+    v[at[4]:], k[at[4]:], q[at[4]:] = math.nan, math.inf, math.nan  # behind the last sequence
+    o, lse = serve.attention_packed(q, k, v, lens, causal=causal)
+    for a, n in zip(at, lens):
+        o64, lse64 = exact_rows(q[a:a + n], k[a:a + n], v[a:a + n], n, causal, d ** -0.5)
+        same_but_for_rounding(o[a:a + n], o64)
+        assert torch.equal(torch.isnan(lse[:, a:a + n]), torch.isnan(lse64))
+    assert torch.isfinite(o[at[3]:at[4]].float()).all()
+
+
+def test_not_finite_values_in_split_items(serve):
+    lens = [2100]
+    q, k, v = make(lens, 4, 1, 128, seed=8)
+    v = v.clone()
+    for token, col in ((2099, 0), (2001, 1), (1500, 2), (17, 3), (1990, 127)):
+        v[token, 0, col] = math.inf if token % 2 else math.nan
+    o, _ = serve.attention_packed(q, k, v, lens)
+    for token in list(range(0, 40)) + list(range(1495, 1510)) + list(range(1960, 2100)):
+        s = torch.einsum("hd,md->hm", q[token].double(), k[:token + 1, 0].double()) * 128 ** -0.5
+        same_but_for_rounding(o[token:token + 1], (torch.softmax(s, -1) @ v[:token + 1, 0].double()).unsqueeze(0))
+    assert torch.isfinite(o[:17].float()).all()
+
+
+def test_scores_that_are_all_minus_infinity(serve):
+    # a row without weight: O = 0, LSE = -inf, and its neighbours as they are
+    q, k, v = make([50], 1, 1, 64, seed=9)
+    k, q = k.clone(), q.clone()
+    q[:, 0, 0], k[:, 0, 0] = 1.0, -math.inf
+    k[20, 0, 0] = 0.0
+    o, lse = serve.attention_packed(q, k, v, [50])
+    assert torch.isneginf(lse[0, :20]).all() and (o[:20] == 0).all()
+    assert torch.isfinite(lse[0, 20:]).all() and torch.equal(o[20:, 0].float(), v[20, 0].float().expand(30, -1))
