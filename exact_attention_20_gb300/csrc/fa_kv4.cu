@@ -120,6 +120,7 @@ int move(bool store, const void* k, const void* v, void* k_out, void* v_out, voi
   p.k_scale = store ? 1.f / k_scale : k_scale;
   p.v_scale = store ? 1.f / v_scale : v_scale;
   p.tokens_per_cta = tokens_per_cta(T, view.num_sms);
+  p.wide = !misaligned(a, 32) && !misaligned(b, 32) && k_stride % 16 == 0 && v_stride % 16 == 0;
   const int grid = (T + p.tokens_per_cta - 1) / p.tokens_per_cta;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (store) {
@@ -245,7 +246,9 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
   rc = check_cache(cache, page_table, seq_lens, n_seqs, max_pages, num_pages, page_size, Hkv, d, k_scale, v_scale, &cb);
   if (rc != FA_OK) return rc;
   const long long row = static_cast<long long>(Hq) * d;
-  if (!std::isfinite(scale) || !(scale > 0.f) || q_stride < row || q_stride % 8 || q_stride > (1ll << 32))
+  const float qk_scale = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
+  if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(qk_scale) || !(qk_scale > 0.f) || q_stride < row ||
+      q_stride % 8 || q_stride > (1ll << 32))
     return FA_ERR_INVALID_ARG;
   if (n_seqs == 0) return FA_OK;
   if (!q || !o || !lse) return FA_ERR_NULL;
@@ -289,7 +292,7 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
   p.status = view.status;
   p.q_stride = q_stride;
   p.wait_limit_ns = fa_internal::kWaitLimitNs;
-  p.qk_scale = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
+  p.qk_scale = qk_scale;
   p.v_scale = v_scale;
   p.n_seqs = n_seqs;
   p.Lq = Lq;

@@ -122,6 +122,13 @@ __device__ __forceinline__ void quantise_block(const uint32_t* x, float inv_g, u
   codes[1] = pack_e2m1x8(y + 8);
 }
 
+// Eight words, read once; `ptr` 32-byte aligned.
+__device__ __forceinline__ void ld_global_nc_v8(const void* ptr, uint32_t* r) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(ptr));
+}
+
 struct MoveParams {
   const __nv_bfloat16* k;  // store: [T][Hkv][D], token strides below
   const __nv_bfloat16* v;
@@ -135,6 +142,7 @@ struct MoveParams {
   long long k_stride, v_stride;
   int T, n_seqs, max_pages, num_pages, page_shift, Hkv;  // page_size = 1 << page_shift
   int tokens_per_cta;
+  int wide;                // rows of k, v (store) or k_out, v_out (load) are 32-byte aligned
   float k_scale, v_scale;  // store: their inverses
 };
 
@@ -213,8 +221,13 @@ __global__ void __launch_bounds__(kMoveThreads) store_kernel(const MoveParams p)
     const __nv_bfloat16* src = (is_v ? p.v + static_cast<long long>(first + i) * p.v_stride
                                      : p.k + static_cast<long long>(first + i) * p.k_stride) +
                                static_cast<long long>(h) * D + block * kBlock;
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t x[8];
+    if (p.wide) {
+      ld_global_nc_v8(src, x);
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
     uint32_t codes[2], scale;
     quantise_block(x, is_v ? p.v_scale : p.k_scale, codes, scale);
     uint8_t* group = p.cache + (place - row) + static_cast<long long>(h) * head_bytes;
@@ -264,8 +277,12 @@ __global__ void __launch_bounds__(kMoveThreads) load_kernel(const MoveParams p) 
     }
     __nv_bfloat16* dst = (is_v ? p.v_out : p.k_out) +
                          (static_cast<long long>(first + i) * p.Hkv + h) * D + block * kBlock;
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    if (p.wide) {
+      st_global_v8(dst, out);
+    } else {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    }
   }
 }
 

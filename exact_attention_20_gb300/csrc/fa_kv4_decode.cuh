@@ -302,6 +302,7 @@ struct State {
       } else {
         load_q_rows<D>(nt, row0, w, p, q[nt], factor);
       }
+      factor = fmaxf(factor, 1.17549435e-38f);  // positive: a masked score is -inf times it
       f[nt][0] = __shfl_sync(0xffffffffu, factor, 8 * t);  // lanes 4 r hold row r's
       f[nt][1] = __shfl_sync(0xffffffffu, factor, 8 * t + 4);
     }

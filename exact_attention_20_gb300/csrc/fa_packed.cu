@@ -106,7 +106,8 @@ int fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* l
   long long total = 0;
   int rc = check_sizes(seq_lens, n_seqs, T, Hq, Hkv, d, causal, &total);
   if (rc != FA_OK) return rc;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  const float qk_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (!std::isfinite(qk_scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   const long long q_row = static_cast<long long>(Hq) * d, kv_row = static_cast<long long>(Hkv) * d;
   constexpr long long kMaxStride = 1ll << 32;  // TMA takes byte strides below 2^40
   if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
@@ -166,7 +167,7 @@ int fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* l
   p.Hkv = Hkv;
   p.G = G;
   p.tpt = tpt;
-  p.qk_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.qk_scale = qk_scale;
   p.wait_limit_ns = fa_internal::kWaitLimitNs;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   begin = 0;

@@ -144,7 +144,8 @@ int fa_kv4_load(const void* cache, const int* page_table, const int* seq_lens, c
  *         to its own.
  *   o   : bf16 [n_seqs * Lq][Hq][d], contiguous; written.
  *   lse : fp32 [Hq][n_seqs * Lq]; written.
- *   scale : as for fa_fwd; k_scale and v_scale as for the store.
+ *   scale : as for fa_fwd; k_scale and v_scale as for the store.  scale *
+ *         k_scale stays within fp32's range.
  * A row that sees no key (a position below 0, an empty sequence) gets O = 0
  * and LSE = -inf.  Scores, sums and O are fp32; P is rounded to f16 before
  * P.V; O is rounded once.  One launch, and a second that merges the parts of

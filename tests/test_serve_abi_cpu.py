@@ -53,7 +53,7 @@ def packed(serve, **over):
 
 @pytest.mark.parametrize("over", [
     dict(n=-1), dict(T=-1), dict(T=(1 << 30) + 1), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(Hq=258),
-    dict(d=96), dict(d=0), dict(causal=2), dict(scale=0.0), dict(scale=float("nan")), dict(scale=-1.0),
+    dict(d=96), dict(d=0), dict(causal=2), dict(scale=0.0), dict(scale=float("nan")), dict(scale=-1.0), dict(scale=3e38),
     dict(T=127), dict(seq_lens=lens(-1, 5)), dict(seq_lens=lens(2 ** 31 - 1, 2 ** 31 - 1)),
     dict(qs=511), dict(qs=504), dict(qs=516), dict(ks=120), dict(vs=(1 << 32) + 8),
 ])
@@ -129,7 +129,7 @@ def test_cache_invalid(serve, fa, call, over):
     (store, dict(T=-1)), (store, dict(T=(1 << 30) + 1)), (store, dict(ks=120)), (store, dict(vs=132)), (load, dict(T=-1)),
     (attention, dict(Lq=0)), (attention, dict(Hq=7)), (attention, dict(Hq=0)), (attention, dict(Hq=258)),
     (attention, dict(scale=0.0)), (attention, dict(scale=float("inf"))), (attention, dict(qs=504)),
-    (attention, dict(qs=513)), (attention, dict(n=1 << 30, Lq=2)), (attention, dict(n=1 << 20, Hkv=1 << 16, Hq=1 << 16)),
+    (attention, dict(qs=513)), (attention, dict(scale=3e38, kg=2.0 ** 40)), (attention, dict(scale=1e-38, kg=2.0 ** -40)), (attention, dict(n=1 << 30, Lq=2)), (attention, dict(n=1 << 20, Hkv=1 << 16, Hq=1 << 16)),
 ])
 def test_cache_calls_invalid(serve, fa, call, over):
     assert call(serve, **over) == fa.FA_ERR_INVALID_ARG
