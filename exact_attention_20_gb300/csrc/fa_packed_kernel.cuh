@@ -29,6 +29,8 @@
 //   out NaN under the mask is looked at again (mend_rows).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_kernel.cuh"
 
 namespace fa {
@@ -246,6 +248,7 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
   const uint64_t v_desc0 = sdesc_sw128(sbase + C::kKVOff, kSlabBytes, 1024);
   const uint32_t tm_s = tmem + t * 128;
   const uint32_t tm_o = tmem + 256 + t * 128;
+  constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, /*b_mn_major=*/false);
   uint32_t q_uses = 0, kv_count = 0, pr_par = 0, of_par = 1, turn_par = 0;
   bool ok = true;
   auto full = [&](uint32_t c) { return sy.kv_full0 + 8 * (c % C::kStages); };
@@ -273,13 +276,16 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
     const int ne = min(ch.ke, tiles_for<CAUSAL>(cur.b, t, cur.len, p.tpt));  // this tile's key tiles: [kb, ne)
     // The item's last V tile, where it is in this chunk: its rows from
     // `visible` on belong to no visible key.  The first issuer that uses the
-    // tile zeroes them (the other is ordered behind it by the turn).
+    // tile zeroes those that the products, 16 keys at a time, still reach (the
+    // other is ordered behind it by the turn).
     const int visible = (CAUSAL ? min((2 * cur.b + 2) * p.tpt, cur.len) : cur.len) - (ch.steps - 1) * kBlockN;
-    const int zero_at =
-        ch.ke == ch.steps && visible < kBlockN &&
-                (t == 0 || tiles_for<CAUSAL>(cur.b, 0, cur.len, p.tpt) < ch.steps)
-            ? ch.steps - 1
-            : -1;
+    const int zero_rows = min(kBlockN, (visible + 15) & ~15) - visible;
+    const int zero_at = ch.ke == ch.steps && zero_rows > 0 &&
+                                (t == 0 || tiles_for<CAUSAL>(cur.b, 0, cur.len, p.tpt) < ch.steps)
+                            ? ch.steps - 1
+                            : -1;
+    // keys that some row of this query tile sees: its last tile's products stop there
+    const int seen = CAUSAL ? min((2 * cur.b + t + 1) * p.tpt, cur.len) : cur.len;
     if (ne > kb) {
       wait_voted(bar_q_full, q_uses & 1u);
       ++q_uses;
@@ -294,11 +300,10 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
         wait_full(cv);
         if (s - 1 == zero_at && ok) {
           uint8_t* tile = smem + C::kKVOff + (cv % C::kStages) * C::kTileBytes;
-          const int rows = kBlockN - visible;
-          for (int n = lane; n < rows * 8 * C::kSlabs; n += 32) {  // whole 128-byte rows, so the swizzle is no matter
-            const int slab = n / (rows * 8), in = n % (rows * 8);
-            *reinterpret_cast<uint4*>(tile + slab * kSlabBytes + visible * 128 + in * 16) = make_uint4(0, 0, 0, 0);
-          }
+#pragma unroll
+          for (int slab = 0; slab < C::kSlabs; ++slab)  // whole 128-byte rows, so the swizzle is no matter
+            for (int n = lane; n < zero_rows * 8; n += 32)
+              *reinterpret_cast<uint4*>(tile + slab * kSlabBytes + visible * 128 + n * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
@@ -318,6 +323,10 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
         }
       }
       const uint32_t acc0 = s > kb + 1 ? 1u : 0u;
+      // Groups of 16 keys that P V takes.  (Q K^T always takes all 128: with fewer
+      // columns it measured slower, and S and P V of one shape are what is known to
+      // stay in order.)
+      const int groups_pv = min(kBlockN, seen - (s - 1) * kBlockN + 15) / 16;
       if (do_pv) {
         if (s == kb + 1) {
           wait_voted(bar_o_free, of_par);
@@ -333,11 +342,16 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
       if (leader) {
         if (do_pv) {
           constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, /*b_mn_major=*/true);
+          if (groups_pv == C::kPvInstr) {
 #pragma unroll
-          for (int kk = 0; kk < C::kPvInstr; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+            for (int kk = 0; kk < C::kPvInstr; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < C::kPvInstr - 1; ++kk)
+              if (kk < groups_pv) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+          }
         }
         if (do_s) {
-          constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, /*b_mn_major=*/false);
 #pragma unroll
           for (int kk = 0; kk < C::kQkInstr; ++kk) umma_ss(tm_s, dq[kk], dk[kk], idesc_qk, kk > 0 ? 1u : 0u);
         }
@@ -586,9 +600,8 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
   Place* place = reinterpret_cast<Place*>(shared_base() + C::kCursorOff) + (threadIdx.x >> 5);
   const Range& r = p.range[blockIdx.x];
   for (int i = 0; i < r.n_items && ok; ++i) {
-    int t0, ne, kb;
+    int ne, kb, first_masked;
     bool empty;
-    int seen, first_masked;
     {
       Cursor c = i == 0 ? Cursor(r, p) : place->c;
       if (i > 0) c.next(p);
@@ -596,13 +609,11 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       __syncwarp();
       if (lane == 0) *place = Place{c, ch};
       __syncwarp();
-      t0 = (2 * c.b + t) * p.tpt;  // the tile's first token within the sequence
       kb = ch.kb;
       ne = min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
       // a part may have no key tile of this query tile; it still reports its rows, as an empty part
       empty = ne <= kb;
-      seen = CAUSAL ? min(t0 + row_in_tile / p.G, c.len - 1) : c.len - 1;             // the row's last visible key
-      first_masked = (CAUSAL ? min(t0, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
+      first_masked = (CAUSAL ? min((2 * c.b + t) * p.tpt, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
       if (!CAUSAL && (c.len & (kBlockN - 1)) == 0) first_masked = ne;
     }
     if (i == 1 && r.first.slot >= 0) {
@@ -618,95 +629,140 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
     float l = 0.f;            // running sum of exp2(s*qk - m_ref), for the logsumexp
     float lq = 0.f;           // the same terms rounded to bf16 (what P.V multiplies), for O
 
-    for (int j = kb; j < ne; ++j) {
+    // One key tile; the masked ones, at the end, have a loop and registers of their own.
+    auto step = [&](auto masked_tile, int j) {
       ok = wait_phase(bar_s_full, s_par, sy, p);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!ok) return;
       s_par ^= 1u;
       tc_fence_after_sync();
-
-      uint32_t s[128];
-      tmem_ld128_wait(tS, s);
-      if (j >= first_masked) {
-        const int lim = seen - j * kBlockN;
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e > lim) s[e] = __float_as_uint(-INFINITY);
-      }
 
       const uint64_t qk2 = f2_pack(qk, qk);
       float alpha = 1.f;
       float sa, sb, lq_tile;
-      // One pass over the tile: exponentials against m_use, P stored to
-      // tensor memory over S, the fp32 and bf16 row sums, and (if asked) the
-      // tile's row maximum from the same values.
-      auto exp_pass = [&](float m_use, bool with_max) -> float {
+      if constexpr (decltype(masked_tile)::value) {
+        // A masked tile: 32 columns at a time, up to the last that some row of
+        // the tile sees; the maximum first, then the exponentials from S read
+        // again (P's 16 columns lie over columns of S read before).
+        const int len = place->c.len, t0 = (2 * place->c.b + t) * p.tpt;  // the tile's first token
+        const int lim = (CAUSAL ? min(t0 + row_in_tile / p.G, len - 1) : len - 1) - j * kBlockN;  // the row's last visible key
+        const int cols = (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN;
+        auto load = [&](int c4, uint32_t* x) {
+          tmem_ld32_wait(tS + c4 * 32, x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c4 * 32 + e > lim) x[e] = __float_as_uint(-INFINITY);
+        };
+        float m_tile = -INFINITY;
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4 && c4 * 32 < cols; ++c4) {
+          uint32_t x[32];
+          load(c4, x);
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx[e >> 1 & 1] = fmax3(mx[e >> 1 & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          m_tile = fmax3(m_tile, mx[0], mx[1]);
+        }
+        m_tile *= qk;  // qk > 0: max commutes with the scale
+        if (m_tile > m_ref + kRescaleThreshold<2>) {
+          alpha = ex2_approx(m_ref - m_tile);  // 0 when m_ref = -inf
+          m_ref = m_tile;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // 0: no key of this part visible yet, P = 0
         const uint64_t negm2 = f2_pack(-m_use, -m_use);
         uint64_t sum2 = f2_pack(0.f, 0.f);
         float lqs[4] = {0.f, 0.f, 0.f, 0.f};
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t pk[16];
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4 && c4 * 32 < cols; ++c4) {
+          uint32_t x[32], pk[16];
+          load(c4, x);
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const int e = c4 * 32 + 2 * n;
-            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), qk2, negm2);
             float xa, xb;
-            f2_unpack(x, xa, xb);
-            const float a = ex2_approx(xa);
-            const float b = ex2_approx(xb);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * n]), __uint_as_float(x[2 * n + 1])), qk2, negm2), xa, xb);
+            const float a = ex2_approx(xa), b = ex2_approx(xb);
             pk[n] = pack_bf16x2(a, b);
             sum2 = f2_add(sum2, f2_pack(a, b));
             add_bf16x2_halves(lqs[(n & 1) * 2], lqs[(n & 1) * 2 + 1], pk[n]);
-            if (with_max) mx[c4] = fmax3(mx[c4], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
           }
           tmem_st16(tS + c4 * 16, pk);
         }
         f2_unpack(sum2, sa, sb);
         lq_tile = (lqs[0] + lqs[1]) + (lqs[2] + lqs[3]);
-        return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;  // qk > 0: max commutes with the scale
-      };
-      auto row_max = [&]() -> float {
-        float mx[4];
+      } else {
+        uint32_t s[128];
+        tmem_ld128_wait(tS, s);
+        // One pass over the tile: exponentials against m_use, P stored to
+        // tensor memory over S, the fp32 and bf16 row sums, and (if asked) the
+        // tile's row maximum from the same values.
+        auto exp_pass = [&](float m_use, bool with_max) -> float {
+          const uint64_t negm2 = f2_pack(-m_use, -m_use);
+          uint64_t sum2 = f2_pack(0.f, 0.f);
+          float lqs[4] = {0.f, 0.f, 0.f, 0.f};
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
-          mx[q4] = fmax3(__uint_as_float(s[32 * q4]), __uint_as_float(s[32 * q4 + 1]), __uint_as_float(s[32 * q4 + 2]));
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t pk[16];
 #pragma unroll
-        for (int e = 3; e < 31; e += 2) {
+            for (int n = 0; n < 16; ++n) {
+              const int e = c4 * 32 + 2 * n;
+              const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), qk2, negm2);
+              float xa, xb;
+              f2_unpack(x, xa, xb);
+              const float a = ex2_approx(xa);
+              const float b = ex2_approx(xb);
+              pk[n] = pack_bf16x2(a, b);
+              sum2 = f2_add(sum2, f2_pack(a, b));
+              add_bf16x2_halves(lqs[(n & 1) * 2], lqs[(n & 1) * 2 + 1], pk[n]);
+              if (with_max) mx[c4] = fmax3(mx[c4], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            }
+            tmem_st16(tS + c4 * 16, pk);
+          }
+          f2_unpack(sum2, sa, sb);
+          lq_tile = (lqs[0] + lqs[1]) + (lqs[2] + lqs[3]);
+          return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;  // qk > 0: max commutes with the scale
+        };
+        auto row_max = [&]() -> float {
+          float mx[4];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4)
-            mx[q4] = fmax3(mx[q4], __uint_as_float(s[32 * q4 + e]), __uint_as_float(s[32 * q4 + e + 1]));
-        }
+            mx[q4] = fmax3(__uint_as_float(s[32 * q4]), __uint_as_float(s[32 * q4 + 1]), __uint_as_float(s[32 * q4 + 2]));
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) mx[q4] = fmaxf(mx[q4], __uint_as_float(s[32 * q4 + 31]));
-        return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;
-      };
-      if constexpr (CAUSAL) {
-        // the maximum first, then one pass (faster under the mask, with its many first tiles)
-        const float m_tile = row_max();
-        if (m_tile > m_ref + kRescaleThreshold<2>) {
-          alpha = ex2_approx(m_ref - m_tile);  // 0 when m_ref = -inf
-          m_ref = m_tile;
-        }
-        exp_pass(m_ref == -INFINITY ? 0.f : m_ref, false);  // 0: no key of this part visible yet, P = 0
-      } else {
-        // the exponentials against the current reference while the tile's
-        // maximum is found in the same pass; taken again where a row moved
-        if (m_ref == -INFINITY) {
-          m_ref = row_max();
-          alpha = 0.f;
-        }
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          const float m_tile = exp_pass(m_ref == -INFINITY ? 0.f : m_ref, true);
-          const bool move = m_tile > m_ref + kRescaleThreshold<2>;
-          if (!__any_sync(0xffffffffu, move)) break;
-          if (move) {
-            alpha = ex2_approx(m_ref - m_tile);
+          for (int e = 3; e < 31; e += 2) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              mx[q4] = fmax3(mx[q4], __uint_as_float(s[32 * q4 + e]), __uint_as_float(s[32 * q4 + e + 1]));
+          }
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) mx[q4] = fmaxf(mx[q4], __uint_as_float(s[32 * q4 + 31]));
+          return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;
+        };
+        if constexpr (CAUSAL) {
+          // the maximum first, then one pass (faster under the mask, with its many first tiles)
+          const float m_tile = row_max();
+          if (m_tile > m_ref + kRescaleThreshold<2>) {
+            alpha = ex2_approx(m_ref - m_tile);  // 0 when m_ref = -inf
             m_ref = m_tile;
           }
-          tmem_st_wait();  // the repeated pass stores P over this one's
+          exp_pass(m_ref == -INFINITY ? 0.f : m_ref, false);  // 0: no key of this part visible yet, P = 0
+        } else {
+          // the exponentials against the current reference while the tile's
+          // maximum is found in the same pass; taken again where a row moved
+          if (m_ref == -INFINITY) {
+            m_ref = row_max();
+            alpha = 0.f;
+          }
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            const float m_tile = exp_pass(m_ref == -INFINITY ? 0.f : m_ref, true);
+            const bool move = m_tile > m_ref + kRescaleThreshold<2>;
+            if (!__any_sync(0xffffffffu, move)) break;
+            if (move) {
+              alpha = ex2_approx(m_ref - m_tile);
+              m_ref = m_tile;
+            }
+            tmem_st_wait();  // the repeated pass stores P over this one's
+          }
         }
       }
       l = l * alpha + (sa + sb);
@@ -734,7 +790,10 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_p_ready);  // one arrival per warp
-    }
+    };
+    int j = kb;
+    for (const int to = min(ne, first_masked); j < to && ok; ++j) step(std::false_type{}, j);
+    for (; j < ne && ok; ++j) step(std::true_type{}, j);
     if (!ok) break;
 
     Own own{kEmpty, -INFINITY, 0.f, tO};
