@@ -137,12 +137,11 @@ int fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* l
 
   // the plans of all launches first, so that a workspace that is too small launches nothing
   pk::Params p;
-  int begin = 0;
+  int begin = 0, grid = 0, n_slots = 0, n_split = 0;
   size_t need = 0;
   for (int i = 0; i < n_seqs; i += pk::kMaxSeqs) {
     const int n = std::min(pk::kMaxSeqs, n_seqs - i);
-    int n_slots = 0, n_split = 0;
-    make_plan(seq_lens + i, n, begin, Hkv, tpt, causal, view.num_sms, p, n_slots, n_split);
+    grid = make_plan(seq_lens + i, n, begin, Hkv, tpt, causal, view.num_sms, p, n_slots, n_split);
     begin = p.cu[n];
     need = std::max(need, workspace_bytes(n_slots, n_split, d));
   }
@@ -173,8 +172,8 @@ int fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* l
   begin = 0;
   for (int i = 0; i < n_seqs; i += pk::kMaxSeqs) {
     const int n = std::min(pk::kMaxSeqs, n_seqs - i);
-    int n_slots = 0, n_split = 0;
-    const int grid = make_plan(seq_lens + i, n, begin, Hkv, tpt, causal, view.num_sms, p, n_slots, n_split);
+    if (n_seqs > pk::kMaxSeqs)  // else p still holds the one launch's plan
+      grid = make_plan(seq_lens + i, n, begin, Hkv, tpt, causal, view.num_sms, p, n_slots, n_split);
     begin = p.cu[n];
     if (grid == 0) continue;
     p.part_o = static_cast<float*>(workspace);

@@ -17,9 +17,10 @@
 //   is, and a short prompt fills G times as many rows as it has tokens.  G
 //   need not divide 128: the tile's last rows then stay unused.
 // - A work item is two such tiles, 2 floor(128 / G) tokens of one (sequence,
-//   KV head).  The host cuts the concatenated items into ranges of equal
-//   cost, one per CTA, as for the dense forward; an item cut between CTAs is
-//   computed in parts that meet in a workspace.
+//   KV head).  Where there are more items than CTAs and none is long, the host
+//   sorts them by length and deals them out; else it cuts the concatenated
+//   items into ranges of equal cost, one per CTA, as for the dense forward,
+//   and an item cut between CTAs is computed in parts that meet in a workspace.
 // - K/V tiles start at their sequence's first token, wherever that lies in
 //   the packed tensors (the token is an outer TMA coordinate, so any start is
 //   fine).  The last tile runs past the item's visible keys, into later
@@ -38,8 +39,10 @@ namespace packed {
 
 constexpr int kMaxCtas = 160;         // one CTA per SM
 constexpr int kMaxSeqs = 1024;        // sequences of one launch
+constexpr int kMaxPairs = 2048;       // (sequence, block) pairs of a dealt launch
 constexpr int kMaxParts = 8;          // parts of one split item
 constexpr int kCountersPerItem = 8;   // per query tile and warp quadrant
+constexpr int kItemsAhead = 4;        // items that the dispatcher has written and not all warps read
 constexpr int kSitePacked = 6;        // status code: a wait gave up
 
 // Shared memory: Q tiles, the K/V ring, and (d = 128) 4 KB a softmax warp to
@@ -57,10 +60,10 @@ struct PackedCfg {
   static constexpr int kOutOff = kKVOff + kStages * kTileBytes;
   static constexpr int kWarpOut = 32 * 128;
   static constexpr int kBarOff = kOutOff + (D == 128 ? 8 * kWarpOut : 0);
-  static constexpr int kNumBars = 2 * 2 + 2 * kStages + 2 * 4 + 1 + 2;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kCursorOff = kMiscOff + 16;         // [softmax warp] where it is
-  static constexpr int kSmemBytes = kCursorOff + 8 * 32 + 1024;  // + alignment slack
+  static constexpr int kNumBars = 2 * 2 + 2 * kStages + 2 * 4 + 1 + 2 + 2 * kItemsAhead;
+  static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kItemsOff = kMiscOff + 16;
+  static constexpr int kSmemBytes = kItemsOff + kItemsAhead * 64 + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "227 KB");
 };
 
@@ -85,6 +88,11 @@ struct Range {
   Part first, last;
 };
 
+// A dealt launch's item, for every KV head.
+struct Pair {
+  uint16_t s, b;
+};
+
 struct Params {
   __nv_bfloat16* o;   // [T][Hq][D]
   float* lse;         // [Hq][T]
@@ -99,7 +107,11 @@ struct Params {
   float qk_scale;     // scale * log2(e)
   unsigned long long wait_limit_ns;
   int cu[kMaxSeqs + 1];  // first token of each sequence, and the end of the last
-  Range range[kMaxCtas];
+  int dealt;          // items of a dealt launch, whose pairs are by length, longest first; 0: ranges
+  union {
+    Range range[kMaxCtas];
+    Pair pair[kMaxPairs];
+  };
 };
 
 // Key tiles that query tile t of block b visits (0 past the sequence's end).
@@ -119,7 +131,18 @@ __host__ __device__ __forceinline__ int item_steps(int b, int len, int tpt) {
   return a > c ? a : c;
 }
 
-// The items of a CTA's range in turn.
+// A CTA's i-th item among those dealt: one of each row of gridDim.x items, in
+// the rows' order back and forth, so that who got a row's longest item gets
+// the next row's shortest.  The pair's KV heads follow one another.
+__device__ __forceinline__ int dealt_at(int i) {
+  return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+__device__ __forceinline__ bool has_item(int i, const Params& p) {
+  return p.dealt > 0 ? dealt_at(i) < p.dealt : i < p.range[blockIdx.x].n_items;
+}
+
+// The items of a CTA in turn.
 struct Cursor {
   int s, h, b;
   int begin, len;  // the sequence's first token and length
@@ -127,9 +150,22 @@ struct Cursor {
     begin = p.cu[s];
     len = p.cu[s + 1] - begin;
   }
-  Cursor() = default;
-  __device__ __forceinline__ Cursor(const Range& r, const Params& p) : s(r.s), h(r.h), b(r.b) { at(p); }
-  __device__ __forceinline__ void next(const Params& p) {
+  __device__ __forceinline__ explicit Cursor(const Params& p) {
+    if (p.dealt > 0) {
+      deal(0, p);
+    } else {
+      const Range& r = p.range[blockIdx.x];
+      s = r.s, h = r.h, b = r.b;
+      at(p);
+    }
+  }
+  __device__ __forceinline__ void deal(int i, const Params& p) {
+    const int item = dealt_at(i), n = item / p.Hkv;
+    s = p.pair[n].s, h = item - n * p.Hkv, b = p.pair[n].b;
+    at(p);
+  }
+  __device__ __forceinline__ void next(int i, const Params& p) {  // to item i, from the one before
+    if (p.dealt > 0) return deal(i, p);
     if (++b * 2 * p.tpt < len) return;
     b = 0;
     if (++h < p.Hkv) return;
@@ -141,22 +177,27 @@ struct Cursor {
   }
 };
 
-// Key tiles [kb, ke) of one item with `steps`; all of them, or a part.
-struct Chunk {
-  int kb, ke, steps;
+// What the warps read of an item, or of the part of it that is this CTA's.
+struct alignas(16) Item {
+  int begin, len, h, b;  // the sequence's first token and length, the KV head, the block
+  int kb, ke, steps;     // key tiles [kb, ke) of `steps`
+  int more;              // whether another item follows
+  int ne[2];             // the key tiles that query tile t visits here: [kb, ne)
+  int plain[2];          // those before this one need no mask
+  int seen[2];           // keys that some row of query tile t sees
+  int visible;           // keys of the item's last tile that some row sees
+  int i;                 // the CTA's items before this one
   __device__ __forceinline__ bool whole() const { return kb == 0 && ke == steps; }
 };
+static_assert(sizeof(Item) == 64, "kItemsOff");
 
-template <bool CAUSAL>
-__device__ __forceinline__ Chunk chunk_of(int i, const Cursor& c, const Range& r, const Params& p) {
-  Chunk ch;
-  ch.steps = item_steps<CAUSAL>(c.b, c.len, p.tpt);
-  ch.kb = i == 0 ? r.step_begin : 0;
-  ch.ke = i == r.n_items - 1 ? r.step_end : ch.steps;
-  return ch;
-}
+struct PackedSync : Sync {
+  uint32_t item_full0, item_empty0;
+  const Item* items;
+};
 
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Sync& sy, const Params& p) {
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Sync& sy, const Params& p,
+                                           unsigned long long more_ns = 0) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   uint32_t polls = 0;
@@ -164,7 +205,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
     if (mbar_try_wait(bar, parity)) return true;
     if ((++polls & 31u) == 0u) {
       if (*sy.abort_flag) return false;
-      if (global_timer_ns() - t0 > p.wait_limit_ns) {
+      if (global_timer_ns() - t0 > p.wait_limit_ns + more_ns) {
         *sy.abort_flag = 1;
         atomicCAS(p.status, 0, kSitePacked);
         return false;
@@ -174,11 +215,51 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 }
 
 // ---------------------------------------------------------------------------
+// Dispatcher (one thread)
+// ---------------------------------------------------------------------------
+// Writes the CTA's items into a ring that all other warps read.  With each
+// warp finding its own way (registers that the issuers and the softmax lack,
+// and waits for parameters between items) a prompt of 16384 tokens took 753 us
+// instead of 745, 24 ragged prompts 125 instead of 121.
+template <bool CAUSAL>
+__device__ __forceinline__ void run_dispatcher(Item* items, const PackedSync& sy, const Params& p) {
+  Cursor c(p);
+  const Range& r = p.range[blockIdx.x];  // read where the launch is not dealt
+  unsigned long long steps = 0;          // of all items so far
+  for (int i = 0;; ++i) {
+    if (i > 0) c.next(i, p);
+    Item it;
+    it.begin = c.begin, it.len = c.len, it.h = c.h, it.b = c.b;
+    it.steps = item_steps<CAUSAL>(c.b, c.len, p.tpt);
+    it.more = has_item(i + 1, p);
+    it.kb = p.dealt == 0 && i == 0 ? r.step_begin : 0;
+    it.ke = p.dealt == 0 && !it.more ? r.step_end : it.steps;
+    it.i = i;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      it.ne[t] = min(it.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
+      it.seen[t] = CAUSAL ? min((2 * c.b + t + 1) * p.tpt, c.len) : c.len;
+      // the first tile with a key that some row does not see
+      const int masked = (CAUSAL ? min((2 * c.b + t) * p.tpt + 1, c.len) : c.len) / kBlockN;
+      it.plain[t] = min(it.ne[t], masked);
+    }
+    it.visible = it.seen[1] - (it.steps - 1) * kBlockN;
+    // free once the item kItemsAhead before is done; a step takes far less than 16 us
+    const uint32_t n = i % kItemsAhead;
+    if (!wait_phase(sy.item_empty0 + 8 * n, ((i / kItemsAhead) & 1u) ^ 1u, sy, p, steps << 14)) return;
+    items[n] = it;
+    mbar_arrive(sy.item_full0 + 8 * n);
+    if (!it.more) return;
+    steps += it.steps;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // TMA producer (one thread)
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL>
 __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                                             uint32_t sbase, const Sync& sy, const Params& p) {
+                                             uint32_t sbase, const PackedSync& sy, const Params& p) {
   using C = PackedCfg<D>;
   uint32_t q_loads[2] = {0, 0};
   uint32_t kv_count = 0;
@@ -186,24 +267,27 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
   const uint64_t pol_kv = l2_policy_evict_last();
   const uint32_t q_bytes = static_cast<uint32_t>(p.G * p.tpt) * D * 2;
   bool ok = true;
-  const Range& r = p.range[blockIdx.x];
-  Cursor c(r, p);
-  for (int i = 0; i < r.n_items && ok; ++i) {
-    if (i > 0) c.next(p);
-    const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
+  bool more = true;
+  for (uint32_t i = 0; more && ok; ++i) {
+    const uint32_t n = i % kItemsAhead;
+    ok = wait_phase(sy.item_full0 + 8 * n, (i / kItemsAhead) & 1u, sy, p);
+    if (!ok) break;
+    const Item it = sy.items[n];
+    mbar_arrive(sy.item_empty0 + 8 * n);
+    more = it.more;
     for (int t = 0; t < kQTiles; ++t) {
-      if (min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt)) <= ch.kb) continue;  // no key tile of its own here
+      if (it.ne[t] <= it.kb) continue;  // no key tile of its own here
       ok = wait_phase(sy.q_empty[t], (q_loads[t] & 1u) ^ 1u, sy, p);
       if (!ok) break;
       ++q_loads[t];
       mbar_arrive_expect_tx(sy.q_full[t], q_bytes);
       const uint32_t dst = sbase + C::kQOff + t * C::kTileBytes;
-      const int token = c.begin + (2 * c.b + t) * p.tpt;
+      const int token = it.begin + (2 * it.b + t) * p.tpt;
 #pragma unroll
       for (int s = 0; s < C::kSlabs; ++s)
-        tma_load_3d_hint(dst + s * kSlabBytes, tmQ, sy.q_full[t], s * 64, c.h * p.G, token, pol_q);
+        tma_load_3d_hint(dst + s * kSlabBytes, tmQ, sy.q_full[t], s * 64, it.h * p.G, token, pol_q);
     }
-    for (int j = ch.kb; j < ch.ke && ok; ++j) {
+    for (int j = it.kb; j < it.ke && ok; ++j) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         if (!ok) break;
@@ -215,7 +299,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
         const uint32_t dst = sbase + C::kKVOff + slot * C::kTileBytes;
 #pragma unroll
         for (int s = 0; s < C::kSlabs; ++s)
-          tma_load_3d_hint(dst + s * kSlabBytes, n == 0 ? tmK : tmV, full, s * 64, c.h, c.begin + j * kBlockN, pol_kv);
+          tma_load_3d_hint(dst + s * kSlabBytes, n == 0 ? tmK : tmV, full, s * 64, it.h, it.begin + j * kBlockN, pol_kv);
         ++kv_count;
       }
     }
@@ -232,7 +316,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
 // MMA issuers (one warp per query tile, strict turns, as in the dense forward)
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL>
-__device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, uint32_t tmem, const Sync& sy,
+__device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, uint32_t tmem, const PackedSync& sy,
                                         const Params& p) {
   using C = PackedCfg<D>;
   const uint32_t bar_q_full = t ? sy.q_full[1] : sy.q_full[0];
@@ -267,31 +351,34 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
   };
   if (t == 1 && leader) mbar_arrive(sy.turn[0]);  // tile 0 takes the first turn
 
-  const Range& r = p.range[blockIdx.x];
-  Cursor cur(r, p);
-  for (int i = 0; i < r.n_items && ok; ++i) {
-    if (i > 0) cur.next(p);
-    const Chunk ch = chunk_of<CAUSAL>(i, cur, r, p);
-    const int kb = ch.kb;
-    const int ne = min(ch.ke, tiles_for<CAUSAL>(cur.b, t, cur.len, p.tpt));  // this tile's key tiles: [kb, ne)
+  bool more = true;
+  for (uint32_t i = 0; more && ok; ++i) {
+    const uint32_t slot = i % kItemsAhead;
+    wait_voted(sy.item_full0 + 8 * slot, (i / kItemsAhead) & 1u);
+    if (!ok) break;
+    const Item& it = sy.items[slot];
+    // the same in every lane, and said to be: computed with once for the warp (740 us; else 744)
+    auto uniform = [&](int x) { return __reduce_max_sync(0xffffffffu, x); };
+    more = uniform(it.more);
+    const int kb = uniform(it.kb), ke = uniform(it.ke);
+    const int ne = uniform(t ? it.ne[1] : it.ne[0]);  // this tile's key tiles: [kb, ne)
     // The item's last V tile, where it is in this chunk: its rows from
     // `visible` on belong to no visible key.  The first issuer that uses the
     // tile zeroes those that the products, 16 keys at a time, still reach (the
     // other is ordered behind it by the turn).
-    const int visible = (CAUSAL ? min((2 * cur.b + 2) * p.tpt, cur.len) : cur.len) - (ch.steps - 1) * kBlockN;
+    const int visible = uniform(it.visible);
     const int zero_rows = min(kBlockN, (visible + 15) & ~15) - visible;
-    const int zero_at = ch.ke == ch.steps && zero_rows > 0 &&
-                                (t == 0 || tiles_for<CAUSAL>(cur.b, 0, cur.len, p.tpt) < ch.steps)
-                            ? ch.steps - 1
-                            : -1;
+    const int zero_at = uniform(ke == it.steps && zero_rows > 0 && (t == 0 || it.ne[0] < ke) ? ke - 1 : -1);
     // keys that some row of this query tile sees: its last tile's products stop there
-    const int seen = CAUSAL ? min((2 * cur.b + t + 1) * p.tpt, cur.len) : cur.len;
+    const int seen = uniform(t ? it.seen[1] : it.seen[0]);
+    __syncwarp();
+    if (leader) mbar_arrive(sy.item_empty0 + 8 * slot);
     if (ne > kb) {
       wait_voted(bar_q_full, q_uses & 1u);
       ++q_uses;
     }
     // step s issues O_t += P_t(s-1) V_{s-1} (if kb <= s-1 < ne) and S_t(s) (if s < ne)
-    for (int s = kb; s <= ch.ke && ok; ++s) {
+    for (int s = kb; s <= ke && ok; ++s) {
       const bool do_pv = s - 1 >= kb && s - 1 < ne;
       const bool do_s = s < ne;
       const uint32_t cv = kv_count + 2 * (s - 1 - kb) + 1;  // V_{s-1}
@@ -326,7 +413,14 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
       // Groups of 16 keys that P V takes.  (Q K^T always takes all 128: with fewer
       // columns it measured slower, and S and P V of one shape are what is known to
       // stay in order.)
-      const int groups_pv = min(kBlockN, seen - (s - 1) * kBlockN + 15) / 16;
+      int groups_pv = min(kBlockN, seen - (s - 1) * kBlockN + 15) / 16;
+      // All of it in registers before the turn, which is what the other issuer
+      // waits for (16384 tokens: 740 us; computed where it is used: 752).
+#pragma unroll
+      for (int kk = 0; kk < C::kPvInstr; ++kk) asm volatile("" : "+l"(dv[kk]));
+#pragma unroll
+      for (int kk = 0; kk < C::kQkInstr; ++kk) asm volatile("" : "+l"(dq[kk]), "+l"(dk[kk]));
+      asm volatile("" : "+r"(groups_pv));
       if (do_pv) {
         if (s == kb + 1) {
           wait_voted(bar_o_free, of_par);
@@ -364,9 +458,9 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
       }
       __syncwarp();
       if (!do_pv && s - 1 >= kb) release_unused(cv);
-      if (!do_s && s < ch.ke) release_unused(ck);
+      if (!do_s && s < ke) release_unused(ck);
     }
-    kv_count += 2 * (ch.ke - kb);
+    kv_count += 2 * (ke - kb);
   }
   // Every MMA this thread issued must finish before tensor memory is released.
   if (leader) umma_commit(sy.drain);
@@ -512,10 +606,10 @@ struct Mend {
 // the warp together on one row.  Only values that are not finite lead here, so
 // it is a call: inlined it cost 24 ragged prompts 3 us of 150.
 template <int D>
-__device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0, const Cursor c, const Chunk ch,
-                                       const Mend mine, const Params& p) {
+__device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0, const Item& c, const Mend mine,
+                                       const Params& p) {
   constexpr int kPer = D / 32;  // columns of a lane
-  const int behind = min(min(2 * (c.b + 1) * p.tpt, c.len), ch.ke * kBlockN);  // V rows from here on were zeroed or not read
+  const int behind = min(min(2 * (c.b + 1) * p.tpt, c.len), c.ke * kBlockN);  // V rows from here on were zeroed or not read
   auto load = [&](const __nv_bfloat16* row, float* x) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] = __bfloat162float(row[lane * kPer + e]);
@@ -528,7 +622,7 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
     const int head = c.h * p.G + quad * 32 + src - in_tile * p.G;
     const __nv_bfloat16* v = p.v + static_cast<long long>(c.begin) * p.v_stride + c.h * D;
     bool need[kPer] = {};
-    for (int key = max(token + 1, ch.kb * kBlockN); key < behind; ++key) {
+    for (int key = max(token + 1, c.kb * kBlockN); key < behind; ++key) {
       float x[kPer];
       load(v + key * p.v_stride, x);
 #pragma unroll
@@ -546,9 +640,9 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     const __nv_bfloat16* k = p.k + static_cast<long long>(c.begin) * p.k_stride + c.h * D;
-    const int to = min(token + 1, ch.ke * kBlockN);
+    const int to = min(token + 1, c.ke * kBlockN);
 #pragma unroll 4
-    for (int key = ch.kb * kBlockN; key < to; ++key) {
+    for (int key = c.kb * kBlockN; key < to; ++key) {
       float x[kPer], y[kPer], dot = 0.f;
       load(k + key * p.k_stride, x);
       load(v + key * p.v_stride, y);
@@ -575,7 +669,7 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
 // Softmax / correction / epilogue warpgroup (128 threads, one row each)
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL>
-__device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy, const Params& p) {
+__device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSync& sy, const Params& p) {
   using C = PackedCfg<D>;
   const int lane = threadIdx.x & 31;
   const int quad = (threadIdx.x >> 5) & 3;  // TMEM lanes 32*quad .. 32*quad+31
@@ -590,35 +684,20 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
   const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
   uint32_t s_par = 0, od_par = 0;
   bool ok = true;
-  // Where the warp is, in shared memory: 128 scores of a row and what the loop
-  // over key tiles needs beside them fill the registers.
-  struct Place {
-    Cursor c;
-    Chunk ch;
-  };
-  static_assert(sizeof(Place) <= 32, "its slot");
-  Place* place = reinterpret_cast<Place*>(shared_base() + C::kCursorOff) + (threadIdx.x >> 5);
-  const Range& r = p.range[blockIdx.x];
-  for (int i = 0; i < r.n_items && ok; ++i) {
-    int ne, kb, first_masked;
-    bool empty;
-    {
-      Cursor c = i == 0 ? Cursor(r, p) : place->c;
-      if (i > 0) c.next(p);
-      const Chunk ch = chunk_of<CAUSAL>(i, c, r, p);
-      __syncwarp();
-      if (lane == 0) *place = Place{c, ch};
-      __syncwarp();
-      kb = ch.kb;
-      ne = min(ch.ke, tiles_for<CAUSAL>(c.b, t, c.len, p.tpt));
-      // a part may have no key tile of this query tile; it still reports its rows, as an empty part
-      empty = ne <= kb;
-      first_masked = (CAUSAL ? min((2 * c.b + t) * p.tpt, c.len - 1) : c.len - 1) / kBlockN;  // key tiles from here on are masked
-      if (!CAUSAL && (c.len & (kBlockN - 1)) == 0) first_masked = ne;
-    }
-    if (i == 1 && r.first.slot >= 0) {
+  uint32_t items = 0;
+  for (bool more = true; more && ok; ++items) {
+    // read from shared memory where it is needed: 128 scores of a row and what the
+    // loop over key tiles needs beside them fill the registers
+    const uint32_t n = items % kItemsAhead;
+    ok = wait_phase(sy.item_full0 + 8 * n, (items / kItemsAhead) & 1u, sy, p);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const Item& it = sy.items[n];
+    const int kb = it.kb;
+    if (it.i == 1 && p.dealt == 0 && p.range[blockIdx.x].first.slot >= 0) {
       // The range's first chunk was a part and has stored its rows; its arrival
       // is made here, while this chunk's first scores are on their way.
+      const Range& r = p.range[blockIdx.x];
       if (part_arrive(p.counters + r.first.k * kCountersPerItem + t * 4 + quad, r.first.count, lane)) {
         const Row row(p.cu[r.s], p.cu[r.s + 1] - p.cu[r.s], r.h, (2 * r.b + t) * p.tpt, row_in_tile, D, p);
         merge_rows<D>(r.first, Own{kStored, 0.f, 0.f, 0u}, t * kBlockM + row_in_tile, row.store, row.o, row.lse,
@@ -644,7 +723,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
         // A masked tile: 32 columns at a time, up to the last that some row of
         // the tile sees; the maximum first, then the exponentials from S read
         // again (P's 16 columns lie over columns of S read before).
-        const int len = place->c.len, t0 = (2 * place->c.b + t) * p.tpt;  // the tile's first token
+        const int len = it.len, t0 = (2 * it.b + t) * p.tpt;  // the tile's first token
         const int lim = (CAUSAL ? min(t0 + row_in_tile / p.G, len - 1) : len - 1) - j * kBlockN;  // the row's last visible key
         const int cols = (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN;
         auto load = [&](int c4, uint32_t* x) {
@@ -792,10 +871,13 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       if (lane == 0) mbar_arrive(bar_p_ready);  // one arrival per warp
     };
     int j = kb;
-    for (const int to = min(ne, first_masked); j < to && ok; ++j) step(std::false_type{}, j);
+    for (const int plain = it.plain[t]; j < plain && ok; ++j) step(std::false_type{}, j);
+    const int ne = it.ne[t];
     for (; j < ne && ok; ++j) step(std::true_type{}, j);
     if (!ok) break;
 
+    // a part may have no key tile of this query tile; it still reports its rows, as an empty part
+    const bool empty = ne <= kb;
     Own own{kEmpty, -INFINITY, 0.f, tO};
     if (!empty) {
       ok = wait_phase(bar_o_done, od_par, sy, p);
@@ -806,21 +888,20 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       // a part may hold no visible key of a row (l = 0): its O is 0 and its logsumexp -inf
       own = Own{kInTmem, (m_ref + log2f(l)) * 0.69314718055994531f, l == 0.f ? 0.f : 1.f / lq, tO};
     }
-    const bool whole = place->ch.whole();
-    if (whole && empty) continue;
-    const Cursor c = place->c;
-    const Row row(c.begin, c.len, c.h, (2 * c.b + t) * p.tpt, row_in_tile, D, p);
+    const bool whole = it.whole();
+    const Row row(it.begin, it.len, it.h, (2 * it.b + t) * p.tpt, row_in_tile, D, p);
     // whether the chunk's last V tiles held keys that some of the item's rows do not see
-    const bool masked = CAUSAL && !empty && place->ch.ke > 2 * c.b * p.tpt / kBlockN;
+    const bool masked = CAUSAL && !empty && it.ke > 2 * it.b * p.tpt / kBlockN;
     if (!whole) {
-      const Part part = i == 0 ? r.first : r.last;
+      const Range& r = p.range[blockIdx.x];
+      const Part part = it.i == 0 ? r.first : r.last;
       const int r_item = t * kBlockM + row_in_tile;  // row within the item, and its slot
       // The end of a chunk that is a part: where every other part is in already
       // (as a rule for the range's last chunk, whose item's other parts were
       // other CTAs' first work), the warp merges from where its rows are;
       // else it stores them and arrives.
       int* ctr = p.counters + part.k * kCountersPerItem + t * 4 + quad;
-      bool merge = (i > 0 || r.n_items == 1) && __all_sync(0xffffffffu, ld_acquire_gpu(ctr) == part.count - 1);
+      bool merge = (it.i > 0 || !it.more) && __all_sync(0xffffffffu, ld_acquire_gpu(ctr) == part.count - 1);
       bool store = !merge;
 #pragma unroll 1
       for (;;) {
@@ -841,13 +922,13 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
             }
             const uint32_t rows = __ballot_sync(0xffffffffu, row.store && is_nan(top));
             if (masked && rows != 0)
-              mend_rows<D>(rows, lane, quad, (2 * c.b + t) * p.tpt, c, place->ch,
+              mend_rows<D>(rows, lane, quad, (2 * it.b + t) * p.tpt, it,
                            Mend{nullptr, p.part_o + part_index<D>(part.slot, r_item, 0), m_ref, own.inv_l}, p);
           }
           p.part_lse[static_cast<size_t>(part.slot) * kItemRows + r_item] = own.lse;
           own.where = kStored;
           // merged already, but for NaN rows; or arrive (in the range's first chunk: with the next one)
-          if (!merge && (i > 0 || r.n_items == 1)) merge = part_arrive(ctr, part.count, lane);
+          if (!merge && (it.i > 0 || !it.more)) merge = part_arrive(ctr, part.count, lane);
         }
         if (!merge) break;
         __syncwarp();
@@ -856,7 +937,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
         store = masked && own.where == kInTmem && __any_sync(0xffffffffu, row.store && is_nan(top));
         if (!store) break;
       }
-    } else {
+    } else if (!empty) {
       uint32_t top = 0;  // NaN where an element of the row is
       const uint64_t il2 = f2_pack(own.inv_l, own.inv_l);
       auto to_bf16 = [&](const uint32_t* o) {  // two elements of the row
@@ -922,13 +1003,15 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const Sync& sy
       if (CAUSAL) {
         const uint32_t rows = __ballot_sync(0xffffffffu, row.store && ((top & 0x7fffu) > 0x7f80u || (top & 0x7fff0000u) > 0x7f800000u));
         if (rows != 0)
-          mend_rows<D>(rows, lane, quad, (2 * c.b + t) * p.tpt, c, place->ch, Mend{row.o, nullptr, m_ref, own.inv_l}, p);
+          mend_rows<D>(rows, lane, quad, (2 * it.b + t) * p.tpt, it, Mend{row.o, nullptr, m_ref, own.inv_l}, p);
       }
     }
-    if (!empty) {
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_o_free);  // one arrival per warp
+    more = it.more;
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {  // one arrival per warp
+      if (!empty) mbar_arrive(bar_o_free);
+      mbar_arrive(sy.item_empty0 + 8 * n);
     }
   }
 }
@@ -946,7 +1029,7 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  Sync sy;
+  PackedSync sy;
   {
     uint32_t b = sbase + C::kBarOff;
     auto take = [&](int n) {
@@ -964,7 +1047,11 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int t = 0; t < 2; ++t) sy.o_free[t] = take(1);
     sy.drain = take(1);
     for (int t = 0; t < 2; ++t) sy.turn[t] = take(1);
+    sy.item_full0 = take(kItemsAhead);
+    sy.item_empty0 = take(kItemsAhead);
   }
+  Item* items = reinterpret_cast<Item*>(smem + C::kItemsOff);
+  sy.items = items;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   sy.abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
 
@@ -983,6 +1070,10 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(sy.kv_empty0 + 8 * s, 2);  // released by both MMA issuers
     }
     mbar_init(sy.drain, 2);
+    for (int n = 0; n < kItemsAhead; ++n) {
+      mbar_init(sy.item_full0 + 8 * n, 1);
+      mbar_init(sy.item_empty0 + 8 * n, 1 + 2 + 8);  // the producer, the issuers, the softmax warps
+    }
     *sy.abort_flag = 0;
     fence_barrier_init();
   }
@@ -1007,6 +1098,9 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       run_mma<D, CAUSAL>(warp - kMmaWarp, smem, sbase, tmem, sy, p);
+      __syncwarp();
+    } else {
+      if (lane == 0) run_dispatcher<CAUSAL>(items, sy, p);
       __syncwarp();
     }
   } else {

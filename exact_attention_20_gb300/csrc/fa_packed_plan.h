@@ -1,5 +1,6 @@
-// Work division of the packed forward, on the host: the concatenated items of
-// one launch cut into contiguous ranges of about equal cost, one per CTA.
+// Work division of the packed forward, on the host: the items of one launch
+// dealt out by length, or their concatenation cut into contiguous ranges of
+// about equal cost, one per CTA.
 #pragma once
 
 #include "fa_packed_kernel.cuh"
@@ -16,27 +17,93 @@ constexpr int kMinPartSteps = 8;
 // With no more items than CTAs, items are cut only while every CTA keeps this
 // many steps.
 constexpr int kMinStepsPerCta = 16;
+// Long items are dealt where the CTA with the most work has at most so many
+// steps more than its equal share; cutting them leaves an overhead like that.
+// A prompt of 4096 tokens at 8 KV heads, 4 query heads each: 109 us dealt, 127
+// cut; 8192 tokens at 2 heads, where the excess is 8 steps: 120 and 121.
+constexpr int kDealtSlack = 8;
 
-// Sequences cu[0..n] (n <= kMaxSeqs): fills p.range and returns the grid; the
-// number of workspace slots and of split items go to n_slots and n_split.
+// Fills p.pair with the pairs of all sequences, those with the most steps first.
+template <bool CAUSAL>
+inline void deal(int n, int tpt, int longest, Params& p) {
+  // Pairs of each number of steps, then where the next one goes.  A block has
+  // 2 tpt <= 256 tokens, a step 128: kMaxPairs blocks make at most so many.
+  int at[2 * kMaxPairs + 1];
+  for (int steps = 0; steps <= longest; ++steps) at[steps] = 0;
+  auto each = [&](auto&& f) {
+    for (int s = 0; s < n; ++s) {
+      const int len = p.cu[s + 1] - p.cu[s];
+      for (int b = 0; b * 2ll * tpt < len; ++b) f(s, b, item_steps<CAUSAL>(b, len, tpt));
+    }
+  };
+  each([&](int, int, int steps) { ++at[steps]; });
+  for (int steps = longest, next = 0; steps >= 0; --steps) {
+    const int k = at[steps];
+    at[steps] = next;
+    next += k;
+  }
+  each([&](int s, int b, int steps) { p.pair[at[steps]++] = Pair{static_cast<uint16_t>(s), static_cast<uint16_t>(b)}; });
+}
+
+// The most work that a CTA of a dealt launch gets.
+template <bool CAUSAL>
+inline long long most_dealt(int items, int Hkv, int tpt, int grid, const Params& p) {
+  long long load[kMaxCtas] = {}, top = 0;
+  int cta = 0, by = 1, pair = 0, left = 0, w = 0;
+  for (int i = 0; i < items; ++i, --left) {
+    if (left == 0) {
+      const Pair x = p.pair[pair++];
+      w = item_steps<CAUSAL>(x.b, p.cu[x.s + 1] - p.cu[x.s], tpt) + kItemCost;
+      left = Hkv;
+    }
+    load[cta] += w;
+    cta += by;
+    if (cta < 0 || cta == grid) {  // the next row goes back
+      cta -= by;
+      by = -by;
+    }
+  }
+  for (int c = 0; c < grid; ++c) top = load[c] > top ? load[c] : top;
+  return top;
+}
+
+// Sequences cu[0..n] (n <= kMaxSeqs): fills p.pair or p.range and returns the
+// grid; the number of workspace slots and of split items go to n_slots and
+// n_split.
 template <bool CAUSAL>
 inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_slots, int& n_split) {
-  n_slots = n_split = 0;
+  n_slots = n_split = p.dealt = 0;
   const int most = num_ctas < kMaxCtas ? num_ctas : kMaxCtas;
-  long long weight = 0, items = 0;
-  int longest = 0;
+  long long weight = 0, pairs = 0;
+  int longest = 0, shortest = 1 << 30;
   for (int s = 0; s < n; ++s) {
     const int len = p.cu[s + 1] - p.cu[s];
     long long w = 0, k = 0;
     for (int b = 0; b * 2ll * tpt < len; ++b, ++k) {
       const int steps = item_steps<CAUSAL>(b, len, tpt);
       longest = steps > longest ? steps : longest;
+      shortest = steps < shortest ? steps : shortest;
       w += steps + kItemCost;
     }
     weight += w * Hkv;
-    items += k * Hkv;
+    pairs += k;
   }
+  const long long items = pairs * Hkv;
   if (items == 0) return 0;
+  // Items too short to be cut are dealt where they differ (24 ragged prompts,
+  // up to 15 steps: 121 us, 147 in contiguous ranges; items of one length are
+  // as even in ranges), long ones where the CTA with the most work has little
+  // more than its share.
+  if (items > most && shortest < longest && pairs <= kMaxPairs && items < (1 << 30)) {
+    const bool short_items = longest < 2 * kMinPartSteps;
+    if (short_items || (longest + kItemCost) * static_cast<long long>(most) <= weight) {
+      deal<CAUSAL>(n, tpt, longest, p);
+      if (short_items || most_dealt<CAUSAL>(static_cast<int>(items), Hkv, tpt, most, p) <= weight / most + kDealtSlack) {
+        p.dealt = static_cast<int>(items);
+        return most;
+      }
+    }
+  }
   long long ctas = items;
   if (ctas < most) {
     const long long by_work = weight / kMinStepsPerCta;
