@@ -140,6 +140,23 @@ def test_split_items(serve, lens, hq, hkv, causal):
     check(serve, lens, hq, hkv, 128, causal, seed=4)
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d,causal", [
+    ([1800, 3, 0, 900, 700, 1, 1500], 8, 8, 128, True),          # short items of many lengths
+    ([1800, 3, 0, 900, 700, 1, 1500], 16, 8, 128, False),
+    ([300, 1, 1999, 0, 40] * 4, 12, 4, 64, True),
+    ([4096], 32, 32, 64, True),                                  # long ones, even without a cut
+    ([6000, 100], 16, 1, 64, True),
+    ([(37 * i) % 500 + 450 for i in range(110)], 8, 1, 64, True),  # more blocks than are dealt
+])
+def test_more_items_than_ctas(serve, lens, hq, hkv, d, causal):
+    import ctypes
+    arr = (ctypes.c_int * len(lens))(*lens)
+    need = ctypes.c_size_t(1)
+    rc = serve.lib().fa_fwd_packed_workspace(arr, len(lens), sum(lens), hq, hkv, d, int(causal), ctypes.byref(need))
+    assert rc == 0 and need.value == 0, "no item is cut"
+    check(serve, lens, hq, hkv, d, causal, seed=8)
+
+
 def test_more_sequences_than_one_launch_takes(serve):
     lens = [(i * 7) % 13 for i in range(2500)]
     check(serve, lens, 4, 2, 64, True, seed=5)
