@@ -28,6 +28,17 @@
 //   replaced by -inf; P is 0 there, but 0 * NaN is NaN: the V rows past the
 //   item's last visible key are zeroed in shared memory, and a row that comes
 //   out NaN under the mask is looked at again (mend_rows).
+//
+// Warps: 0-7 softmax, one row a thread; 8 TMA; 9 and 10 MMA; 11 dispatcher.
+// Measured on a GB300: 16384 tokens, 2 KV heads of 8 query heads, d = 128,
+// causal, 740-750 us: 1475 TFLOP/s of visible products, 77 % of cuBLAS' bf16
+// rate; 24 prompts of 40 to 1901 tokens, 32 / 8 heads, 121 us (55 at that
+// rate; two products of 256 rows and the softmax between them are 1.7 us a
+// step, an item's start and end 3.6 us).  What bounds long prompts is the
+// turn from S to P and back in a tile's softmax warps: the tensor pipe is
+// active 62 % of the time, issue slots are 47 % used.  Without a mask at d =
+// 64, 8 x 1024 tokens of 16 heads take 62 us: 134 M exponentials, 27 us of
+// the MUFU's rate, in 3.4 rounds of items that cost four.
 #pragma once
 
 #include <type_traits>
