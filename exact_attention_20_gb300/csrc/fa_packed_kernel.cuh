@@ -37,7 +37,7 @@
 // step, an item's start and end 3.6 us).  What bounds long prompts is the
 // turn from S to P and back in a tile's softmax warps: the tensor pipe is
 // active 62 % of the time, issue slots are 47 % used.  Without a mask at d =
-// 64, 8 x 1024 tokens of 16 heads take 62 us: 134 M exponentials, 27 us of
+// 64, 8 x 1024 tokens of 16 heads take 59 us: 134 M exponentials, 27 us of
 // the MUFU's rate, in 3.4 rounds of items that cost four.
 #pragma once
 
@@ -66,12 +66,18 @@ struct PackedCfg {
   static constexpr int kSlabs = Cfg<D>::kSlabs, kTileBytes = Cfg<D>::kTileBytes;
   static constexpr int kQkInstr = Cfg<D>::kQkInstr, kPvInstr = Cfg<D>::kPvInstr;
   static constexpr int kStages = D == 128 ? 4 : 9;
+  // P in two halves: the product with V's first 64 keys starts while the other
+  // half's exponentials are taken.  8 x 1024 tokens of 16 heads at d = 64 without
+  // a mask: 59 us, 62 in one piece.  At d = 128, where the tensor core has twice
+  // the work, an issuer that holds its turn between the halves is in the other's
+  // way: 16384 tokens 823 us, 744 in one piece.
+  static constexpr bool kHalves = D == 64;
   static constexpr int kQOff = 0;
   static constexpr int kKVOff = kQTiles * kTileBytes;
   static constexpr int kOutOff = kKVOff + kStages * kTileBytes;
   static constexpr int kWarpOut = 32 * 128;
   static constexpr int kBarOff = kOutOff + (D == 128 ? 8 * kWarpOut : 0);
-  static constexpr int kNumBars = 2 * 2 + 2 * kStages + 2 * 4 + 1 + 2 + 2 * kItemsAhead;
+  static constexpr int kNumBars = 2 * 2 + 2 * kStages + 2 * 5 + 1 + 2 + 2 * kItemsAhead;
   static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kItemsOff = kMiscOff + 16;
   static constexpr int kSmemBytes = kItemsOff + kItemsAhead * 64 + 1024;  // + alignment slack
@@ -203,6 +209,7 @@ struct alignas(16) Item {
 static_assert(sizeof(Item) == 64, "kItemsOff");
 
 struct PackedSync : Sync {
+  uint32_t p_half[2];  // kHalves: as p_ready, for P's first 64 keys
   uint32_t item_full0, item_empty0;
   const Item* items;
 };
@@ -334,6 +341,7 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
   const uint32_t bar_q_empty = t ? sy.q_empty[1] : sy.q_empty[0];
   const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
   const uint32_t bar_p_ready = t ? sy.p_ready[1] : sy.p_ready[0];
+  const uint32_t bar_p_half = t ? sy.p_half[1] : sy.p_half[0];
   const uint32_t bar_o_done = t ? sy.o_done[1] : sy.o_done[0];
   const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
   const uint32_t my_turn = t ? sy.turn[1] : sy.turn[0];
@@ -437,25 +445,41 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
           wait_voted(bar_o_free, of_par);
           of_par ^= 1u;
         }
-        wait_voted(bar_p_ready, pr_par);
-        pr_par ^= 1u;
+        wait_voted(C::kHalves ? bar_p_half : bar_p_ready, pr_par);
+        if constexpr (!C::kHalves) pr_par ^= 1u;
       }
       wait_voted(my_turn, turn_par);
       turn_par ^= 1u;
       if (!ok) break;
       tc_fence_after_sync();
-      if (leader) {
-        if (do_pv) {
-          constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, /*b_mn_major=*/true);
-          if (groups_pv == C::kPvInstr) {
+      // P V's instructions [FROM, TO), as far as some row sees
+      auto issue_pv = [&](auto from, auto to) {
+        constexpr int kFrom = decltype(from)::value, kTo = decltype(to)::value;
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, /*b_mn_major=*/true);
+        if (groups_pv >= kTo) {
 #pragma unroll
-            for (int kk = 0; kk < C::kPvInstr; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
-          } else {
+          for (int kk = kFrom; kk < kTo; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+        } else {
 #pragma unroll
-            for (int kk = 0; kk < C::kPvInstr - 1; ++kk)
-              if (kk < groups_pv) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
-          }
+          for (int kk = kFrom; kk < kTo - 1; ++kk)
+            if (kk < groups_pv) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
         }
+      };
+      using Begin = std::integral_constant<int, 0>;
+      using Half = std::integral_constant<int, C::kHalves ? C::kPvInstr / 2 : 0>;
+      using End = std::integral_constant<int, C::kPvInstr>;
+      if constexpr (C::kHalves) {
+        if (do_pv) {
+          if (leader) issue_pv(Begin{}, Half{});
+          __syncwarp();
+          wait_voted(bar_p_ready, pr_par);
+          pr_par ^= 1u;
+          if (!ok) break;
+          tc_fence_after_sync();
+        }
+      }
+      if (leader) {
+        if (do_pv) issue_pv(Half{}, End{});
         if (do_s) {
 #pragma unroll
           for (int kk = 0; kk < C::kQkInstr; ++kk) umma_ss(tm_s, dq[kk], dk[kk], idesc_qk, kk > 0 ? 1u : 0u);
@@ -691,6 +715,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
   const float qk = p.qk_scale;
   const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
   const uint32_t bar_p_ready = t ? sy.p_ready[1] : sy.p_ready[0];
+  const uint32_t bar_p_half = t ? sy.p_half[1] : sy.p_half[0];
   const uint32_t bar_o_done = t ? sy.o_done[1] : sy.o_done[0];
   const uint32_t bar_o_free = t ? sy.o_free[1] : sy.o_free[0];
   uint32_t s_par = 0, od_par = 0;
@@ -727,10 +752,39 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
       s_par ^= 1u;
       tc_fence_after_sync();
 
+      constexpr bool kMasked = decltype(masked_tile)::value;
       const uint64_t qk2 = f2_pack(qk, qk);
       float alpha = 1.f;
       float sa, sb, lq_tile;
-      if constexpr (decltype(masked_tile)::value) {
+      // O_t holds the sum up to tile j-1: brought to the new reference, 32
+      // columns at a time where the tile's scores are still in registers
+      auto rescale = [&]() {
+        if (j == kb || !__any_sync(0xffffffffu, alpha != 1.f)) return;
+        const uint64_t a2 = f2_pack(alpha, alpha);
+        constexpr int kCols = C::kHalves ? 32 : 64, kUnroll = C::kHalves ? 1 : 2;
+#pragma unroll kUnroll
+        for (int e = 0; e < D / kCols; ++e) {
+          uint32_t o[kCols];
+          if constexpr (kCols == 64) tmem_ld64_wait(tO + e * 64, o);
+          else tmem_ld32_wait(tO + e * 32, o);
+#pragma unroll
+          for (int n = 0; n < kCols / 2; ++n) {
+            float lo, hi;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1])), a2), lo, hi);
+            o[2 * n] = __float_as_uint(lo);
+            o[2 * n + 1] = __float_as_uint(hi);
+          }
+#pragma unroll
+          for (int n = 0; n < kCols; n += 32) tmem_st32(tO + e * kCols + n, o + n);
+        }
+      };
+      auto hand_over = [&](uint32_t bar) {
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);  // one arrival per warp
+      };
+      if constexpr (kMasked) {
         // A masked tile: 32 columns at a time, up to the last that some row of
         // the tile sees; the maximum first, then the exponentials from S read
         // again (P's 16 columns lie over columns of S read before).
@@ -807,6 +861,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
               if (with_max) mx[c4] = fmax3(mx[c4], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             }
             tmem_st16(tS + c4 * 16, pk);
+            if (C::kHalves && c4 == 1) hand_over(bar_p_half);
           }
           f2_unpack(sum2, sa, sb);
           lq_tile = (lqs[0] + lqs[1]) + (lqs[2] + lqs[3]);
@@ -827,13 +882,15 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
           for (int q4 = 0; q4 < 4; ++q4) mx[q4] = fmaxf(mx[q4], __uint_as_float(s[32 * q4 + 31]));
           return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * qk;
         };
-        if constexpr (CAUSAL) {
-          // the maximum first, then one pass (faster under the mask, with its many first tiles)
+        if constexpr (CAUSAL || C::kHalves) {
+          // the maximum first, then one pass (faster under the mask, with its many first tiles;
+          // and where the first half of P goes to its product before the second is known)
           const float m_tile = row_max();
           if (m_tile > m_ref + kRescaleThreshold<2>) {
             alpha = ex2_approx(m_ref - m_tile);  // 0 when m_ref = -inf
             m_ref = m_tile;
           }
+          if (C::kHalves) rescale();
           exp_pass(m_ref == -INFINITY ? 0.f : m_ref, false);  // 0: no key of this part visible yet, P = 0
         } else {
           // the exponentials against the current reference while the tile's
@@ -858,28 +915,9 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
       l = l * alpha + (sa + sb);
       lq = lq * alpha + lq_tile;
 
-      if (j > kb && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O_t holds the sum up to tile j-1: bring it to the new reference
-        const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          uint32_t o[64];
-          tmem_ld64_wait(tO + e * 64, o);
-#pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            float lo, hi;
-            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1])), a2), lo, hi);
-            o[2 * n] = __float_as_uint(lo);
-            o[2 * n + 1] = __float_as_uint(hi);
-          }
-          tmem_st32(tO + e * 64, o);
-          tmem_st32(tO + e * 64 + 32, o + 32);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p_ready);  // one arrival per warp
+      if (!C::kHalves || kMasked) rescale();
+      if (C::kHalves && kMasked) hand_over(bar_p_half);
+      hand_over(bar_p_ready);
     };
     int j = kb;
     for (const int plain = it.plain[t]; j < plain && ok; ++j) step(std::false_type{}, j);
@@ -1058,6 +1096,7 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int t = 0; t < 2; ++t) sy.o_free[t] = take(1);
     sy.drain = take(1);
     for (int t = 0; t < 2; ++t) sy.turn[t] = take(1);
+    for (int t = 0; t < 2; ++t) sy.p_half[t] = take(1);
     sy.item_full0 = take(kItemsAhead);
     sy.item_empty0 = take(kItemsAhead);
   }
@@ -1072,6 +1111,7 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(sy.q_empty[t], 1);
       mbar_init(sy.s_full[t], 1);
       mbar_init(sy.p_ready[t], kBlockM / 32);
+      mbar_init(sy.p_half[t], kBlockM / 32);
       mbar_init(sy.o_done[t], 1);
       mbar_init(sy.o_free[t], kBlockM / 32);
       mbar_init(sy.turn[t], 1);
