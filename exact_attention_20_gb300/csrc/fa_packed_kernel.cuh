@@ -796,12 +796,16 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
         // again (P's 16 columns lie over columns of S read before).
         const int len = it.len, t0 = (2 * it.b + t) * p.tpt;  // the tile's first token
         const int lim = (CAUSAL ? min(t0 + row_in_tile / p.G, len - 1) : len - 1) - j * kBlockN;  // the row's last visible key
-        const int cols = (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN;
+        const int cols = min(kBlockN, (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN);
+        const int all = CAUSAL ? __reduce_min_sync(0xffffffffu, lim) : lim;
+        const int any = min(cols - 1, CAUSAL ? __reduce_max_sync(0xffffffffu, lim) : lim);
         auto load = [&](int c4, uint32_t* x) {
           tmem_ld32_wait(tS + c4 * 32, x);
+          if (c4 * 32 + 31 > all) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c4 * 32 + e > lim) x[e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e)
+              if (c4 * 32 + e > lim) x[e] = __float_as_uint(-INFINITY);
+          }
         };
         float m_tile = -INFINITY;
 #pragma unroll 1
