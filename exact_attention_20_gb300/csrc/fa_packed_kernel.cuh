@@ -31,10 +31,10 @@
 //
 // Warps: 0-7 softmax, one row a thread; 8 TMA; 9 and 10 MMA; 11 dispatcher.
 // Measured on a GB300: 16384 tokens, 2 KV heads of 8 query heads, d = 128,
-// causal, 740-750 us: 1475 TFLOP/s of visible products, 77 % of cuBLAS' bf16
-// rate; 24 prompts of 40 to 1901 tokens, 32 / 8 heads, 121 us (55 at that
-// rate; two products of 256 rows and the softmax between them are 1.7 us a
-// step, an item's start and end 3.6 us).  What bounds long prompts is the
+// causal, 735-745 us: 1485 TFLOP/s of visible products, 78 % of cuBLAS' bf16
+// rate; 24 prompts of 40 to 1901 tokens, 32 / 8 heads, 118 us (55 at that
+// rate; two products of 256 rows and the softmax between them are 1.6 us a
+// step, an item's start and end 3.5 us).  What bounds long prompts is the
 // turn from S to P and back in a tile's softmax warps: the tensor pipe is
 // active 62 % of the time, issue slots are 47 % used.  Without a mask at d =
 // 64, 8 x 1024 tokens of 16 heads take 59 us: 134 M exponentials, 27 us of
@@ -796,9 +796,10 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
         // again (P's 16 columns lie over columns of S read before).
         const int len = it.len, t0 = (2 * it.b + t) * p.tpt;  // the tile's first token
         const int lim = (CAUSAL ? min(t0 + row_in_tile / p.G, len - 1) : len - 1) - j * kBlockN;  // the row's last visible key
-        const int cols = min(kBlockN, (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN);
-        const int all = CAUSAL ? __reduce_min_sync(0xffffffffu, lim) : lim;
-        const int any = min(cols - 1, CAUSAL ? __reduce_max_sync(0xffffffffu, lim) : lim);
+        const int cols = (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN;
+        const int all = CAUSAL ? __reduce_min_sync(0xffffffffu, lim) : lim;  // what every row of the warp sees
+        // Only columns that some row of the warp does not see are compared (24
+        // ragged prompts 118 us, with all compared 121).
         auto load = [&](int c4, uint32_t* x) {
           tmem_ld32_wait(tS + c4 * 32, x);
           if (c4 * 32 + 31 > all) {
