@@ -23,6 +23,14 @@ constexpr int kMinStepsPerCta = 16;
 // cut; 8192 tokens at 2 heads, where the excess is 8 steps: 120 and 121.
 constexpr int kDealtSlack = 8;
 
+// item_steps in one step, for the loops over all blocks: the last query tile
+// that has tokens visits the most key tiles.
+template <bool CAUSAL>
+inline int plan_steps(int b, int len, int tpt) {
+  const int end = (2 * b + 2) * tpt;
+  return ((CAUSAL && end < len ? end : len) - 1) / kBlockN + 1;
+}
+
 // Fills p.pair with the pairs of all sequences, those with the most steps first.
 template <bool CAUSAL>
 inline void deal(int n, int tpt, int longest, Params& p) {
@@ -33,7 +41,7 @@ inline void deal(int n, int tpt, int longest, Params& p) {
   auto each = [&](auto&& f) {
     for (int s = 0; s < n; ++s) {
       const int len = p.cu[s + 1] - p.cu[s];
-      for (int b = 0; b * 2ll * tpt < len; ++b) f(s, b, item_steps<CAUSAL>(b, len, tpt));
+      for (int b = 0; b * 2ll * tpt < len; ++b) f(s, b, plan_steps<CAUSAL>(b, len, tpt));
     }
   };
   each([&](int, int, int steps) { ++at[steps]; });
@@ -53,7 +61,7 @@ inline long long most_dealt(int items, int Hkv, int tpt, int grid, const Params&
   for (int i = 0; i < items; ++i, --left) {
     if (left == 0) {
       const Pair x = p.pair[pair++];
-      w = item_steps<CAUSAL>(x.b, p.cu[x.s + 1] - p.cu[x.s], tpt) + kItemCost;
+      w = plan_steps<CAUSAL>(x.b, p.cu[x.s + 1] - p.cu[x.s], tpt) + kItemCost;
       left = Hkv;
     }
     load[cta] += w;
@@ -80,7 +88,7 @@ inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_sl
     const int len = p.cu[s + 1] - p.cu[s];
     long long w = 0, k = 0;
     for (int b = 0; b * 2ll * tpt < len; ++b, ++k) {
-      const int steps = item_steps<CAUSAL>(b, len, tpt);
+      const int steps = plan_steps<CAUSAL>(b, len, tpt);
       longest = steps > longest ? steps : longest;
       shortest = steps < shortest ? steps : shortest;
       w += steps + kItemCost;
@@ -117,12 +125,24 @@ inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_sl
   int grid = 0;             // ranges closed so far
   bool open = false;        // p.range[grid] has a first chunk
   long long cut = 1, at = 0;
+  long long next = weight / ctas;  // where cut lies
   for (int s = 0; s < n; ++s) {
     const int len = p.cu[s + 1] - p.cu[s];
     for (int h = 0; h < Hkv; ++h) {
       for (int b = 0; b * 2ll * tpt < len; ++b) {
-        const int steps = item_steps<CAUSAL>(b, len, tpt);
+        const int steps = plan_steps<CAUSAL>(b, len, tpt);
         const long long w = steps + kItemCost;
+        if (next >= at + w || cut >= ctas) {  // the usual case: no cut in it
+          Range& r = p.range[grid];
+          if (!open) {
+            r = Range{s, h, b, 0, 0, 0, Part{-1, 0, 0, 0}, Part{-1, 0, 0, 0}};
+            open = true;
+          }
+          ++r.n_items;
+          r.step_end = steps;
+          at += w;
+          continue;
+        }
         // this item's parts: their ranges, patched when their number is known
         int part_range[kMaxParts];
         bool part_first[kMaxParts];
@@ -145,8 +165,8 @@ inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_sl
           }
           done = to;
         };
-        for (; cut < ctas && weight * cut / ctas < at + w; ++cut) {
-          const int off = static_cast<int>(weight * cut / ctas - at) - kItemCost / 2;
+        for (; cut < ctas && next < at + w; next = weight * ++cut / ctas) {
+          const int off = static_cast<int>(next - at) - kItemCost / 2;
           int step = off < 0 ? 0 : off > steps ? steps : off;
           if (steps < 2 * kMinPartSteps) step = 2 * step < steps ? 0 : steps;
           if (step - done < kMinPartSteps) step = done;
