@@ -60,6 +60,11 @@ def _checked(rc: int) -> None:
         raise FAError(rc)
 
 
+# what torch.cuda.current_stream and current_device ask, without the objects they make
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 class _Target:
     """The device and stream of one call: ``with _Target(...) as handle`` makes them current.
 
@@ -74,8 +79,9 @@ class _Target:
             raise ValueError("tensors must be on a CUDA device")
         self.context = self.stream = self.other = None
         if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
-            if torch._C._cuda_getDevice() != device.index:
+            index = device.index
+            self.handle = _raw_stream(index)
+            if _current_device() != index:
                 self.context = torch.cuda.device(device)
             return
         if not isinstance(stream, torch.cuda.Stream):
@@ -113,7 +119,7 @@ class _Target:
 
 def _check(name, t, dtype, shape, device) -> None:
     """fa._check, with the usual case decided in one expression."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
             and t.is_contiguous()):
         fa._check(name, t, dtype, shape, device)
 
@@ -126,7 +132,7 @@ def _check_tokens(name, t, heads, d, device, tokens) -> int:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must have shape {(tokens, heads, d)}, got {tuple(t.shape)}")
-    if t.device != device:
+    if t.get_device() != device.index and t.device != device:  # (a CPU tensor's are -1 and None)
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     token, head, element = t.stride()
     if tokens == 0:
