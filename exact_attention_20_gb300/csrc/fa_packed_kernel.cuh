@@ -636,12 +636,14 @@ struct Row {
 struct Mend {
   __nv_bfloat16* o;  // the row in O, or null
   float* part;       // the row's first group in the workspace, groups kItemRows * 8 apart
-  float m_ref, inv_l;
+  float m_ref, inv_l;  // inv_l = 0: no visible score above -inf
 };
 
-// Rows with NaN among their columns, stored by their warp: a NaN that comes
-// from keys that the row does not see (0 * NaN or 0 * infinity in the product
-// with P) is replaced by what the visible keys give.  A column needs that
+// Rows with NaN among their columns, stored by their warp.  A row without
+// weight is 0 whatever V holds: zeros in O; of a part nothing, since the merge
+// leaves a part of weight 0 out.  In the others a NaN that comes from keys
+// that the row does not see (0 * NaN or 0 * infinity in the product with P) is
+// replaced by what the visible keys give.  A column needs that
 // where V is not finite at a key behind the row's token within the chunk's
 // tiles; its sum over the chunk's visible keys is then taken anew, key by key,
 // the warp together on one row.  Only values that are not finite lead here, so
@@ -661,6 +663,15 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
     rows &= rows - 1;
     const int in_tile = (quad * 32 + src) / p.G, token = t0 + in_tile;
     const int head = c.h * p.G + quad * 32 + src - in_tile * p.G;
+    const float m_ref = __shfl_sync(0xffffffffu, mine.m_ref, src), inv_l = __shfl_sync(0xffffffffu, mine.inv_l, src);
+    const unsigned long long o = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.o), src);
+    const unsigned long long part = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.part), src);
+    if (inv_l == 0.f) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (o != 0) reinterpret_cast<__nv_bfloat16*>(o)[lane * kPer + e] = __float2bfloat16_rn(0.f);
+      continue;
+    }
     const __nv_bfloat16* v = p.v + static_cast<long long>(c.begin) * p.v_stride + c.h * D;
     bool need[kPer] = {};
     for (int key = max(token + 1, c.kb * kBlockN); key < behind; ++key) {
@@ -672,9 +683,6 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
     bool any = false;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) any |= need[e];
-    const float m_ref = __shfl_sync(0xffffffffu, mine.m_ref, src), inv_l = __shfl_sync(0xffffffffu, mine.inv_l, src);
-    const unsigned long long o = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.o), src);
-    const unsigned long long part = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.part), src);
     if (!__any_sync(0xffffffffu, any)) continue;
     float q[kPer], acc[kPer];
     load(p.q + (c.begin + token) * p.q_stride + static_cast<long long>(head) * D, q);
@@ -1060,10 +1068,16 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
         }
       }
       if (row.store) *row.lse = own.lse;
-      if (CAUSAL) {
+      if constexpr (CAUSAL) {
         const uint32_t rows = __ballot_sync(0xffffffffu, row.store && ((top & 0x7fffu) > 0x7f80u || (top & 0x7fff0000u) > 0x7f800000u));
         if (rows != 0)
           mend_rows<D>(rows, lane, quad, (2 * it.b + t) * p.tpt, it, Mend{row.o, nullptr, m_ref, own.inv_l}, p);
+      } else if (__any_sync(0xffffffffu, own.inv_l == 0.f)) {
+        // a row without weight is 0 whatever V holds; NaN is right in any other, since it sees all of V
+        if (row.store && own.inv_l == 0.f) {
+#pragma unroll 1
+          for (int n = 0; n < D / 8; ++n) reinterpret_cast<uint4*>(row.o)[n] = make_uint4(0, 0, 0, 0);
+        }
       }
     }
     more = it.more;

@@ -51,11 +51,14 @@ extern "C" {
  *   causal  : 1 = a token sees its sequence up to itself; 0 = all of it.
  *   scale   : as for fa_fwd.
  *
- * A row whose visible scores are all -inf gets O = 0 and LSE = -inf.  P is
- * rounded to bf16 before P.V, every sum is fp32, O is rounded once.  What a
- * row does not see, other sequences and (causal) later tokens, does not reach
- * it even where that holds NaN or infinities.  One launch per 1024 sequences, with a memset of the
- * workspace's counters before it where items are split between CTAs.
+ * A row whose visible scores are all -inf gets O = 0 and LSE = -inf, whatever
+ * V holds.  (In any other row NaN or an infinity in the value of a visible key
+ * whose score is -inf may reach O or not: 0 * NaN in a product, or left out
+ * with a part of weight 0.)  P is rounded to bf16 before P.V, every sum is
+ * fp32, O is rounded once.  What a row does not see, other sequences and
+ * (causal) later tokens, does not reach it even where that holds NaN or
+ * infinities.  One launch per 1024 sequences, with a memset of the workspace's
+ * counters before it where items are split between CTAs.
  * Results do not depend on timing: two calls give the same bits.
  *
  * Returns FA_OK (also when there is no token to do), FA_ERR_INVALID_ARG,

@@ -252,3 +252,58 @@ def test_scores_that_are_all_minus_infinity(serve):
     o, lse = serve.attention_packed(q, k, v, [50])
     assert torch.isneginf(lse[0, :20]).all() and (o[:20] == 0).all()
     assert torch.isfinite(lse[0, 20:]).all() and torch.equal(o[20:, 0].float(), v[20, 0].float().expand(30, -1))
+
+
+def rows_without_weight(serve, lens, hq, hkv, d, causal, none, bad, seed):
+    """The keys before `none` of every sequence score -inf in every row, and V is not finite at the tokens `bad` of each.
+
+    Rows that see no other key have to give O = 0 and LSE = -inf, whatever V holds.  Returns the inputs and O.
+    """
+    q, k, v = make(lens, hq, hkv, d, seed=seed)
+    q[:, :, 0] = 1.0
+    at, empty = 0, torch.zeros(sum(lens), dtype=torch.bool, device=DEV)
+    for n in lens:
+        k[at:at + none, :, 0] = -math.inf
+        empty[at:at + (min(none, n) if causal else n if none >= n else 0)] = True
+        for i, (token, col) in enumerate(bad):
+            v[at + token, :, col] = math.nan if i % 2 else math.inf
+        at += n
+    o, lse = serve.attention_packed(q, k, v, lens, causal=causal)
+    assert torch.isneginf(lse[:, empty]).all() and (o[empty] == 0).all()
+    assert not torch.isneginf(lse[:, ~empty]).any()
+    return q, k, v, o
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2), (3, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_without_weight_are_zero_whatever_the_values(serve, hq, hkv, d):
+    # values behind them (30: in reach of the tile's product), and values that they see (5)
+    lens = [50, 300]
+    q, k, v, o = rows_without_weight(serve, lens, hq, hkv, d, True, 20, [(30, 1), (33, 0), (5, 2)], seed=10)
+    cols = [c for c in range(d) if c != 2]  # a row with weight elsewhere: 0 * inf from its keys without weight may be NaN
+    at = 0
+    for n in lens:
+        o64, _ = exact_rows(q[at:at + n], k[at:at + n], v[at:at + n], n, True, d ** -0.5)
+        same_but_for_rounding(o[at + 20:at + n, :, cols], o64[20:, :, cols])
+        at += n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_without_weight_where_all_keys_are_seen(serve, d):
+    rows_without_weight(serve, [40, 150, 300], 4, 2, d, False, 300, [(30, 1), (5, 2)], seed=11)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_without_weight_in_split_items(serve, d, causal):
+    import ctypes
+    need = ctypes.c_size_t(0)
+    rc = serve.lib().fa_fwd_packed_workspace((ctypes.c_int * 1)(4200), 1, 4200, 4, 1, d, int(causal), ctypes.byref(need))
+    assert rc == 0 and need.value > 0, "the call must split items"
+    none = 4160 if causal else 4200
+    q, k, v, o = rows_without_weight(serve, [4200], 4, 1, d, causal, none, [(4190, 1), (4158, 3), (17, 2)], seed=12)
+    cols = [c for c in range(d) if c not in (2, 3)]
+    for token in range(4160, 4200) if causal else ():
+        s = torch.einsum("hd,md->hm", q[token].double(), k[:token + 1, 0].double()) * d ** -0.5
+        o64 = (torch.softmax(s, -1) @ v[:token + 1, 0].double()).unsqueeze(0)
+        same_but_for_rounding(o[token:token + 1, :, cols], o64[:, :, cols])
