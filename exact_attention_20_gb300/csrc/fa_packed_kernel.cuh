@@ -214,7 +214,17 @@ struct PackedSync : Sync {
   const Item* items;
 };
 
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Sync& sy, const Params& p,
+// When a warp was last seen in mend_rows; beside the abort flag.
+__device__ __forceinline__ volatile unsigned long long* alive_word(volatile int* abort_flag) {
+  return reinterpret_cast<volatile unsigned long long*>(abort_flag + 1);
+}
+
+// Bounded wait, as the dense forward's.  A warp in mend_rows, which only the
+// mask needs, holds the others up for as long as its keys take: its last sign
+// of life counts.  (Without a mask that check alone, never reached, cost 8192
+// tokens 4 %.)
+template <bool CAUSAL>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const PackedSync& sy, const Params& p,
                                            unsigned long long more_ns = 0) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
@@ -223,7 +233,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
     if (mbar_try_wait(bar, parity)) return true;
     if ((++polls & 31u) == 0u) {
       if (*sy.abort_flag) return false;
-      if (global_timer_ns() - t0 > p.wait_limit_ns + more_ns) {
+      uint64_t since = t0;
+      if constexpr (CAUSAL) {
+        const uint64_t alive = *alive_word(sy.abort_flag);  // read before the clock
+        if (alive > since) since = alive;
+      }
+      if (global_timer_ns() - since > p.wait_limit_ns + more_ns) {
         *sy.abort_flag = 1;
         atomicCAS(p.status, 0, kSitePacked);
         return false;
@@ -264,7 +279,7 @@ __device__ __forceinline__ void run_dispatcher(Item* items, const PackedSync& sy
     it.visible = it.seen[1] - (it.steps - 1) * kBlockN;
     // free once the item kItemsAhead before is done; a step takes far less than 16 us
     const uint32_t n = i % kItemsAhead;
-    if (!wait_phase(sy.item_empty0 + 8 * n, ((i / kItemsAhead) & 1u) ^ 1u, sy, p, steps << 14)) return;
+    if (!wait_phase<CAUSAL>(sy.item_empty0 + 8 * n, ((i / kItemsAhead) & 1u) ^ 1u, sy, p, steps << 14)) return;
     items[n] = it;
     mbar_arrive(sy.item_full0 + 8 * n);
     if (!it.more) return;
@@ -288,14 +303,14 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
   bool more = true;
   for (uint32_t i = 0; more && ok; ++i) {
     const uint32_t n = i % kItemsAhead;
-    ok = wait_phase(sy.item_full0 + 8 * n, (i / kItemsAhead) & 1u, sy, p);
+    ok = wait_phase<CAUSAL>(sy.item_full0 + 8 * n, (i / kItemsAhead) & 1u, sy, p);
     if (!ok) break;
     const Item it = sy.items[n];
     mbar_arrive(sy.item_empty0 + 8 * n);
     more = it.more;
     for (int t = 0; t < kQTiles; ++t) {
       if (it.ne[t] <= it.kb) continue;  // no key tile of its own here
-      ok = wait_phase(sy.q_empty[t], (q_loads[t] & 1u) ^ 1u, sy, p);
+      ok = wait_phase<CAUSAL>(sy.q_empty[t], (q_loads[t] & 1u) ^ 1u, sy, p);
       if (!ok) break;
       ++q_loads[t];
       mbar_arrive_expect_tx(sy.q_full[t], q_bytes);
@@ -310,7 +325,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tmQ, const CUten
       for (int n = 0; n < 2; ++n) {
         if (!ok) break;
         const uint32_t slot = kv_count % C::kStages;
-        ok = wait_phase(sy.kv_empty0 + 8 * slot, ((kv_count / C::kStages) & 1u) ^ 1u, sy, p);
+        ok = wait_phase<CAUSAL>(sy.kv_empty0 + 8 * slot, ((kv_count / C::kStages) & 1u) ^ 1u, sy, p);
         if (!ok) break;
         const uint32_t full = sy.kv_full0 + 8 * slot;
         mbar_arrive_expect_tx(full, C::kTileBytes);
@@ -359,7 +374,7 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
   const int lane = threadIdx.x & 31;
   const bool leader = lane == 0;
   auto wait_voted = [&](uint32_t bar, uint32_t par) {
-    ok = __all_sync(0xffffffffu, ok && wait_phase(bar, par, sy, p));
+    ok = __all_sync(0xffffffffu, ok && wait_phase<CAUSAL>(bar, par, sy, p));
   };
   // Both issuers wait for every position of the ring, in order: a full
   // barrier's wait is by parity and tells a fill only from the one before.
@@ -652,7 +667,9 @@ template <int D>
 __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0, const Item& c, const Mend mine,
                                        const Params& p) {
   constexpr int kPer = D / 32;  // columns of a lane
+  constexpr int kRound = 128;   // keys between signs of life, about 20 us
   const int behind = min(min(2 * (c.b + 1) * p.tpt, c.len), c.ke * kBlockN);  // V rows from here on were zeroed or not read
+  volatile unsigned long long* alive = alive_word(reinterpret_cast<volatile int*>(shared_base() + PackedCfg<D>::kMiscOff + 4));
   auto load = [&](const __nv_bfloat16* row, float* x) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] = __bfloat162float(row[lane * kPer + e]);
@@ -690,18 +707,28 @@ __device__ __noinline__ void mend_rows(uint32_t rows, int lane, int quad, int t0
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     const __nv_bfloat16* k = p.k + static_cast<long long>(c.begin) * p.k_stride + c.h * D;
     const int to = min(token + 1, c.ke * kBlockN);
+    // 32 rows over a million keys take a warp seconds: the others wait while it
+    // shows that it goes on.  Columns that are NaN from visible keys stay so.
+    bool open = true;
+    for (int key = c.kb * kBlockN; key < to && __any_sync(0xffffffffu, open);) {
+      if (lane == 0) *alive = global_timer_ns();
+      const int stop = min(key + kRound, to);
 #pragma unroll 4
-    for (int key = c.kb * kBlockN; key < to; ++key) {
-      float x[kPer], y[kPer], dot = 0.f;
-      load(k + key * p.k_stride, x);
-      load(v + key * p.v_stride, y);
+      for (; key < stop; ++key) {
+        float x[kPer], y[kPer], dot = 0.f;
+        load(k + key * p.k_stride, x);
+        load(v + key * p.v_stride, y);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) dot = fmaf(q[e], x[e], dot);
+        for (int e = 0; e < kPer; ++e) dot = fmaf(q[e], x[e], dot);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-      const float w = exp2f(fmaf(dot, p.qk_scale, -m_ref));
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        const float w = exp2f(fmaf(dot, p.qk_scale, -m_ref));
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, y[e], acc[e]);
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, y[e], acc[e]);
+      }
+      open = false;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) open |= need[e] && !isnan(acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -739,7 +766,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
     // read from shared memory where it is needed: 128 scores of a row and what the
     // loop over key tiles needs beside them fill the registers
     const uint32_t n = items % kItemsAhead;
-    ok = wait_phase(sy.item_full0 + 8 * n, (items / kItemsAhead) & 1u, sy, p);
+    ok = wait_phase<CAUSAL>(sy.item_full0 + 8 * n, (items / kItemsAhead) & 1u, sy, p);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const Item& it = sy.items[n];
@@ -760,7 +787,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
 
     // One key tile; the masked ones, at the end, have a loop and registers of their own.
     auto step = [&](auto masked_tile, int j) {
-      ok = wait_phase(bar_s_full, s_par, sy, p);
+      ok = wait_phase<CAUSAL>(bar_s_full, s_par, sy, p);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       s_par ^= 1u;
@@ -948,7 +975,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
     const bool empty = ne <= kb;
     Own own{kEmpty, -INFINITY, 0.f, tO};
     if (!empty) {
-      ok = wait_phase(bar_o_done, od_par, sy, p);
+      ok = wait_phase<CAUSAL>(bar_o_done, od_par, sy, p);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       od_par ^= 1u;
@@ -1151,6 +1178,7 @@ fa_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(sy.item_empty0 + 8 * n, 1 + 2 + 8);  // the producer, the issuers, the softmax warps
     }
     *sy.abort_flag = 0;
+    *alive_word(sy.abort_flag) = 0;
     fence_barrier_init();
   }
   if (warp == kLoadWarp && lane == 0) {

@@ -307,3 +307,31 @@ def test_rows_without_weight_in_split_items(serve, d, causal):
         s = torch.einsum("hd,md->hm", q[token].double(), k[:token + 1, 0].double()) * d ** -0.5
         o64 = (torch.softmax(s, -1) @ v[:token + 1, 0].double()).unsqueeze(0)
         same_but_for_rounding(o[token:token + 1, :, cols], o64[:, :, cols])
+
+
+def test_a_long_prompt_whose_last_value_is_not_finite(serve):
+    # The rows before the last one are taken anew, each over 2^19 keys, a warp's
+    # 32 one after another: that lasts longer than the 2 s after which the CTA's
+    # other warps, at the next prompt's items already, give up where nothing moves.
+    from exact_attention_20_gb300 import fa
+    n, d, lens = 1 << 19, 64, [1 << 19, 3000]
+    q, k, v = make(lens, 1, 1, d, seed=13)
+    v[n - 1, 0, 9] = math.nan
+    o, lse = serve.attention_packed(q, k, v, lens)
+    torch.cuda.synchronize()
+    assert fa.device_status() == fa.FA_OK
+    assert torch.isnan(o[n - 1, 0, 9]) and int(torch.isnan(o).sum()) == 1
+    rows = torch.arange(n - 128, n - 1, device=DEV)
+    kd, vd = k[:n, 0].double(), v[:n, 0].double().nan_to_num(0.0)
+    for part in rows.split(16):
+        qd = q[part, 0].double()
+        s = (qd @ kd.T) * d ** -0.5
+        s.masked_fill_(torch.arange(n, device=DEV) > part.unsqueeze(1), -math.inf)
+        w = torch.softmax(s, -1)
+        o64 = w @ vd
+        bound = w @ vd.abs() + o64.abs()
+        # P and O in bf16 as everywhere; the fp32 sums of n terms 2^-24 n^1/2 and the scores below 2^-11
+        err = (o[part, 0].double() - o64).abs()
+        assert (err <= (2.0 ** -7 + 2.0 ** -11) * bound + 2.0 ** -8 * o64.abs()).all()
+    o64, lse64, bound, most = reference(q[n:], k[n:], v[n:], lens[1:], True, d ** -0.5)
+    compare(o[n:], lse[:, n:], o64, lse64, bound, most, d, lens[1])
