@@ -72,6 +72,14 @@ struct PackedCfg {
   // the work, an issuer that holds its turn between the halves is in the other's
   // way: 16384 tokens 823 us, 744 in one piece.
   static constexpr bool kHalves = D == 64;
+  // Tensor memory columns of query tile 0, tile 1's 128 further on.  At d = 64
+  // P has the columns that O leaves free: no product writes where another, not
+  // known to be done, still reads.  At d = 128 there are none, and P lies over
+  // S, as in the dense forward: the next S is issued behind the P V that reads
+  // P by the same thread, and of the same shape, which keeps their order.
+  static constexpr int kTmemS = 0, kTmemO = 256, kTmemP = D == 64 ? kTmemO + D : kTmemS;
+  static constexpr int kTmemTile = 128;
+  static_assert(kTmemP == kTmemS || (kTmemO + D <= kTmemP && kTmemP + kBlockN / 2 <= kTmemO + kTmemTile), "P's columns");
   static constexpr int kQOff = 0;
   static constexpr int kKVOff = kQTiles * kTileBytes;
   static constexpr int kOutOff = kKVOff + kStages * kTileBytes;
@@ -364,8 +372,9 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
   const uint64_t q_desc = sdesc_advance(sdesc_sw128(sbase + C::kQOff, 16, 1024), t * C::kTileBytes);
   const uint64_t k_desc0 = sdesc_sw128(sbase + C::kKVOff, 16, 1024);
   const uint64_t v_desc0 = sdesc_sw128(sbase + C::kKVOff, kSlabBytes, 1024);
-  const uint32_t tm_s = tmem + t * 128;
-  const uint32_t tm_o = tmem + 256 + t * 128;
+  const uint32_t tm_s = tmem + C::kTmemS + t * C::kTmemTile;
+  const uint32_t tm_p = tmem + C::kTmemP + t * C::kTmemTile;
+  const uint32_t tm_o = tmem + C::kTmemO + t * C::kTmemTile;
   constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, /*b_mn_major=*/false);
   uint32_t q_uses = 0, kv_count = 0, pr_par = 0, of_par = 1, turn_par = 0;
   bool ok = true;
@@ -445,8 +454,7 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
       }
       const uint32_t acc0 = s > kb + 1 ? 1u : 0u;
       // Groups of 16 keys that P V takes.  (Q K^T always takes all 128: with fewer
-      // columns it measured slower, and S and P V of one shape are what is known to
-      // stay in order.)
+      // columns it measured slower, and at d = 128 S and P V have to be of one shape.)
       int groups_pv = min(kBlockN, seen - (s - 1) * kBlockN + 15) / 16;
       // All of it in registers before the turn, which is what the other issuer
       // waits for (16384 tokens: 740 us; computed where it is used: 752).
@@ -479,11 +487,11 @@ __device__ __forceinline__ void run_mma(int t, uint8_t* smem, uint32_t sbase, ui
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, /*b_mn_major=*/true);
         if (groups_pv >= kTo) {
 #pragma unroll
-          for (int kk = kFrom; kk < kTo; ++kk) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+          for (int kk = kFrom; kk < kTo; ++kk) umma_ts(tm_o, tm_p + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
         } else {
 #pragma unroll
           for (int kk = kFrom; kk < kTo - 1; ++kk)
-            if (kk < groups_pv) umma_ts(tm_o, tm_s + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
+            if (kk < groups_pv) umma_ts(tm_o, tm_p + kk * 8, dv[kk], idesc_pv, kk > 0 ? 1u : acc0);
         }
       };
       using Begin = std::integral_constant<int, 0>;
@@ -751,8 +759,9 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
   const int quad = (threadIdx.x >> 5) & 3;  // TMEM lanes 32*quad .. 32*quad+31
   const int row_in_tile = quad * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t tS = tmem + lane_off + t * 128;
-  const uint32_t tO = tmem + lane_off + 256 + t * 128;
+  const uint32_t tS = tmem + lane_off + C::kTmemS + t * C::kTmemTile;
+  const uint32_t tP = tmem + lane_off + C::kTmemP + t * C::kTmemTile;
+  const uint32_t tO = tmem + lane_off + C::kTmemO + t * C::kTmemTile;
   const float qk = p.qk_scale;
   const uint32_t bar_s_full = t ? sy.s_full[1] : sy.s_full[0];
   const uint32_t bar_p_ready = t ? sy.p_ready[1] : sy.p_ready[0];
@@ -828,7 +837,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
       if constexpr (kMasked) {
         // A masked tile: 32 columns at a time, up to the last that some row of
         // the tile sees; the maximum first, then the exponentials from S read
-        // again (P's 16 columns lie over columns of S read before).
+        // again (where P lies over S, its 16 columns over some read before).
         const int len = it.len, t0 = (2 * it.b + t) * p.tpt;  // the tile's first token
         const int lim = (CAUSAL ? min(t0 + row_in_tile / p.G, len - 1) : len - 1) - j * kBlockN;  // the row's last visible key
         const int cols = (CAUSAL ? min(t0 + p.tpt, len) : len) - j * kBlockN;
@@ -875,7 +884,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
             sum2 = f2_add(sum2, f2_pack(a, b));
             add_bf16x2_halves(lqs[(n & 1) * 2], lqs[(n & 1) * 2 + 1], pk[n]);
           }
-          tmem_st16(tS + c4 * 16, pk);
+          tmem_st16(tP + c4 * 16, pk);
         }
         f2_unpack(sum2, sa, sb);
         lq_tile = (lqs[0] + lqs[1]) + (lqs[2] + lqs[3]);
@@ -883,7 +892,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
         uint32_t s[128];
         tmem_ld128_wait(tS, s);
         // One pass over the tile: exponentials against m_use, P stored to
-        // tensor memory over S, the fp32 and bf16 row sums, and (if asked) the
+        // tensor memory, the fp32 and bf16 row sums, and (if asked) the
         // tile's row maximum from the same values.
         auto exp_pass = [&](float m_use, bool with_max) -> float {
           const uint64_t negm2 = f2_pack(-m_use, -m_use);
@@ -906,7 +915,7 @@ __device__ __forceinline__ void run_softmax(int t, uint32_t tmem, const PackedSy
               add_bf16x2_halves(lqs[(n & 1) * 2], lqs[(n & 1) * 2 + 1], pk[n]);
               if (with_max) mx[c4] = fmax3(mx[c4], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             }
-            tmem_st16(tS + c4 * 16, pk);
+            tmem_st16(tP + c4 * 16, pk);
             if (C::kHalves && c4 == 1) hand_over(bar_p_half);
           }
           f2_unpack(sum2, sa, sb);
