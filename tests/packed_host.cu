@@ -13,5 +13,27 @@ int packed_tmem(int d, int which, int t) {
   return at[d == 128][which] + t * (d == 128 ? B::kTmemTile : A::kTmemTile);
 }
 
+// The plan of n sequences: info = {grid, dealt, slots, split items}; ranges [grid][14] as in pk::Range, or pairs
+// [dealt / Hkv][2].
+void packed_plan(const int* lens, int n, int Hkv, int tpt, int causal, int num_ctas, int* info, int* ranges, int* pairs) {
+  static pk::Params p;
+  p.cu[0] = 0;
+  for (int i = 0; i < n; ++i) p.cu[i + 1] = p.cu[i] + lens[i];
+  info[0] = causal ? pk::make_plan<true>(n, Hkv, tpt, num_ctas, p, info[2], info[3])
+                   : pk::make_plan<false>(n, Hkv, tpt, num_ctas, p, info[2], info[3]);
+  info[1] = p.dealt;
+  if (p.dealt > 0) {
+    for (int i = 0; i < p.dealt / Hkv; ++i) pairs[2 * i] = p.pair[i].s, pairs[2 * i + 1] = p.pair[i].b;
+    return;
+  }
+  for (int c = 0; c < info[0]; ++c) {
+    const pk::Range& r = p.range[c];
+    const int x[14] = {r.s, r.h, r.b, r.n_items, r.step_begin, r.step_end,
+                       r.first.slot, r.first.slot0, r.first.count, r.first.k,
+                       r.last.slot, r.last.slot0, r.last.count, r.last.k};
+    for (int i = 0; i < 14; ++i) ranges[14 * c + i] = x[i];
+  }
+}
+
 int packed_halves(int d) { return d == 128 ? pk::PackedCfg<128>::kHalves : pk::PackedCfg<64>::kHalves; }
 }

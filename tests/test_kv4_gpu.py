@@ -350,3 +350,57 @@ def test_nothing_to_do(serve):
     k, v = serve.kv4_load(cache, table, int32([]), int32([0]), 0, 64)
     o, lse = serve.kv4_attention(none, cache, table, int32([]))
     assert k.shape == (0, 1, 64) and o.shape == (0, 1, 64) and lse.shape == (1, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g_k,g_v", [(2.0 ** -9, 2.0 ** 7), (2.0 ** 5, 2.0 ** -12), (2.0 ** 40, 2.0 ** -40)])
+def test_attention_with_scales_of_the_tensors(serve, d, g_k, g_v):
+    # a product with a power of two is exact, so nothing else changes: whole items, and a cut one
+    lens, hq, hkv, page = [70, 3000], 8, 2, 32
+    table, pages = layout(lens, page, 21)
+    cache = serve.kv4_cache(pages, hkv, d, page).fill_(0xFF)
+    g = generator(21)
+    k = (torch.randn((sum(lens), hkv, d), generator=g, device=DEV) * g_k).bfloat16()
+    v = (torch.randn((sum(lens), hkv, d), generator=g, device=DEV) * g_v).bfloat16()
+    serve.kv4_store(cache, k, v, table, int32(lens), cumulative(lens), k_scale=g_k, v_scale=g_v)
+    q = torch.randn((2, hq, d), generator=g, device=DEV).bfloat16()
+    scale = d ** -0.5 / g_k
+    o, lse = serve.kv4_attention(q, cache, table, int32(lens), scale=scale, k_scale=g_k, v_scale=g_v)
+    for i, n in enumerate(lens):
+        kk, vv = ref.read(cache, d, page, table[i].tolist()[:-(-n // page)], n, g_k, g_v)
+        compare(o[i:i + 1], lse[:, i:i + 1], *ref.attend(q[i:i + 1], kk, vv, scale), n, float(vv.abs().max()), d)
+
+
+def split(serve, n, nq, hq, hkv, d, max_pages, page):
+    import ctypes
+    need = ctypes.c_size_t(0)
+    rc = serve.lib().fa_kv4_attention_workspace(n, nq, hq, hkv, d, max_pages, page, ctypes.byref(need))
+    assert rc == 0
+    return need.value > 0
+
+
+@pytest.mark.parametrize("lens,nq,hq,hkv,d", [
+    # more sequences than a CTA has threads (512; 256 for the 32-row tile at d = 128), most of them empty or short
+    ([0, 1, 0, 2] * 300 + [9000] + [1, 0, 33] * 50, 1, 4, 2, 64),
+    ([5000] + [i % 3 for i in range(1500)] + [4000, 17], 1, 4, 1, 128),
+    ([i * 53 % 1400 for i in range(600)], 1, 2, 1, 64),              # ranges end within many of them
+    ([0] * 299 + [3000] + [1] * 300 + [2000], 4, 8, 1, 128),
+    ([0] * 1100 + [600], 1, 1, 1, 64),
+])
+def test_more_sequences_than_threads_with_cut_items(serve, lens, nq, hq, hkv, d):
+    page = 64
+    assert split(serve, len(lens), nq, hq, hkv, d, -(-max(lens) // page), page)
+    check_attention(serve, lens, hq, hkv, d, page, nq=nq, seed=22)
+
+
+def test_a_store_of_refused_tokens_alone_leaves_the_cache(serve):
+    d, page = 64, 16
+    k = torch.ones((6, 1, d), dtype=torch.bfloat16, device=DEV)
+    cache = serve.kv4_cache(4, 1, d, page).fill_(0x5A)
+    before = cache.clone()
+    table = int32([[0, 4], [1, 2], [-1, 3]])
+    errors = int32([0])
+    # positions 31 (page 4 of 4) and 32 (past the table), 32 and 33, 38 and 39
+    serve.kv4_store(cache, k, k, table, int32([33, 34, 40]), int32([0, 2, 4, 6]), errors=errors)
+    assert errors.item() == serve.BAD_PAGE | serve.BAD_POSITION
+    assert torch.equal(cache, before)

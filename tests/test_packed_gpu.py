@@ -335,3 +335,32 @@ def test_a_long_prompt_whose_last_value_is_not_finite(serve):
         assert (err <= (2.0 ** -7 + 2.0 ** -11) * bound + 2.0 ** -8 * o64.abs()).all()
     o64, lse64, bound, most = reference(q[n:], k[n:], v[n:], lens[1:], True, d ** -0.5)
     compare(o[n:], lse[:, n:], o64, lse64, bound, most, d, lens[1])
+
+
+@pytest.mark.parametrize("lens,hq,hkv,causal", [
+    ([4096], 4, 1, True),
+    ([4096], 2, 2, False),
+    ([6000, 10, 2000], 8, 2, True),
+    ([3333, 3333], 12, 4, False),
+    ([10635], 1, 1, True),            # items of up to six parts
+])
+def test_split_items_of_head_size_64(serve, lens, hq, hkv, causal):
+    import ctypes
+    arr = (ctypes.c_int * len(lens))(*lens)
+    need = ctypes.c_size_t(0)
+    rc = serve.lib().fa_fwd_packed_workspace(arr, len(lens), sum(lens), hq, hkv, 64, int(causal), ctypes.byref(need))
+    assert rc == 0 and need.value > 0, "the call must split items"
+    check(serve, lens, hq, hkv, 64, causal, seed=14)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.02, 1e-6])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales(serve, scale, d):
+    # 1: peaked rows, whose references move; 1e-6: nearly the mean of V
+    lens = [700, 33, 300]
+    q, k, v = make(lens, 8, 2, d, seed=15)
+    o, lse = serve.attention_packed(q, k, v, lens, scale=scale)
+    o64, lse64, bound, most = reference(q, k, v, lens, True, scale)
+    # scores up to `most` = scale sum|q||k| are off by (d + 8) 2^-24 of it, which moves a weight by twice that
+    bound = bound * (1 + 2 * (d + 8) * 2.0 ** -24 * most / 2.0 ** -7)
+    compare(o, lse, o64, lse64, bound, most, d, max(lens))
