@@ -364,3 +364,18 @@ def test_scales(serve, scale, d):
     # scores up to `most` = scale sum|q||k| are off by (d + 8) 2^-24 of it, which moves a weight by twice that
     bound = bound * (1 + 2 * (d + 8) * 2.0 ** -24 * most / 2.0 ** -7)
     compare(o, lse, o64, lse64, bound, most, d, max(lens))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_split_items_in_several_launches(serve, d):
+    # a launch takes 1024 sequences; each has items to cut, and the launches share the workspace one after another
+    import ctypes
+    lens = [5000] + [i % 2 for i in range(1100)] + [6001] + [1, 0] * 500 + [3000]
+    need = []
+    for part in (lens[:1024], lens[1024:2048], lens[2048:], lens):
+        b = ctypes.c_size_t(0)
+        arr = (ctypes.c_int * len(part))(*part)
+        assert serve.lib().fa_fwd_packed_workspace(arr, len(part), sum(part), 2, 1, d, 1, ctypes.byref(b)) == 0
+        need.append(b.value)
+    assert min(need[:3]) > 0 and need[3] == max(need[:3])
+    check(serve, lens, 2, 1, d, True, seed=16)
