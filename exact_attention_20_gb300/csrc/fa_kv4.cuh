@@ -198,8 +198,8 @@ __device__ __forceinline__ void find_places(int first, int count, int D, const M
 // A thread stores one block: 32 bytes read, 8 code bytes and a scale byte
 // written.  Consecutive threads take a token's blocks of one head, then the
 // next token's, so that a warp writes whole runs of a group's rows.  Bound by
-// the bytes: 107846 tokens of 8 heads, d = 128, stored and loaded again, 1.13
-// GB, 188 us, 6.0 TB/s (203 with 16-byte accesses).
+// the bytes: 107846 tokens of 8 heads, d = 128, 566 MB, 95 us, 6.0 TB/s (and
+// loaded again 188 us in all; 203 with 16-byte accesses).
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) store_kernel(const MoveParams p) {
   constexpr int kBlocks = D / kBlock;

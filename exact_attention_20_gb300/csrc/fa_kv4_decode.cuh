@@ -36,7 +36,7 @@
 // what an item has in several CTAs by merge_kernel.
 //
 // Measured on a GB300 (8 KV heads of 4 query heads, d = 128): 96 contexts of
-// 320 to 16000 tokens, 403 MB of cache, 78 us (59 at the copy rate); one of
+// 350 to 16000 tokens, 403 MB of cache, 79 us (59 at the copy rate); one of
 // 131072, 151 MB, 39 us (22).  About 219 instructions a group of 16 tokens
 // leave issue slots 60 % used; of a call's time 3 us go to finding the
 // ranges, 4 to the first loads, 3 to the combination and 4 to the merge, and
@@ -95,9 +95,13 @@ struct DecodeCfg {
   static constexpr int kRows = 8 * NT;
   // One CTA an SM (two of eight warps, whose ends an SM's preference for its
   // older warps draws 10 us apart, took 84 us where this takes 80).  O^T takes
-  // NT D / 4 registers of a lane: up to 64 of them leave room for 16 warps,
-  // with Q in shared memory where it would take 32 more; the ring has three
-  // units a warp then (216 KB, two thirds of it in flight).
+  // NT D / 4 registers of a lane: with 128 of them a CTA has 8 warps, else 16,
+  // whose 128 registers a lane hold everything at NT D / 4 = 16, 32 and, but
+  // for spills (112 bytes stored at d = 128, 304 at d = 64), 64, with Q in
+  // shared memory where it would take 32 more.  At d = 128 and 8 rows the ring
+  // has three units a warp (216 KB, two thirds of it in flight).  The 96
+  // contexts above, with 8 / 16 / 32 rows of a KV head: 80 / 122 / 191 us at d =
+  // 128, 53 / 72 / 153 at d = 64; the cache alone would take 59 and 30.
   static constexpr bool kWide = NT * D > 256;
   static constexpr int kWarps = kWide ? 8 : kMaxWarps;
   static constexpr int kThreads = kWarps * 32;

@@ -27,17 +27,19 @@
 //   tokens, the next sequence or rows behind the last one.  Their scores are
 //   replaced by -inf; P is 0 there, but 0 * NaN is NaN: the V rows past the
 //   item's last visible key are zeroed in shared memory, and a row that comes
-//   out NaN under the mask is looked at again (mend_rows).
+//   out NaN under the mask is looked at again (mend_rows).  That is slow: where
+//   the last of 131072 tokens alone has a NaN, the 127 rows before it take 0.55
+//   s, with finite values the whole prompt of one head 3 ms.
 //
 // Warps: 0-7 softmax, one row a thread; 8 TMA; 9 and 10 MMA; 11 dispatcher.
 // Measured on a GB300: 16384 tokens, 2 KV heads of 8 query heads, d = 128,
-// causal, 735-745 us: 1485 TFLOP/s of visible products, 78 % of cuBLAS' bf16
+// causal, 735 us: 1495 TFLOP/s of visible products, 78 % of cuBLAS' bf16
 // rate; 24 prompts of 40 to 1901 tokens, 32 / 8 heads, 118 us (55 at that
 // rate; two products of 256 rows and the softmax between them are 1.6 us a
 // step, an item's start and end 3.5 us).  What bounds long prompts is the
 // turn from S to P and back in a tile's softmax warps: the tensor pipe is
 // active 62 % of the time, issue slots are 47 % used.  Without a mask at d =
-// 64, 8 x 1024 tokens of 16 heads take 59 us: 134 M exponentials, 27 us of
+// 64, 8 x 1024 tokens of 16 heads take 60 us: 134 M exponentials, 27 us of
 // the MUFU's rate, in 3.4 rounds of items that cost four.
 #pragma once
 
@@ -68,7 +70,8 @@ struct PackedCfg {
   static constexpr int kStages = D == 128 ? 4 : 9;
   // P in two halves: the product with V's first 64 keys starts while the other
   // half's exponentials are taken.  8 x 1024 tokens of 16 heads at d = 64 without
-  // a mask: 59 us, 62 in one piece.  At d = 128, where the tensor core has twice
+  // a mask: 59 us, 62 in one piece (both with P over S, below; with P beside it
+  // 60).  At d = 128, where the tensor core has twice
   // the work, an issuer that holds its turn between the halves is in the other's
   // way: 16384 tokens 823 us, 744 in one piece.
   static constexpr bool kHalves = D == 64;

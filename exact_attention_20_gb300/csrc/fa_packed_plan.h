@@ -168,6 +168,8 @@ inline int make_plan(int n, int Hkv, int tpt, int num_ctas, Params& p, int& n_sl
         for (; cut < ctas && next < at + w; next = weight * ++cut / ctas) {
           const int off = static_cast<int>(next - at) - kItemCost / 2;
           int step = off < 0 ? 0 : off > steps ? steps : off;
+          // a cut in an item too short for it goes to the nearer end, with
+          // fewer than kMinPartSteps steps (below) always in front
           if (steps < 2 * kMinPartSteps) step = 2 * step < steps ? 0 : steps;
           if (step - done < kMinPartSteps) step = done;
           if (steps - step < kMinPartSteps && step > done) step = steps;
