@@ -154,9 +154,10 @@ constexpr int kCuCached = 2048;  // sequences whose cu entries a CTA keeps in sh
 // its group of head 0 plus its row in the low four bits, or -1 if it has no
 // place (behind the last sequence, -2 where that is an error).
 // cu_at(i) = cu[i].  The token's sequence is the last whose first token is
-// not behind it, found by bisection.
+// not behind it, found by bisection.  *at: its position in the sequence (not
+// set for -1).
 template <class Cu>
-__device__ __forceinline__ long long place_of(int tok, int D, const MoveParams& p, Cu cu_at) {
+__device__ __forceinline__ long long place_of(int tok, int D, const MoveParams& p, Cu cu_at, long long* at = nullptr) {
   const int n = p.n_seqs;
   if (n == 0 || tok < cu_at(0) || tok >= cu_at(n)) return -1;
   int lo = 0, hi = n;  // cu[lo] <= tok < cu[hi]
@@ -166,6 +167,7 @@ __device__ __forceinline__ long long place_of(int tok, int D, const MoveParams& 
   }
   // position: the sequence's last cu[lo+1] - cu[lo] positions
   const long long pos = static_cast<long long>(p.seq_lens[lo]) - cu_at(lo + 1) + tok;
+  if (at) *at = pos;
   const long long page_at = pos >> p.page_shift;
   if (pos < 0 || page_at >= p.max_pages) {
     if (p.errors) atomicOr(p.errors, kErrPosition);
