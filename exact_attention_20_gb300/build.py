@@ -17,13 +17,13 @@ ROOT = os.path.dirname(PKG)
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("fa_api.cu", "fa_noalloc.cu", "fa_bwd.cu", "fa_fp8.cu", "fa_packed.cu",
-                                                     "fa_kv4.cu", "fa_rotary.cu")]
+                                                     "fa_kv4.cu", "fa_rotary.cu", "fa_draft.cu")]
 DEPENDS = SOURCES + [
     os.path.join(PKG, "csrc", n)
     for n in ("fa_fwd_kernel.cuh", "fa_bwd_kernel.cuh", "fa_fp8_quant.cuh", "fa_decode.cuh", "sm103_ptx.cuh", "tma_host.h",
               "fa_internal.h", "fa_packed_kernel.cuh", "fa_packed_plan.h", "fa_kv4.cuh",
-              "fa_kv4_decode.cuh", "fa_kv4_host.h", "fa_rotary.cuh")
-] + [os.path.join(ROOT, "include", n) for n in ("fa_gb300.h", "fa_gb300_serve.h", "fa_gb300_rotary.h")]
+              "fa_kv4_decode.cuh", "fa_kv4_host.h", "fa_rotary.cuh", "fa_verify.cuh", "fa_keep.cuh")
+] + [os.path.join(ROOT, "include", n) for n in ("fa_gb300.h", "fa_gb300_serve.h", "fa_gb300_rotary.h", "fa_gb300_draft.h")]
 
 COMPILE_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

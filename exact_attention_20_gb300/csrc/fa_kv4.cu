@@ -7,7 +7,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "fa_gb300_serve.h"
+#include "fa_gb300_draft.h"
 #include "fa_internal.h"
 #include "fa_kv4_decode.cuh"
 #include "fa_kv4_host.h"
@@ -17,8 +17,10 @@ namespace {
 namespace kv = fa::kv4;
 using namespace fa_internal;
 
+constexpr int kMaxNodes = 64;  // of a tree: a node's line is one word
+
 std::mutex g_mu;
-bool g_attr[kMaxDevices][2][3];  // shared-memory attribute set: [d == 128][row tiles of 8, 16, 32]
+bool g_attr[kMaxDevices][2][2][3];  // shared-memory attribute set: [tree][d == 128][row tiles of 8, 16, 32]
 
 int move(bool store, const void* k, const void* v, void* k_out, void* v_out, void* cache, const int* page_table,
          const int* seq_lens, const int* cu, int T, int n_seqs, int max_pages, int num_pages, int page_size, int Hkv,
@@ -116,13 +118,13 @@ DecodePlan decode_plan(int n_seqs, int Lq, int G, int Hkv, int d, int max_pages,
   return pl;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cudaStream_t stream) {
-  auto kernel = kv::decode_kernel<D, NT>;
+  auto kernel = kv::decode_kernel<D, NT, TREE>;
   constexpr int smem = kv::DecodeCfg<D, NT>::kSmemBytes;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_attr[dev][D == 128][NT / 2];
+    bool& set = g_attr[dev][TREE][D == 128][NT / 2];
     if (!set) {
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return FA_ERR_LAUNCH;
@@ -156,6 +158,89 @@ int check_decode_sizes(int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages
   if (Lq > (1 << 16) || rows > (1 << 20) || static_cast<long long>(n_seqs) * Lq > (1 << 30)) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(n_seqs) * Hkv * ((rows + 7) / 8) > (1ll << 30)) return FA_ERR_INVALID_ARG;
   return FA_OK;
+}
+
+template <bool TREE>
+int launch_rows(const kv::DecodeParams& p, const DecodePlan& pl, int d, int dev, cudaStream_t s) {
+  if (d == 128)
+    return pl.nt == 1 ? launch_decode<128, 1, TREE>(p, pl, dev, s)
+         : pl.nt == 2 ? launch_decode<128, 2, TREE>(p, pl, dev, s) : launch_decode<128, 4, TREE>(p, pl, dev, s);
+  return pl.nt == 1 ? launch_decode<64, 1, TREE>(p, pl, dev, s)
+       : pl.nt == 2 ? launch_decode<64, 2, TREE>(p, pl, dev, s) : launch_decode<64, 4, TREE>(p, pl, dev, s);
+}
+
+// The attention of the newest tokens, in order or as a tree's nodes.
+int attention(bool tree, const void* q, const void* cache, const int* page_table, const int* seq_lens,
+              const int* parents, void* o, float* lse, int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages,
+              int num_pages, int page_size, long long q_stride, float scale, float k_scale, float v_scale, int* errors,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_decode_sizes(n_seqs, Lq, Hq, Hkv, d, max_pages, page_size);
+  if (rc != FA_OK) return rc;
+  size_t cb = 0;
+  rc = check_cache(cache, page_table, seq_lens, n_seqs, max_pages, num_pages, page_size, Hkv, d, k_scale, v_scale, &cb);
+  if (rc != FA_OK) return rc;
+  const long long row = static_cast<long long>(Hq) * d;
+  const float qk_scale = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
+  if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(qk_scale) || !(qk_scale > 0.f) || q_stride < row ||
+      q_stride % 8 || q_stride > (1ll << 32))
+    return FA_ERR_INVALID_ARG;
+  if (n_seqs == 0) return FA_OK;
+  if (!q || !o || !lse || (tree && !parents)) return FA_ERR_NULL;
+  if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(errors, 4) ||
+      misaligned(parents, 4) || misaligned(workspace, 256))
+    return FA_ERR_ALIGN;
+  const size_t T = static_cast<size_t>(n_seqs) * Lq;
+  const void* in[6] = {q, cache, page_table, seq_lens, parents, errors};
+  const size_t in_bytes[6] = {((T - 1) * q_stride + row) * 2, cb, static_cast<size_t>(n_seqs) * max_pages * 4,
+                              static_cast<size_t>(n_seqs) * 4, T * 4, 4};
+  const void* out[3] = {o, lse, workspace};
+  const size_t out_bytes[3] = {T * row * 2, T * Hq * 4, workspace_bytes};
+  for (int i = 0; i < 3; ++i) {
+    if (out[i] == nullptr) continue;
+    for (int j = 0; j < 6; ++j)
+      if (in[j] && overlaps(out[i], out_bytes[i], in[j], in_bytes[j])) return FA_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (out[j] && overlaps(out[i], out_bytes[i], out[j], out_bytes[j])) return FA_ERR_ALIAS;
+  }
+  for (int j = 0; j < 5; ++j)
+    if (errors && in[j] && overlaps(errors, 4, in[j], in_bytes[j])) return FA_ERR_ALIAS;
+  int dev = 0;
+  fa_internal::DeviceView view;
+  rc = current(&dev, &view);
+  if (rc != FA_OK) return rc;
+  const DecodePlan pl = decode_plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms);
+  if (pl.bytes > 0 && (workspace == nullptr || workspace_bytes < pl.bytes)) return FA_ERR_SCRATCH;
+  kv::DecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  const long long rows = pl.grid * 8 * pl.nt;
+  p.part_o = static_cast<float*>(workspace);
+  p.first_o = p.part_o + 2 * rows * d;
+  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kMaxWarps * rows * d);
+  p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * rows);
+  p.errors = errors;
+  p.status = view.status;
+  p.q_stride = q_stride;
+  p.wait_limit_ns = fa_internal::kWaitLimitNs;
+  p.qk_scale = qk_scale;
+  p.v_scale = v_scale;
+  p.n_seqs = n_seqs;
+  p.Lq = Lq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.row_tiles = pl.row_tiles;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.page_shift = page_shift(page_size);
+  p.split = pl.split;
+  p.parents = parents;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return tree ? launch_rows<true>(p, pl, d, dev, s) : launch_rows<false>(p, pl, d, dev, s);
 }
 
 }  // namespace
@@ -194,76 +279,23 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
                      int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages, int num_pages, int page_size,
                      long long q_stride, float scale, float k_scale, float v_scale, int* errors, void* workspace,
                      size_t workspace_bytes, void* stream) {
-  int rc = check_decode_sizes(n_seqs, Lq, Hq, Hkv, d, max_pages, page_size);
-  if (rc != FA_OK) return rc;
-  size_t cb = 0;
-  rc = check_cache(cache, page_table, seq_lens, n_seqs, max_pages, num_pages, page_size, Hkv, d, k_scale, v_scale, &cb);
-  if (rc != FA_OK) return rc;
-  const long long row = static_cast<long long>(Hq) * d;
-  const float qk_scale = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
-  if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(qk_scale) || !(qk_scale > 0.f) || q_stride < row ||
-      q_stride % 8 || q_stride > (1ll << 32))
-    return FA_ERR_INVALID_ARG;
-  if (n_seqs == 0) return FA_OK;
-  if (!q || !o || !lse) return FA_ERR_NULL;
-  if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(errors, 4) ||
-      misaligned(workspace, 256))
-    return FA_ERR_ALIGN;
-  const size_t T = static_cast<size_t>(n_seqs) * Lq;
-  const void* in[5] = {q, cache, page_table, seq_lens, errors};
-  const size_t in_bytes[5] = {((T - 1) * q_stride + row) * 2, cb, static_cast<size_t>(n_seqs) * max_pages * 4,
-                              static_cast<size_t>(n_seqs) * 4, 4};
-  const void* out[3] = {o, lse, workspace};
-  const size_t out_bytes[3] = {T * row * 2, T * Hq * 4, workspace_bytes};
-  for (int i = 0; i < 3; ++i) {
-    if (out[i] == nullptr) continue;
-    for (int j = 0; j < 5; ++j)
-      if (in[j] && overlaps(out[i], out_bytes[i], in[j], in_bytes[j])) return FA_ERR_ALIAS;
-    for (int j = i + 1; j < 3; ++j)
-      if (out[j] && overlaps(out[i], out_bytes[i], out[j], out_bytes[j])) return FA_ERR_ALIAS;
-  }
-  for (int j = 0; j < 4; ++j)
-    if (errors && overlaps(errors, 4, in[j], in_bytes[j])) return FA_ERR_ALIAS;
-  int dev = 0;
-  fa_internal::DeviceView view;
-  rc = current(&dev, &view);
-  if (rc != FA_OK) return rc;
-  const DecodePlan pl = decode_plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms);
-  if (pl.bytes > 0 && (workspace == nullptr || workspace_bytes < pl.bytes)) return FA_ERR_SCRATCH;
-  kv::DecodeParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.cache = static_cast<const uint8_t*>(cache);
-  p.page_table = page_table;
-  p.seq_lens = seq_lens;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  const long long rows = pl.grid * 8 * pl.nt;
-  p.part_o = static_cast<float*>(workspace);
-  p.first_o = p.part_o + 2 * rows * d;
-  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kMaxWarps * rows * d);
-  p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * rows);
-  p.errors = errors;
-  p.status = view.status;
-  p.q_stride = q_stride;
-  p.wait_limit_ns = fa_internal::kWaitLimitNs;
-  p.qk_scale = qk_scale;
-  p.v_scale = v_scale;
-  p.n_seqs = n_seqs;
-  p.Lq = Lq;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.row_tiles = pl.row_tiles;
-  p.max_pages = max_pages;
-  p.num_pages = num_pages;
-  p.page_shift = page_shift(page_size);
-  p.split = pl.split;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 128)
-    return pl.nt == 1 ? launch_decode<128, 1>(p, pl, dev, s)
-         : pl.nt == 2 ? launch_decode<128, 2>(p, pl, dev, s) : launch_decode<128, 4>(p, pl, dev, s);
-  return pl.nt == 1 ? launch_decode<64, 1>(p, pl, dev, s)
-       : pl.nt == 2 ? launch_decode<64, 2>(p, pl, dev, s) : launch_decode<64, 4>(p, pl, dev, s);
+  return attention(false, q, cache, page_table, seq_lens, nullptr, o, lse, n_seqs, Lq, Hq, Hkv, d, max_pages, num_pages,
+                   page_size, q_stride, scale, k_scale, v_scale, errors, workspace, workspace_bytes, stream);
+}
+
+int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, int d, int max_pages, int page_size,
+                                    size_t* bytes) {
+  if (n_nodes > kMaxNodes) return FA_ERR_INVALID_ARG;
+  return fa_kv4_attention_workspace(n_seqs, n_nodes, Hq, Hkv, d, max_pages, page_size, bytes);
+}
+
+int fa_kv4_tree_attention(const void* q, const void* cache, const int* page_table, const int* seq_lens,
+                          const int* parents, void* o, float* lse, int n_seqs, int n_nodes, int Hq, int Hkv, int d,
+                          int max_pages, int num_pages, int page_size, long long q_stride, float scale, float k_scale,
+                          float v_scale, int* errors, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_nodes > kMaxNodes) return FA_ERR_INVALID_ARG;
+  return attention(true, q, cache, page_table, seq_lens, parents, o, lse, n_seqs, n_nodes, Hq, Hkv, d, max_pages,
+                   num_pages, page_size, q_stride, scale, k_scale, v_scale, errors, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -88,6 +88,7 @@ struct DecodeParams {
   int row_tiles;           // row tiles of an item's Lq * G rows
   int max_pages, num_pages, page_shift;  // page_size = 1 << page_shift
   int split;               // ranges may cut items (the merge kernel follows)
+  const int* parents;      // a tree's, [n_seqs][Lq]; null where the queries are the newest tokens in order
 };
 
 template <int D, int NT>
@@ -232,6 +233,22 @@ __device__ __forceinline__ RowPlace row_place(int s, int item, int r_in_tile, in
   return RowPlace{r < p.Lq * p.G, static_cast<long long>(s) * p.Lq + i, h * p.G + r - i * p.G};
 }
 
+// What node `i` of a tree sees of the tree: bit j where j lies on the line from
+// the context (parent -1) to i, which it ends with; 0 where there is no such line
+// (an absent node: a parent below -1 or not before its child, on the way too, or
+// a position below 0).  Ends after at most i steps: a parent comes before its child.
+__device__ __forceinline__ unsigned long long tree_line(const int* parents, int i, int first_position) {
+  unsigned long long line = 0;
+  for (;;) {
+    if (first_position + i < 0) return 0ull;
+    line |= 1ull << i;
+    const int parent = __ldg(parents + i);
+    if (parent == -1) return line;
+    if (parent < 0 || parent >= i) return 0ull;
+    i = parent;
+  }
+}
+
 // Query rows to f16 fragments: lane (g, t) of row tile nt holds row 8 nt + g,
 // d = (D/4) t ..., step i the elements 4i .. 4i+3 of those in two words; and
 // each row's factor from a product of S^T to log2 units.
@@ -271,8 +288,10 @@ __device__ __forceinline__ void load_q_rows(int nt, int row_tile0, const Walk& w
   }
 }
 
-// One warp's state over the units it took of one item.
-template <int D, int NT>
+// One warp's state over the units it took of one item.  TREE: the queries are
+// the nodes of a tree, whose row r sees the context (positions before the
+// sequence's last Lq) and the nodes in lines[r].
+template <int D, int NT, bool TREE>
 struct State {
   static constexpr bool kSharedQ = DecodeCfg<D, NT>::kSharedQ;
   float acc[NT][D / 16][4];  // O^T: d = (D/8) g + 2j (+1: elements 2, 3), rows 2t (+1: elements 1, 3)
@@ -280,6 +299,44 @@ struct State {
   float f[NT][2];            // a product of S^T to log2 units, for rows 2t and 2t+1
   uint32_t q[kSharedQ ? 1 : NT][D / 16][2];
   const uint2* q_shared;     // this lane's words in shared memory, steps and row tiles 32 apart
+  unsigned long long* lines; // TREE: [kRows], the warp's
+
+  // Whether row r of the item's row tile at row0 sees a position (one of the sequence's, where TREE).
+  __device__ __forceinline__ bool sees(int r, int row0, int position, const Walk& w, const DecodeParams& p) const {
+    if constexpr (TREE) {
+      const int node = position - (w.len - p.Lq);
+      return node < 0 || (node < 64 && ((lines[r] >> node) & 1ull));
+    } else {
+      // a row past the item's last is as its last
+      return position <= w.len - p.Lq + min(row0 + r, p.Lq * p.G - 1) / p.G;  // the row's own position
+    }
+  }
+
+  __device__ __forceinline__ void load_lines(const Walk& w, const DecodeParams& p, unsigned long long* where) {
+    lines = where;
+    const int lane = threadIdx.x & 31;
+    if (lane < 8 * NT) {
+      const int r = min(w.item % p.row_tiles * 8 * NT + lane, p.Lq * p.G - 1);
+      lines[lane] = tree_line(p.parents + static_cast<long long>(w.s) * p.Lq, r / p.G, w.len - p.Lq);
+    }
+    __syncwarp();
+  }
+
+  // Rows of absent nodes, which see nothing, as if there had been no key.
+  __device__ __forceinline__ void drop_absent() {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (lines[nt * 8 + 2 * t + e] != 0) continue;
+        m[nt][e] = kNone;
+        l[nt][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) acc[nt][j][e] = acc[nt][j][2 + e] = 0.f;
+      }
+    __syncwarp();  // before the next segment's lines
+  }
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -456,8 +513,7 @@ struct State {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int r = min(row0 + nt * 8 + 2 * t + e, p.Lq * p.G - 1);
-              if (pos + k > w.len - p.Lq + r / p.G) continue;
+              if (!sees(nt * 8 + 2 * t + e, row0, pos + k, w, p)) continue;
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) acc[nt][j][e] = acc[nt][j][2 + e] = __uint_as_float(0x7fffffffu);
             }
@@ -528,13 +584,11 @@ struct State {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // a row past the item's last is as its last
-          const int r = min(row0 + nt * 8 + 2 * t + e, p.Lq * p.G - 1);
-          const int last = w.len - p.Lq + r / p.G;  // the row's own position
+          const int r = nt * 8 + 2 * t + e;
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            if (((skip >> n) & 1u) || pos + n * kGroup + key > last) c[n][nt][e] = -INFINITY;
-            if (((skip >> n) & 1u) || pos + n * kGroup + key + 8 > last) c[n][nt][2 + e] = -INFINITY;
+            if (((skip >> n) & 1u) || !sees(r, row0, pos + n * kGroup + key, w, p)) c[n][nt][e] = -INFINITY;
+            if (((skip >> n) & 1u) || !sees(r, row0, pos + n * kGroup + key + 8, w, p)) c[n][nt][2 + e] = -INFINITY;
           }
         }
     }
@@ -678,7 +732,7 @@ __device__ __forceinline__ void combine(const int* entries, const int* starts, i
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(const DecodeParams p) {
   using C = DecodeCfg<D, NT>;
   constexpr int kRows = C::kRows, kWarps = C::kWarps, kThreads = C::kThreads;
@@ -688,6 +742,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(c
   __shared__ LoadCursor s_load[kWarps];
   __shared__ Shared s_shared[kWarps][2];
   __shared__ int s_entry[2 * kWarps], s_group[2 * kWarps + 1], s_groups;
+  __shared__ unsigned long long s_lines[TREE ? kWarps * kRows : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * C::kWarpRing;
   const uint32_t ring_u32 = smem_u32(ring);
@@ -759,6 +814,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(c
   if (p.errors && blockIdx.x == 0) {
     for (int s = threadIdx.x; s < p.n_seqs; s += kThreads)
       if (p.seq_lens[s] != tokens_of(s, p)) atomicOr(p.errors, kErrPosition);
+    if constexpr (TREE) {
+      for (int i = threadIdx.x; i < p.n_seqs * p.Lq; i += kThreads)
+        if (p.parents[i] >= i % p.Lq) atomicOr(p.errors, kErrTree);
+    }
   }
 
   // The loads run ahead of the arithmetic, through the same units.  Up to 32
@@ -838,14 +897,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(c
   uint32_t used = 0;            // units taken from the ring
   uint32_t at = 0, parity = 0;  // the stage of the next one, and its phase
   bool dead = false;            // a wait gave up
-  State<D, NT> state;
+  State<D, NT, TREE> state;
 #pragma unroll 1
   for (; w.left > 0; w.next(p)) {
     if (w.count == 0) continue;  // the range ends with an item's own cost
     state.reset();
     state.load_q(w, p, reinterpret_cast<uint2*>(smem + C::kQAt + warp * C::kQBytes));
+    if constexpr (TREE) state.load_lines(w, p, s_lines + warp * kRows);
     const int end = w.end();
-    const int tail_from = w.len - p.Lq + 1;  // a unit that reaches past it is masked
+    const int tail_from = w.len - p.Lq + (TREE ? 0 : 1);  // a unit that reaches past it is masked
 #pragma unroll 1
     for (int u = w.u0; u < end && !dead; ++u) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * at, parity, p.wait_limit_ns))) {
@@ -859,6 +919,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(c
       if (++at == C::kStages) at = 0, parity ^= 1u;
       issue();
     }
+    if constexpr (TREE) state.drop_absent();
     state.sum_l();
     if (w.count == w.units) {
       state.write(w, p);

@@ -1,0 +1,505 @@
+// Verification of a tree of drafted tokens against the target's probabilities.
+//
+// One cluster of CTAs walks one sequence's tree.  At node c, with logits l over
+// V tokens, M = max l and w(x) = exp((l(x) - M) / temperature), the target is p =
+// w / sum w.  Child j with token x, drawn from q, is accepted where u_j q(x)
+// T < a(x), a being what is left of w and T its sum: a = w at first, and after a
+// child that is not accepted
+//
+//     a <- max(0, a - q T),   T <- sum a,
+//
+// which is max(r - q, 0) normalised, r = a / T.  A token given (no q) loses its
+// w.  The next token is the first x where a(0) + ... + a(x) > u_0 T.
+//
+// A running sum over 10^5 tokens meets u_0 T next to some token's border all
+// the time: with sums and exponentials in fp32 one call in a hundred would give
+// another token than the same sums in 64 bits do.  So each w is computed as a sum
+// of two floats (relative error about 2^-40: exp2 by the table-driven method, 128
+// table entries and a short polynomial, every product with its error) and rounded to
+// a multiple of 2^-44; sums of those are 64-bit integers, exact, and the same
+// however the row is cut.
+//
+// Work: a node costs a pass over its row for M, one for T, and one more for each
+// drawn child that is not accepted.  CTA r of the cluster takes the r-th part of
+// the row's tiles of 256 tokens, a warp a tile at a time, a lane eight tokens,
+// and every CTA takes every decision from the same numbers.  Tiles' sums stay in
+// shared memory, so that the token is found by looking at one tile again.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace verify {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxNodes = 64;
+constexpr int kMaxVocab = 1 << 18;
+constexpr int kTile = 256;                        // tokens of a warp's step
+constexpr int kMaxTiles = kMaxVocab / kTile + 1;  // of a row that starts within a tile
+constexpr int kMaxCluster = 8;
+constexpr float kMinLog = -46.f;                  // 2^-46 is rounded to 0
+
+// 2^(k / 128) as a sum of two floats.
+__device__ const float2 kExp2[128] = {
+    {0x1p+0f, 0x0p+0f}, {0x1.0163dap+0f, 0x1.3f6666p-25f}, {0x1.02c9a4p+0f, -0x1.887fap-28f},
+    {0x1.04315ep+0f, 0x1.0dcffp-25f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0706b2p+0f, 0x1.3bbedcp-25f},
+    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.09e3ecp+0f, 0x1.58de7p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
+    {0x1.0cc922p+0f, 0x1.6e48fep-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f}, {0x1.0fb66ap+0f, 0x1.ffda64p-25f},
+    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.12abdcp+0f, 0x1.b0c73p-30f}, {0x1.1429aap+0f, 0x1.d525bcp-25f},
+    {0x1.15a98cp+0f, 0x1.14b1cap-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.18af94p+0f, -0x1.dcdc86p-26f},
+    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1bbe08p+0f, 0x1.011734p-26f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
+    {0x1.1ed502p+0f, 0x1.7e6c8ep-27f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f}, {0x1.21f49ap+0f, -0x1.d0446ep-25f},
+    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.251ce4p+0f, 0x1.f654c8p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f},
+    {0x1.284dfep+0f, 0x1.f5638p-28f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f}, {0x1.2b87fep+0f, -0x1.e4a4cep-25f},
+    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.2ecafap+0f, 0x1.27c5eap-25f}, {0x1.306fep+0f, 0x1.4636e2p-25f},
+    {0x1.32171p+0f, -0x1.d993e8p-27f}, {0x1.33c08cp+0f, -0x1.b37d2p-25f}, {0x1.356c56p+0f, -0x1.b5803cp-30f},
+    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.38cae6p+0f, 0x1.a0bb0cp-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f},
+    {0x1.3c32dcp+0f, 0x1.89d472p-27f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.3fa45p+0f, 0x1.2b2006p-26f},
+    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.431f5ep+0f, -0x1.abd5dap-26f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.46a41ep+0f, 0x1.a3a00ap-25f}, {0x1.486a2cp+0f, -0x1.47d866p-25f}, {0x1.4a32bp+0f, -0x1.e50584p-25f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4dcb2ap+0f, -0x1.8088bcp-26f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f},
+    {0x1.516daap+0f, 0x1.67b32p-27f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.551a4cp+0f, 0x1.4bb242p-25f},
+    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.58d12ep+0f, -0x1.6d07p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
+    {0x1.5c9268p+0f, 0x1.4b28d6p-25f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f}, {0x1.605e1cp+0f, -0x1.a248fep-26f},
+    {0x1.6247ecp+0f, -0x1.f8b55p-25f}, {0x1.643464p+0f, -0x1.66679cp-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f},
+    {0x1.68155ep+0f, -0x1.766ad2p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6c0128p+0f, -0x1.5e84a8p-25f},
+    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.6ff7ep+0f, -0x1.ab9aep-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
+    {0x1.73f9a4p+0f, 0x1.14b02ep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f}, {0x1.780694p+0f, 0x1.fbcba8p-25f},
+    {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.7c1edp+0f, 0x1.30c132p-28f}, {0x1.7e2f34p+0f, -0x1.261634p-25f},
+    {0x1.804276p+0f, -0x1.783cbep-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8471a4p+0f, 0x1.88f1ecp-26f},
+    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.88ac7ep+0f, -0x1.9d665ap-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.8cf322p+0f, -0x1.29576ep-25f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f}, {0x1.9145bp+0f, 0x1.723ff8p-25f},
+    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.95a44cp+0f, 0x1.790a42p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f},
+    {0x1.9a0f18p+0f, -0x1.e6bf08p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.9e8632p+0f, -0x1.873738p-26f},
+    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a309bep+0f, 0x1.8945a6p-25f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.a799e2p+0f, -0x1.99e994p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f}, {0x1.ac36bcp+0f, -0x1.606432p-31f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b0e072p+0f, 0x1.31b6ccp-25f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f},
+    {0x1.b59728p+0f, 0x1.bcab28p-25f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.ba5b04p+0f, -0x1.ebdf36p-25f},
+    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.bf2c26p+0f, -0x1.0a387ep-26f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
+    {0x1.c40ab6p+0f, -0x1.7c2c98p-39f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f}, {0x1.c8f6dap+0f, -0x1.7f230ap-25f},
+    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.cdf0b6p+0f, -0x1.54478p-25f}, {0x1.d072d4p+0f, 0x1.40f13p-25f},
+    {0x1.d2f87p+0f, 0x1.01b13ep-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.d80e32p+0f, -0x1.26cf8ep-25f},
+    {0x1.da9e6p+0f, 0x1.ed9942p-27f}, {0x1.dd322p+0f, -0x1.9fc974p-25f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
+    {0x1.e26462p+0f, -0x1.614bdap-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f}, {0x1.e7a52p+0f, -0x1.0e2cep-26f},
+    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.ecf482p+0f, 0x1.b1ccfep-25f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f},
+    {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246ebp-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f},
+    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f},
+};
+
+struct Params {
+  const void* logits;
+  const int* tokens;
+  const int* parents;
+  const float* uniforms;
+  const float* draft;
+  int* path;
+  int* n_kept;
+  int* next_token;
+  int n_nodes, V;
+  long long logits_stride, draft_stride;
+  float c_hi, c_lo;  // log2(e) / temperature
+  int greedy;        // temperature 0
+};
+
+struct Pair {  // hi + lo
+  float hi, lo;
+};
+
+__device__ __forceinline__ Pair quick_sum(float a, float b) {  // |a| >= |b|, or a = 0 = b
+  const float s = __fadd_rn(a, b);
+  return Pair{s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x))};
+}
+
+// exp((x - M) / temperature) for x <= M: z = (x - M) c as a sum of two floats,
+// z = n / 128 + r with |r| <= 2^-8, 2^z = 2^(n / 128) (1 + y + y^2 / 2 + ...), y = r
+// ln 2.  What the polynomial leaves out is below 2^-49.
+__device__ __forceinline__ Pair weight(float x, float M, const Params& p, const float2* table) {
+  const Pair d = two_sum(x, -M);
+  const float z = d.hi * p.c_hi;
+  if (!(z > kMinLog)) return Pair{0.f, 0.f};
+  const float z_lo = fmaf(d.hi, p.c_hi, -z) + fmaf(d.hi, p.c_lo, d.lo * p.c_hi);
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+  const float t = __fadd_rn(z * 128.f, kRound);
+  const int n = __float_as_int(t) - __float_as_int(kRound);
+  const float r = fmaf(__fsub_rn(t, kRound), -1.f / 128.f, z);  // exact
+  constexpr float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
+  const float y = r * kLn2;
+  const float y_lo = fmaf(r, kLn2, -y) + fmaf(r, kLn2Lo, z_lo * kLn2);
+  const float more = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y_lo);  // 2^z / 2^(n/128) - 1 - y
+  const float2 e = table[n & 127];
+  const float q = e.x * y;
+  const float low = fmaf(e.x, y, -q) + fmaf(e.x, more, fmaf(e.y, y, e.y));
+  const Pair s = quick_sum(e.x, q);
+  const Pair v = quick_sum(s.hi, s.lo + low);
+  const float scale = __int_as_float((127 + (n >> 7)) << 23);
+  return Pair{v.hi * scale, v.lo * scale};
+}
+
+// a - q T, at least 0, for T as a sum of two floats.
+__device__ __forceinline__ Pair without(const Pair& a, float q, const float2& T) {
+  const float h = q * T.x;
+  const Pair d = two_sum(a.hi, -h);
+  const Pair v = quick_sum(d.hi, d.lo + (a.lo - fmaf(q, T.y, fmaf(q, T.x, -h))));
+  return v.hi > 0.f ? v : Pair{0.f, 0.f};  // not where it is NaN
+}
+
+// A value from 0 to 1 to a multiple of 2^-44, in those: first to 2^-22, then the rest.
+__device__ __forceinline__ long long fixed44(const Pair& a) {
+  constexpr float kHi = 3.f;           // sums near it are multiples of 2^-22
+  constexpr float kLo = 0x1.8p-21f;    // of 2^-44
+  const float h = __fadd_rn(a.hi, kHi);
+  const float rest = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(h, kHi)), a.lo);
+  const int low = __float_as_int(__fadd_rn(rest, kLo)) - __float_as_int(kLo);
+  return (static_cast<long long>(__float_as_int(h) - __float_as_int(kHi)) << 22) + low;
+}
+
+__device__ __forceinline__ float2 from_fixed44(long long T) {
+  const float hi = __ll2float_rz(T);
+  return make_float2(hi * 0x1p-44f, __ll2float_rn(T - static_cast<long long>(hi)) * 0x1p-44f);
+}
+
+// u to 64 fractional bits, from [0, 1); anything else is taken as an end of it.
+__device__ __forceinline__ unsigned long long fraction64(float u) {
+  if (!(u > 0.f)) return 0ull;
+  if (u >= 1.f) return ~0ull;
+  return __float2ull_rd(u * 0x1p40f) << 24 | __float2ull_rd((u * 0x1p40f - __ull2float_rz(__float2ull_rd(u * 0x1p40f))) * 0x1p24f);
+}
+
+__device__ __forceinline__ float usable(float x) { return x != x ? -INFINITY : fminf(x, 3.40282347e38f) + 0.f; }  // + 0: -0 orders as 0
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 64-bit store to the same place in CTA `rank`'s shared memory.
+__device__ __forceinline__ void store_to(uint32_t rank, void* where, long long v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(where)), "r"(rank));
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// One CTA's part of one row: tokens tile * 256 - shift ..., tiles [begin, end).
+// The shift puts every lane's eight tokens on a boundary for wide loads.
+template <bool FP32>
+struct Row {
+  const __nv_bfloat16* b;
+  const float* f;
+  const float* q;  // the draft's row, or null
+  int V, shift, begin, end, per;
+
+  __device__ __forceinline__ Row(const Params& p, long long row, uint32_t rank, uint32_t size) {
+    V = p.V;
+    b = static_cast<const __nv_bfloat16*>(p.logits) + (FP32 ? 0 : row * p.logits_stride);
+    f = static_cast<const float*>(p.logits) + (FP32 ? row * p.logits_stride : 0);
+    q = p.draft ? p.draft + row * p.draft_stride : nullptr;
+    shift = static_cast<int>(FP32 ? reinterpret_cast<uintptr_t>(f) / 4 : reinterpret_cast<uintptr_t>(b) / 2) & 7;
+    const int tiles = (V + shift + kTile - 1) / kTile;
+    per = (tiles + static_cast<int>(size) - 1) / static_cast<int>(size);
+    begin = min(tiles, static_cast<int>(rank) * per);
+    end = min(tiles, begin + per);
+  }
+  __device__ __forceinline__ int first(int tile) const { return tile * kTile - shift + static_cast<int>(threadIdx.x & 31) * 8; }
+  __device__ __forceinline__ float at(int x) const { return usable(FP32 ? __ldg(f + x) : __bfloat162float(b[x])); }
+  // Tokens x .. x + 7; -inf outside the row.
+  __device__ __forceinline__ void load(int x, float* v) const {
+    if (x >= 0 && x + 8 <= V) {
+      if constexpr (FP32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(f + x)), c = __ldg(reinterpret_cast<const float4*>(f + x) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+      } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(b + x));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = usable(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x + i >= 0 && x + i < V ? at(x + i) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void load_draft(int x, float* v) const {
+    if (x >= 0 && x + 8 <= V && (reinterpret_cast<uintptr_t>(q + x) & 15) == 0) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(q + x)), c = __ldg(reinterpret_cast<const float4*>(q + x) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x + i >= 0 && x + i < V ? __ldg(q + x + i) : 0.f;
+    }
+  }
+};
+
+struct Shared {
+  float2 table[128];
+  float2 T[kMaxNodes];             // what q was multiplied with, child by child
+  long long tile[kMaxTiles];       // this CTA's tiles' sums
+  long long total[kMaxCluster];    // each CTA's sum
+  long long gather[2][kMaxCluster];
+  long long warp[kWarps];
+  int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
+  float u[kMaxNodes];
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Every CTA's value to every CTA, in gather[phase]; whole CTA.  A buffer is
+// written again after the barrier of the exchange between, which every CTA
+// enters only when it is done reading this one.
+__device__ __forceinline__ void exchange(long long v, Shared& s, int& phase, uint32_t rank, uint32_t size) {
+  phase ^= 1;
+  if (size == 1) {
+    if (threadIdx.x == 0) s.gather[phase][0] = v;
+    __syncthreads();
+    return;
+  }
+  if (threadIdx.x < size) store_to(threadIdx.x, &s.gather[phase][rank], v);
+  cluster_sync();
+}
+
+// A row's maximum as an integer key that orders as (value, lowest token first):
+// the value's bits made monotonic above the inverted token.
+__device__ __forceinline__ long long max_key(float v, int x) {
+  const uint32_t b = __float_as_uint(v);
+  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return static_cast<long long>(static_cast<unsigned long long>(k) << 32 | (0xffffffffu - static_cast<uint32_t>(x))) ^ (1ll << 63);
+}
+__device__ __forceinline__ float key_value(long long key) {
+  const uint32_t k = static_cast<uint32_t>(static_cast<unsigned long long>(key ^ (1ll << 63)) >> 32);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ int key_token(long long key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
+
+template <bool FP32>
+__device__ __forceinline__ long long row_max(const Row<FP32>& row, Shared& s, int& phase, uint32_t rank, uint32_t size) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float best = -INFINITY;
+  int where = 0x7fffffff;
+  for (int t = row.begin + warp; t < row.end; t += kWarps) {
+    float v[8];
+    const int x = row.first(t);
+    row.load(x, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (v[i] > best) best = v[i], where = x + i;  // ascending tokens: the first of equals stays
+  }
+  long long key = max_key(best, where);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+  if (lane == 0) s.warp[warp] = key;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) key = max(key, s.warp[w]);
+  exchange(key, s, phase, rank, size);
+  for (uint32_t r = 0; r < size; ++r) key = max(key, s.gather[phase][r]);
+  return key;
+}
+
+// What is left of the weights of tokens x .. x + 7 after m drawn children.
+template <bool FP32>
+__device__ __forceinline__ void left8(const Row<FP32>& row, int x, float M, int m, int gone, const Params& p, const Shared& s,
+                                      long long* out) {
+  float v[8], q[8];
+  row.load(x, v);
+  if (m > 0) row.load_draft(x, q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    Pair a = weight(v[i], M, p, s.table);
+    if (m > 0)
+      for (int n = 0; n < m; ++n) a = without(a, q[i], s.T[n]);
+    out[i] = fixed44(a);
+  }
+  for (int n = 0; n < gone; ++n) {
+    const int i = s.gone[n] - x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i == e) out[e] = 0;
+  }
+}
+
+// The sums of what is left: tiles', CTAs' and, returned, the row's.
+template <bool FP32>
+__device__ __forceinline__ long long row_sum(const Row<FP32>& row, float M, int m, const Params& p, Shared& s, int& phase,
+                                             uint32_t rank, uint32_t size) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long mine = 0;
+  for (int t = row.begin + warp; t < row.end; t += kWarps) {
+    long long w[8], sum = 0;
+    left8(row, row.first(t), M, m, 0, p, s, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += w[i];
+    sum = warp_sum(sum);
+    if (lane == 0) s.tile[t - row.begin] = sum;
+    mine += sum;
+  }
+  if (lane == 0) s.warp[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += s.warp[w];
+  exchange(total, s, phase, rank, size);
+  if (threadIdx.x < size) s.total[threadIdx.x] = s.gather[phase][threadIdx.x];
+  total = 0;
+  for (uint32_t r = 0; r < size; ++r) total += s.gather[phase][r];
+  __syncthreads();
+  return total;
+}
+
+// The first token whose running sum exceeds `target` (below the sum of all), by
+// the CTA whose part it is in.
+template <bool FP32>
+__device__ __forceinline__ void find_token(const Row<FP32>& row, long long target, float M, int m, int gone, const Params& p,
+                                           const Shared& s, uint32_t rank, int* where) {
+  long long before = 0;
+  for (uint32_t r = 0; r < rank; ++r) before += s.total[r];
+  if (threadIdx.x >= 32 || target < before || target >= before + s.total[rank]) return;
+  const int lane = threadIdx.x;
+  auto scan = [&](long long v) {  // inclusive, over the lanes
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += y;
+    }
+    return v;
+  };
+  for (int t0 = row.begin; t0 < row.end; t0 += 32) {
+    const long long v = t0 + lane < row.end ? s.tile[t0 + lane - row.begin] : 0;
+    const long long c = before + scan(v);
+    const uint32_t past = __ballot_sync(0xffffffffu, c > target);
+    if (past == 0) {
+      before = __shfl_sync(0xffffffffu, c, 31);
+      continue;
+    }
+    const int l = __ffs(past) - 1;
+    before = __shfl_sync(0xffffffffu, c - v, l);
+    long long w[8], sum = 0;
+    const int x = row.first(t0 + l);
+    left8(row, x, M, m, gone, p, s, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += w[i];
+    long long at = before + scan(sum) - sum;
+    int found = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at += w[i];
+      if (found < 0 && at > target) found = x + i;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, found >= 0);
+    if (hit != 0 && lane == __ffs(hit) - 1) *where = found;
+    return;
+  }
+}
+
+template <bool FP32>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
+  __shared__ Shared s;
+  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const long long seq = blockIdx.x / size, node0 = seq * p.n_nodes;
+  const bool writer = rank == 0 && threadIdx.x == 0;
+  if (threadIdx.x < 128) s.table[threadIdx.x] = kExp2[threadIdx.x];
+  if (threadIdx.x < p.n_nodes) {
+    s.parents[threadIdx.x] = p.parents[node0 + threadIdx.x];
+    s.tokens[threadIdx.x] = p.tokens[node0 + threadIdx.x];
+    s.u[threadIdx.x] = p.uniforms[node0 + threadIdx.x];
+    if (rank == 0) p.path[node0 + threadIdx.x] = -1;
+  }
+  __syncthreads();
+  int kept = 0, phase = 0, cur = s.parents[0] == -1 ? 0 : -1;
+  if (writer) p.next_token[seq] = -1;
+  // Every CTA takes the same way: each decision is made from s.u, s.tokens and sums that all have.
+  while (cur >= 0) {
+    if (writer) p.path[node0 + kept] = cur;
+    ++kept;
+    const Row<FP32> row(p, node0 + cur, rank, size);
+    const long long top = row_max(row, s, phase, rank, size);
+    const float M = key_value(top);
+    int accepted = -1;
+    if (M == -INFINITY) break;
+    if (p.greedy) {
+      for (int j = cur + 1; j < p.n_nodes && accepted < 0; ++j)
+        if (s.parents[j] == cur && s.tokens[j] == key_token(top)) accepted = j;
+      if (accepted < 0 && writer) p.next_token[seq] = key_token(top);
+      cur = accepted;
+      continue;
+    }
+    int m = 0, gone = 0;
+    bool stale = false;  // the sums in shared memory are not those of m
+    long long T = row_sum(row, M, 0, p, s, phase, rank, size);
+    for (int j = cur + 1; j < p.n_nodes; ++j) {
+      const int x = s.tokens[j];
+      if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
+      Pair a = weight(row.at(x), M, p, s.table);
+      if (row.q) {
+        const float q = __ldg(row.q + x), u = s.u[j];
+        for (int n = 0; n < m; ++n) a = without(a, q, s.T[n]);
+        // u q T < a
+        const float2 t = from_fixed44(T);
+        const float uq = u * q, uq_lo = fmaf(u, q, -uq);
+        const float h = uq * t.x, l = fmaf(uq, t.x, -h) + fmaf(uq, t.y, uq_lo * t.x);
+        if ((h - a.hi) + (l - a.lo) < 0.f) {
+          accepted = j;
+          break;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) s.T[m] = t;
+        __syncthreads();
+        const long long left = row_sum(row, M, m + 1, p, s, phase, rank, size);
+        stale = left <= 0;
+        if (!stale) T = left, ++m;
+      } else {
+        long long w = fixed44(a);
+        for (int n = 0; n < gone; ++n)
+          if (s.gone[n] == x) w = 0;
+        if (static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T))) < w) {
+          accepted = j;
+          break;
+        }
+        if (w == 0 || T - w <= 0) continue;
+        T -= w;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          s.gone[gone] = x;
+          const int tile = (x + row.shift) / kTile;
+          s.total[tile / row.per] -= w;
+          if (tile >= row.begin && tile < row.end) s.tile[tile - row.begin] -= w;
+        }
+        __syncthreads();
+        ++gone;
+      }
+    }
+    if (accepted < 0) {
+      if (stale) row_sum(row, M, m, p, s, phase, rank, size);
+      const long long target = static_cast<long long>(__umul64hi(fraction64(s.u[0]), static_cast<unsigned long long>(T)));
+      find_token(row, target, M, m, gone, p, s, rank, p.next_token + seq);
+    }
+    cur = accepted;
+    __syncthreads();  // shared sums have been read
+  }
+  if (writer) p.n_kept[seq] = kept;
+  if (size > 1) cluster_sync();  // no CTA leaves while another may still store to it
+}
+
+}  // namespace verify
+}  // namespace fa
