@@ -22,7 +22,7 @@ DEPENDS = SOURCES + [
     os.path.join(PKG, "csrc", n)
     for n in ("fa_fwd_kernel.cuh", "fa_bwd_kernel.cuh", "fa_fp8_quant.cuh", "fa_decode.cuh", "sm103_ptx.cuh", "tma_host.h",
               "fa_internal.h", "fa_packed_kernel.cuh", "fa_packed_plan.h", "fa_kv4.cuh",
-              "fa_kv4_decode.cuh", "fa_kv4_host.h", "fa_rotary.cuh", "fa_verify.cuh", "fa_keep.cuh")
+              "fa_kv4_decode.cuh", "fa_kv4_host.h", "fa_kv4_tree.cuh", "fa_rotary.cuh", "fa_verify.cuh", "fa_keep.cuh")
 ] + [os.path.join(ROOT, "include", n) for n in ("fa_gb300.h", "fa_gb300_serve.h", "fa_gb300_rotary.h", "fa_gb300_draft.h")]
 
 COMPILE_FLAGS = [

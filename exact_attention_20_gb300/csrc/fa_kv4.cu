@@ -11,15 +11,18 @@
 #include "fa_internal.h"
 #include "fa_kv4_decode.cuh"
 #include "fa_kv4_host.h"
+#include "fa_kv4_tree.cuh"
 
 namespace {
 
 namespace kv = fa::kv4;
 using namespace fa_internal;
 
-constexpr int kMaxNodes = 64;  // of a tree: a node's line is one word
+constexpr int kMaxNodes = kv::kMaxTreeNodes;
+constexpr int kTreeRows = 16;  // rows of a KV head above which a tree goes to the tensor core's 128-row tiles
 
 std::mutex g_mu;
+bool g_tree_attr[kMaxDevices][2];  // of tree_kernel: [d == 128]
 bool g_attr[kMaxDevices][2][2][3];  // shared-memory attribute set: [tree][d == 128][row tiles of 8, 16, 32]
 
 int move(bool store, const void* k, const void* v, void* k_out, void* v_out, void* cache, const int* page_table,
@@ -118,6 +121,61 @@ DecodePlan decode_plan(int n_seqs, int Lq, int G, int Hkv, int d, int max_pages,
   return pl;
 }
 
+// The same for a tree's rows in tiles of 128, with keys in tiles of 128.
+DecodePlan tree_plan(int n_seqs, int nodes, int G, int Hkv, int d, int max_pages, int page_size, int num_sms) {
+  namespace tr = kv::tree;
+  DecodePlan pl{};
+  pl.row_tiles = (nodes * G + tr::kRows - 1) / tr::kRows;
+  const long long items = static_cast<long long>(n_seqs) * Hkv * pl.row_tiles;
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + tr::kKeys - 1) / tr::kKeys;  // of an item, at most
+  // Few short items are taken whole, one by each CTA: nothing to merge.
+  pl.split = items > num_sms || tiles > 2 * tr::kMinTiles;
+  if (!pl.split) {
+    pl.grid = items;
+    return pl;
+  }
+  pl.grid = std::min(static_cast<long long>(num_sms),
+                     (items * std::min(tiles + tr::kItemTiles, 1ll << 26) + tr::kMinTiles - 1) / tr::kMinTiles);
+  const size_t rows = static_cast<size_t>(pl.grid) * 2 * tr::kRows;  // parts: two of a CTA, and their (m, l); then the cuts
+  pl.bytes = rows * d * 4 + rows * 8 + static_cast<size_t>(pl.grid) * sizeof(kv::Cut);
+  return pl;
+}
+
+bool tensor_tiles(bool tree, int Lq, int G) { return tree && Lq * G > kTreeRows; }
+
+template <int D>
+int launch_merge(const kv::DecodeParams& p, const DecodePlan& pl, int rows, cudaStream_t stream) {
+  // the merge may be set up while the first kernel runs; its CTAs wait for it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), rows / kv::kMergeRows);
+  cfg.blockDim = dim3(kv::kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv::merge_kernel<D>, p, rows) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <int D>
+int launch_tree(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cudaStream_t stream) {
+  auto kernel = kv::tree::tree_kernel<D>;
+  constexpr int smem = kv::tree::Cfg<D>::kSmemBytes;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    bool& set = g_tree_attr[dev][D == 128];
+    if (!set) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return FA_ERR_LAUNCH;
+      set = true;
+    }
+  }
+  kernel<<<static_cast<int>(pl.grid), kv::tree::kThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+  return pl.split ? launch_merge<D>(p, pl, kv::tree::kRows, stream) : FA_OK;
+}
+
 template <int D, int NT, bool TREE>
 int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cudaStream_t stream) {
   auto kernel = kv::decode_kernel<D, NT, TREE>;
@@ -133,20 +191,16 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
   }
   kernel<<<static_cast<int>(pl.grid), kv::DecodeCfg<D, NT>::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  if (!pl.split) return FA_OK;
-  // the merge may be set up while the first kernel runs; its CTAs wait for it
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 8 * NT / kv::kMergeRows);
-  cfg.blockDim = dim3(kv::kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv::merge_kernel<D>, p, 8 * NT) != cudaSuccess)
-    return FA_ERR_LAUNCH;
-  return FA_OK;
+  return pl.split ? launch_merge<D>(p, pl, 8 * NT, stream) : FA_OK;
+}
+
+template <bool TREE>
+int launch_rows(const kv::DecodeParams& p, const DecodePlan& pl, int d, int dev, cudaStream_t s) {
+  if (d == 128)
+    return pl.nt == 1 ? launch_decode<128, 1, TREE>(p, pl, dev, s)
+         : pl.nt == 2 ? launch_decode<128, 2, TREE>(p, pl, dev, s) : launch_decode<128, 4, TREE>(p, pl, dev, s);
+  return pl.nt == 1 ? launch_decode<64, 1, TREE>(p, pl, dev, s)
+       : pl.nt == 2 ? launch_decode<64, 2, TREE>(p, pl, dev, s) : launch_decode<64, 4, TREE>(p, pl, dev, s);
 }
 
 int check_decode_sizes(int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages, int page_size) {
@@ -160,13 +214,17 @@ int check_decode_sizes(int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages
   return FA_OK;
 }
 
-template <bool TREE>
-int launch_rows(const kv::DecodeParams& p, const DecodePlan& pl, int d, int dev, cudaStream_t s) {
-  if (d == 128)
-    return pl.nt == 1 ? launch_decode<128, 1, TREE>(p, pl, dev, s)
-         : pl.nt == 2 ? launch_decode<128, 2, TREE>(p, pl, dev, s) : launch_decode<128, 4, TREE>(p, pl, dev, s);
-  return pl.nt == 1 ? launch_decode<64, 1, TREE>(p, pl, dev, s)
-       : pl.nt == 2 ? launch_decode<64, 2, TREE>(p, pl, dev, s) : launch_decode<64, 4, TREE>(p, pl, dev, s);
+int attention_workspace(bool tree, int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages, int page_size, size_t* bytes) {
+  if (bytes == nullptr) return FA_ERR_NULL;
+  int rc = check_decode_sizes(n_seqs, Lq, Hq, Hkv, d, max_pages, page_size);
+  if (rc != FA_OK) return rc;
+  int dev = 0;
+  fa_internal::DeviceView view;
+  rc = current(&dev, &view);
+  if (rc != FA_OK) return rc;
+  const auto plan = tensor_tiles(tree, Lq, Hq / Hkv) ? tree_plan : decode_plan;
+  *bytes = n_seqs == 0 ? 0 : plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms).bytes;
+  return FA_OK;
 }
 
 // The attention of the newest tokens, in order or as a tree's nodes.
@@ -208,7 +266,8 @@ int attention(bool tree, const void* q, const void* cache, const int* page_table
   fa_internal::DeviceView view;
   rc = current(&dev, &view);
   if (rc != FA_OK) return rc;
-  const DecodePlan pl = decode_plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms);
+  const bool tiles = tensor_tiles(tree, Lq, Hq / Hkv);
+  const DecodePlan pl = (tiles ? tree_plan : decode_plan)(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms);
   if (pl.bytes > 0 && (workspace == nullptr || workspace_bytes < pl.bytes)) return FA_ERR_SCRATCH;
   kv::DecodeParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -217,10 +276,10 @@ int attention(bool tree, const void* q, const void* cache, const int* page_table
   p.seq_lens = seq_lens;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  const long long rows = pl.grid * 8 * pl.nt;
+  const long long rows = pl.grid * (tiles ? kv::tree::kRows : 8 * pl.nt);
   p.part_o = static_cast<float*>(workspace);
   p.first_o = p.part_o + 2 * rows * d;
-  p.part_ml = reinterpret_cast<float2*>(p.first_o + kv::kMaxWarps * rows * d);
+  p.part_ml = reinterpret_cast<float2*>(p.first_o + (tiles ? 0 : kv::kMaxWarps * rows * d));
   p.cuts = reinterpret_cast<kv::Cut*>(p.part_ml + 2 * rows);
   p.errors = errors;
   p.status = view.status;
@@ -240,6 +299,7 @@ int attention(bool tree, const void* q, const void* cache, const int* page_table
   p.split = pl.split;
   p.parents = parents;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tiles) return d == 128 ? launch_tree<128>(p, pl, dev, s) : launch_tree<64>(p, pl, dev, s);
   return tree ? launch_rows<true>(p, pl, d, dev, s) : launch_rows<false>(p, pl, d, dev, s);
 }
 
@@ -264,15 +324,7 @@ int fa_kv4_load(const void* cache, const int* page_table, const int* seq_lens, c
 
 int fa_kv4_attention_workspace(int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages, int page_size,
                                size_t* bytes) {
-  if (bytes == nullptr) return FA_ERR_NULL;
-  int rc = check_decode_sizes(n_seqs, Lq, Hq, Hkv, d, max_pages, page_size);
-  if (rc != FA_OK) return rc;
-  int dev = 0;
-  fa_internal::DeviceView view;
-  rc = current(&dev, &view);
-  if (rc != FA_OK) return rc;
-  *bytes = n_seqs == 0 ? 0 : decode_plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms).bytes;
-  return FA_OK;
+  return attention_workspace(false, n_seqs, Lq, Hq, Hkv, d, max_pages, page_size, bytes);
 }
 
 int fa_kv4_attention(const void* q, const void* cache, const int* page_table, const int* seq_lens, void* o, float* lse,
@@ -286,7 +338,7 @@ int fa_kv4_attention(const void* q, const void* cache, const int* page_table, co
 int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, int d, int max_pages, int page_size,
                                     size_t* bytes) {
   if (n_nodes > kMaxNodes) return FA_ERR_INVALID_ARG;
-  return fa_kv4_attention_workspace(n_seqs, n_nodes, Hq, Hkv, d, max_pages, page_size, bytes);
+  return attention_workspace(true, n_seqs, n_nodes, Hq, Hkv, d, max_pages, page_size, bytes);
 }
 
 int fa_kv4_tree_attention(const void* q, const void* cache, const int* page_table, const int* seq_lens,

@@ -40,6 +40,7 @@ __host__ __device__ constexpr int scales_at(int d, int v) { return codes_at(d, v
 // What a call's `errors` word may hold (bits).
 constexpr int kErrPage = 1;      // a page id outside [0, num_pages)
 constexpr int kErrPosition = 2;  // a token before position 0 or past the table's pages
+constexpr int kMaxTreeNodes = 64;  // a node's line is one word
 constexpr int kErrTree = 4;      // a node whose parent does not come before it
 
 // Two e4m3 values (low byte first) to f16, exact.

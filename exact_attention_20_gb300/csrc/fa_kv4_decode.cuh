@@ -129,7 +129,8 @@ __device__ __forceinline__ int data_units(int len) { return (len + kUnit - 1) / 
 __device__ __forceinline__ int units_of(int len) { return max(1, data_units(len)); }
 __device__ __forceinline__ int cost_of(int len) { return units_of(len) + kItemUnits; }
 
-// Exclusive scan of one value per thread over the block, and the total.
+// Exclusive scan of one value per thread over the block (of at most WARPS warps), and the total.
+template <int WARPS = kMaxWarps>
 __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
@@ -143,7 +144,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_sums, 
   long long before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kMaxWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w * 32 >= static_cast<int>(blockDim.x)) break;
     if (w < warp) before += s_sums[w];
     total += s_sums[w];

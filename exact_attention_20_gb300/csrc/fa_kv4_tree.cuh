@@ -1,0 +1,791 @@
+// Attention of a tree of drafted tokens over the paged 4-bit cache on the
+// tensor core (tcgen05), for trees whose rows fill a good part of its 128.
+//
+// Row r of an item is node r / G of the tree and query head r % G of the item's
+// KV head; it sees the context and the nodes on its line (tree_line):
+//
+//     O = sum_j softmax_j(scale q . k_j) v_j,   L = ln sum_j exp(scale q . k_j).
+//
+// fa_kv4_decode.cuh turns a lane's codes into its own operands of mma.sync, all
+// over again for every 8 to 32 rows; here a tile of 128 keys is turned into f16
+// once, in shared memory, for 128 rows:
+//
+// - Codes times scales are exact in f16 (fa_kv4.cuh).  Q rows are brought to
+//   [2^14, 2^15) by a power of two, P lies in [0, 2^15) with a maximum at 2^8 when
+//   the reference is set: as in fa_kv4_decode.cuh, f16 then loses nothing above
+//   2^-33 of the maximum, P's rounding is 2^-11, every sum is fp32.
+// - Two softmax warpgroups, one row a thread, take a CTA's tiles in turn, each
+//   with its own S, P and O in tensor memory, its own running maximum and sum and
+//   its own issuer, so that one's products overlap the other's exponentials and
+//   neither waits for the other's maximum.  An item's two states meet at its end.
+// - Eight warps turn codes into operands, a group of 16 keys each, from rings of
+//   their own (bulk copies some tiles ahead, across items).  A tile's K and V each
+//   have two places in shared memory, one for each warpgroup.
+//
+// What a row does not see must not reach it: scores are replaced by -inf, bit by
+// bit of the row's line; of V, keys past the sequence's end and blocks that are NaN
+// at a tree's node are zeros in the product (0 * NaN is NaN), the latter being
+// set to NaN at the end in the rows that see the node.
+//
+// Work: the (sequence, KV head, row tile) items' tiles, concatenated, are cut
+// into ranges of equal cost, one per CTA, from the lengths on the device; an item
+// cut between CTAs is merged by merge_kernel (fa_kv4_decode.cuh).
+//
+// Warps: 0-7 softmax; 8-15 codes to operands; 16, 17 MMA issuers.
+#pragma once
+
+#include "fa_kv4_decode.cuh"
+
+namespace fa {
+namespace kv4 {
+namespace tree {
+
+constexpr int kRows = 128;             // of an item
+constexpr int kKeys = 128;             // of a tile
+constexpr int kTurnWarps = 8;          // a tile's groups
+constexpr int kThreads = 640;
+constexpr int kItemTiles = 2;          // an item's own cost, in tiles
+constexpr int kMinTiles = 2;           // a CTA takes at least, where there are that many
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSiteTree = 8;           // status code: a wait gave up
+// Registers: the launch gives every thread 96 (65536 / 640, rounded down to 8).
+constexpr uint32_t kRegsSoftmax = 136, kRegsTurn = 72, kRegsIssue = 64;
+static_assert(256 * kRegsSoftmax + 256 * kRegsTurn + 128 * kRegsIssue <= kThreads * 96, "register split exceeds the launch");
+
+template <int D>
+struct Cfg {
+  static constexpr int kSlabs = D / 64;                 // 64 columns of d each
+  static constexpr int kSlabBytes = 128 * 128;          // 128 rows of 128 bytes
+  static constexpr int kTileBytes = kSlabs * kSlabBytes;
+  static constexpr int kRing = D == 128 ? 3 : 6;        // tiles ahead, of a turning warp's group
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kTileBytes;              // two places
+  static constexpr int kVOff = kKOff + 2 * kTileBytes;  // two places
+  static constexpr int kRawOff = kVOff + 2 * kTileBytes;
+  static constexpr int kWarpRaw = kRing * group_bytes(D);
+  static constexpr int kBarOff = kRawOff + kTurnWarps * kWarpRaw;
+  static constexpr int kNumBars = kTurnWarps * kRing + 4 * 2 + 1 + 3 * 2 + 2 + 1;
+  static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + alignment slack
+  static_assert(kSmemBytes + 4096 <= 232448, "227 KB with the static part");
+  // Tensor memory: S and O of each warpgroup; P over S, or at d = 64 beside O
+  static constexpr int kTmemS = 0, kTmemO = 256, kTmemP = D == 64 ? kTmemO + 64 : kTmemS, kTmemGroup = 128;
+};
+
+struct Bars {
+  uint32_t raw0;                            // [warp][kRing]
+  uint32_t k_full, k_empty, v_full, v_empty;  // [2] each
+  uint32_t q_full;
+  uint32_t s_full, p_ready, o_done;         // [2] each
+  uint32_t states, written;                 // between the warpgroups: an item's states are there; its O has been read
+  uint32_t drain;
+  volatile int* abort_flag;
+};
+
+// kv4's costs and walk over the concatenated items, in tiles of 128 keys.
+__device__ __forceinline__ int data_tiles(int len) { return (len + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int tiles_of(int len) { return max(1, data_tiles(len)); }
+__device__ __forceinline__ int tile_cost(int len) { return tiles_of(len) + kItemTiles; }
+
+// A CTA's place in the concatenated items: the segment (tiles of one item) it is at.
+struct Segments {
+  int s, item;     // sequence, item within it (head * row_tiles + row tile)
+  int len, tiles;  // the sequence's
+  int t0, count;   // the segment's tiles: [t0, t0 + count); none where the range ends within the item's own cost
+  int take, left;  // the segment's cost; that from here to the end of the range (0: done)
+  __device__ __forceinline__ void set(int at) {
+    take = min(tiles + kItemTiles - at, left);
+    t0 = max(0, at - kItemTiles);
+    count = max(0, at + take - kItemTiles - t0);
+  }
+  __device__ __forceinline__ void next(const DecodeParams& p) {
+    left -= take;
+    if (left <= 0) return;
+    if (++item == p.Hkv * p.row_tiles) {
+      item = 0;
+      ++s;
+      len = tokens_of(s, p);
+      tiles = tiles_of(len);
+    }
+    set(0);
+  }
+  // To the next segment with a share in its item, from the present one on.
+  __device__ __forceinline__ void skip_empty(const DecodeParams& p) {
+    while (left > 0 && count == 0) next(p);
+  }
+  __device__ __forceinline__ int data() const { return max(0, min(t0 + count, data_tiles(len)) - t0); }  // tiles with tokens
+  __device__ __forceinline__ bool whole() const { return count == tiles; }
+};
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& b, const DecodeParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t polls = 0;
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((++polls & 31u) == 0u) {
+      if (*b.abort_flag) return false;
+      if (global_timer_ns() - t0 > p.wait_limit_ns) {
+        *b.abort_flag = 1;
+        atomicCAS(p.status, 0, kSiteTree);
+        return false;
+      }
+    }
+  }
+}
+
+// What the warps pass each other beside the barriers.
+struct Notes {
+  uint32_t skip[4][2];                // a tile's groups whose page was refused (a byte each), by tile number mod 4
+  uint32_t nan[4][kMaxTreeNodes];     // by item number mod 4: (item number << 8) | V blocks of a node that are NaN
+  uint32_t any_nan[4];                // the item number + 1 where there is one
+  float2 ml[2][kRows];                // the warpgroups' running maxima and sums
+};
+
+// ---------------------------------------------------------------------------
+// Codes to operands (one warp: a tile's keys 16 w .. 16 w + 15)
+// ---------------------------------------------------------------------------
+// Half of a group, K or V (16 keys x D), into rows key0 .. of a tile: blocks of 16
+// elements, four or two a lane.  A row is 128 bytes of each 64-column slab, its
+// 16-byte chunks permuted by the row's low bits as the 128-byte swizzle wants;
+// the lanes' blocks are dealt so that eight lanes' chunks fall into all banks.
+// scale_of(key, block, byte) may change a block's scale.
+template <int D, class Scale>
+__device__ __forceinline__ void turn_group(const uint8_t* raw, uint8_t* tile, int key0, Scale scale_of) {
+  constexpr int kKeysAtOnce = 32 * 16 / D;
+  const int lane = threadIdx.x & 31;
+  const int block = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+  const int key_in = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
+  uint2 codes[kGroup / kKeysAtOnce];
+  uint32_t scales[kGroup / kKeysAtOnce];
+#pragma unroll
+  for (int i = 0; i < kGroup / kKeysAtOnce; ++i) {
+    const int key = i * kKeysAtOnce + key_in;
+    codes[i] = *reinterpret_cast<const uint2*>(raw + key * (D / 2) + block * 8);
+    scales[i] = raw[kGroup * D / 2 + key * (D / 16) + block];
+  }
+#pragma unroll
+  for (int i = 0; i < kGroup / kKeysAtOnce; ++i) {
+    const int key = i * kKeysAtOnce + key_in, row = key0 + key;
+    const uint32_t sb = scale_of(key, block, scales[i]);
+    const uint32_t s = e4m3x2_to_f16x2(sb | (sb << 8));
+    uint32_t x[8];
+    e2m1x8_to_f16x2(codes[i].x, x);
+    e2m1x8_to_f16x2(codes[i].y, x + 4);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x[n] = f16x2_mul(x[n], s);
+    uint8_t* at = tile + (block >> 2) * Cfg<D>::kSlabBytes + row * 128;
+    const int chunk = (block & 3) * 2;
+    *reinterpret_cast<uint4*>(at + ((chunk ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ (row & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// Zeros in place of a group that was not loaded.
+template <int D>
+__device__ __forceinline__ void zero_group(uint8_t* tile, int key0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < Cfg<D>::kSlabs * kGroup * 8 / 32; ++i) {
+    const int n = i * 32 + lane;
+    *reinterpret_cast<uint4*>(tile + n / (kGroup * 8) * Cfg<D>::kSlabBytes + key0 * 128 + n % (kGroup * 8) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, const Bars& b, Notes& notes, const DecodeParams& p) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint8_t* raw = smem + C::kRawOff + w * C::kWarpRaw;
+  const uint32_t raw_u32 = smem_u32(raw), raw_bar = b.raw0 + w * C::kRing * 8;
+  const int group_shift = p.page_shift - 4;
+  const long long head_bytes = static_cast<long long>(row_bytes(D)) << p.page_shift, page_bytes = head_bytes * p.Hkv;
+
+  // Loads run kRing tiles ahead, across segments.  Up to 32 tiles' groups are
+  // looked up together, one by each lane, which later issues its copy.
+  Segments ahead = seg;
+  int ahead_at = 0;                          // tiles of `ahead` that were looked up
+  const uint8_t* src = nullptr;
+  uint32_t loaded = 0, refused = 0;          // of those looked up
+  int batch = 0, next = 0;
+  uint32_t issued = 0;                       // tiles
+  uint32_t stage_loaded = 0, stage_refused = 0;  // bit per ring place
+  auto look_up = [&]() {
+    batch = next = 0;
+    while (ahead.left > 0 && ahead_at >= ahead.data()) {
+      ahead.next(p);
+      ahead_at = 0;
+    }
+    if (ahead.left <= 0) return;
+    batch = min(32, ahead.data() - ahead_at);
+    const int group = (ahead.t0 + ahead_at + lane) * (kKeys / kGroup) + w;
+    const bool exists = lane < batch && group < (ahead.len + kGroup - 1) / kGroup;
+    int page = -1;
+    if (exists) page = __ldg(p.page_table + static_cast<long long>(ahead.s) * p.max_pages + (group >> group_shift));
+    const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages);
+    src = p.cache + page * page_bytes + head_bytes * (ahead.item / p.row_tiles) +
+          static_cast<long long>(group & ((1 << group_shift) - 1)) * group_bytes(D);
+    loaded = __ballot_sync(0xffffffffu, ok);
+    refused = __ballot_sync(0xffffffffu, exists && !ok);
+    if (p.errors && exists && !ok) atomicOr(p.errors, kErrPage);
+    ahead_at += batch;
+  };
+  auto issue = [&]() {
+    if (next == batch) {
+      look_up();
+      if (batch == 0) return;
+    }
+    const uint32_t st = issued % C::kRing, bar = raw_bar + 8 * st;
+    const uint32_t on = loaded >> next & 1u;
+    stage_loaded = (stage_loaded & ~(1u << st)) | on << st;
+    stage_refused = (stage_refused & ~(1u << st)) | (refused >> next & 1u) << st;
+    if (lane == next) {
+      if (on) {
+        mbar_arrive_expect_tx(bar, group_bytes(D));
+        bulk_load(raw_u32 + st * group_bytes(D), src, group_bytes(D), bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    ++next;
+    ++issued;
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::kRing; ++i) issue();
+
+  uint32_t c = 0;       // tiles taken
+  uint32_t number = 0;  // items with tiles
+  bool ok = true;
+  const int key0 = w * kGroup;
+  auto arrive = [&](uint32_t bar) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+#pragma unroll 1
+  for (; seg.left > 0 && ok; seg.next(p)) {
+    const int n = seg.data();
+    if (n == 0) continue;
+    const int prefix = seg.len - p.Lq;
+#pragma unroll 1
+    for (int t = seg.t0; t < seg.t0 + n; ++t, ++c) {
+      const uint32_t st = c % C::kRing, place = c & 1u, use = c >> 1;
+      const int pos = t * kKeys + key0;
+      const bool on = stage_loaded >> st & 1u;
+      ok = __all_sync(0xffffffffu, wait(raw_bar + 8 * st, c / C::kRing & 1u, b, p) && wait(b.k_empty + 8 * place, (use & 1u) ^ 1u, b, p));
+      if (!ok) break;
+      if (lane == 0) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[w] = stage_refused >> st & 1u ? 0xffu : 0u;
+      const uint8_t* group = raw + st * group_bytes(D);
+      uint8_t* k_tile = smem + C::kKOff + place * C::kTileBytes;
+      uint8_t* v_tile = smem + C::kVOff + place * C::kTileBytes;
+      const int live = seg.len - pos;  // keys of the group that are the sequence's, if fewer than 16
+      if (!on) {
+        zero_group<D>(k_tile, key0);
+      } else if (live >= kGroup) {
+        turn_group<D>(group, k_tile, key0, [](int, int, uint32_t s) { return s; });
+      } else {
+        turn_group<D>(group, k_tile, key0, [&](int key, int, uint32_t s) { return key < live ? s : 0u; });
+      }
+      arrive(b.k_full + 8 * place);
+      ok = __all_sync(0xffffffffu, wait(b.v_empty + 8 * place, (use & 1u) ^ 1u, b, p));
+      if (!ok) break;
+      if (!on) {
+        zero_group<D>(v_tile, key0);
+      } else if (pos + kGroup <= prefix) {
+        turn_group<D>(group + codes_at(D, 1), v_tile, key0, [](int, int, uint32_t s) { return s; });
+      } else {
+        // the tree's nodes, and keys behind the sequence
+        const int node0 = pos - prefix;
+        uint32_t* noted = notes.nan[number & 3u];
+        if (lane < kGroup && node0 + lane >= 0 && node0 + lane < p.Lq) noted[node0 + lane] = number << 8;
+        __syncwarp();
+        turn_group<D>(group + codes_at(D, 1), v_tile, key0, [&](int key, int block, uint32_t s) {
+          if (key >= live) return 0u;
+          if ((s & 0x7fu) == 0x7fu && node0 + key >= 0) {
+            atomicOr(noted + node0 + key, 1u << block);
+            notes.any_nan[number & 3u] = number + 1;
+            return 0u;
+          }
+          return s;
+        });
+      }
+      arrive(b.v_full + 8 * place);  // every lane has read the group
+      issue();
+    }
+    ++number;
+  }
+  // Copies still in flight land before the CTA exits (only after a wait gave up).
+  for (uint32_t i = c; i < issued; ++i) mbar_wait_bounded(raw_bar + 8 * (i % C::kRing), i / C::kRing & 1u, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuers (warp g: the products of softmax warpgroup g)
+// ---------------------------------------------------------------------------
+// Instruction descriptor for kind::f16 with f16 A and B and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <int D>
+__device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t tmem, Segments seg, const Bars& b, const DecodeParams& p) {
+  using C = Cfg<D>;
+  const bool leader = (threadIdx.x & 31) == 0;
+  const uint64_t q_desc = sdesc_sw128(sbase + C::kQOff, 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(sbase + C::kKOff + g * C::kTileBytes, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(sbase + C::kVOff + g * C::kTileBytes, C::kSlabBytes, 1024);
+  const uint32_t tm_s = tmem + C::kTmemS + g * C::kTmemGroup, tm_p = tmem + C::kTmemP + g * C::kTmemGroup;
+  const uint32_t tm_o = tmem + C::kTmemO + g * C::kTmemGroup;
+  bool ok = true;
+  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(bar, parity, b, p)); };
+  uint32_t c = 0, uses = 0, items = 0;  // tiles; this warpgroup's; items with tiles
+  auto qk = [&]() {
+    wait_voted(b.k_full + 8 * g, uses & 1u);
+    if (!ok) return;
+    tc_fence_after_sync();
+    if (leader) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
+        umma_ss(tm_s, sdesc_advance(q_desc, off), sdesc_advance(k_desc, off), idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+      }
+      umma_commit(b.s_full + 8 * g);
+      umma_commit(b.k_empty + 8 * g);
+    }
+    __syncwarp();
+  };
+#pragma unroll 1
+  for (; seg.left > 0 && ok; seg.next(p)) {
+    const int n = seg.data();
+    if (n == 0) continue;
+    const int mine = (n + ((c & 1u) == g ? 1 : 0)) / 2;  // of the segment's tiles, dealt in turn
+    c += n;
+    wait_voted(b.q_full, items & 1u);
+    ++items;
+    if (mine > 0 && ok) qk();
+#pragma unroll 1
+    for (int i = 0; i < mine && ok; ++i) {
+      wait_voted(b.v_full + 8 * g, uses & 1u);
+      wait_voted(b.p_ready + 8 * g, uses & 1u);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_ts(tm_o, tm_p + kk * 8, sdesc_advance(v_desc, kk * 2048), idesc_f16_f32(kRows, D, true), i > 0 || kk > 0 ? 1u : 0u);
+        umma_commit(b.v_empty + 8 * g);
+        if (i == mine - 1) umma_commit(b.o_done + 8 * g);
+      }
+      __syncwarp();
+      ++uses;
+      if (i < mine - 1) qk();
+    }
+  }
+  // Every MMA this thread issued must finish before tensor memory is released.
+  if (leader) umma_commit(b.drain);
+  __syncwarp();
+  mbar_wait_bounded(b.drain, 0, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and output (warpgroup g: one row a thread)
+// ---------------------------------------------------------------------------
+// A row of an item: what it sees, and the factor from its scores to log2 units.
+struct RowState {
+  unsigned long long line;  // 0: sees nothing, or no such row
+  float factor;
+};
+
+template <int D>
+__device__ __forceinline__ RowState load_row(int g, int row, uint8_t* smem, const Segments& seg, const DecodeParams& p) {
+  // both warpgroups look for the row's largest element, each writes its half of the row
+  const int h = seg.item / p.row_tiles, r = (seg.item - h * p.row_tiles) * kRows + row, node = r / p.G;
+  const bool exists = node < p.Lq;
+  RowState st{0ull, 1.f};
+  if (exists) st.line = tree_line(p.parents + static_cast<long long>(seg.s) * p.Lq, node, seg.len - p.Lq);
+  const __nv_bfloat16* src = p.q + (static_cast<long long>(seg.s) * p.Lq + node) * p.q_stride +
+                             static_cast<long long>(h * p.G + r - node * p.G) * D;
+  uint32_t m2 = 0;
+#pragma unroll 4
+  for (int n = 0; n < D / 8; ++n) {
+    const uint4 x = exists ? __ldg(reinterpret_cast<const uint4*>(src) + n) : make_uint4(0, 0, 0, 0);
+    m2 = __vmaxu2(m2, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
+    m2 = __vmaxu2(m2, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  }
+  const uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+  const int e = max(static_cast<int>(top >> 7) - 127, -100);  // floor(log2) of the row's largest element
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+  st.factor = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.qk_scale, 1.17549435e-38f);
+#pragma unroll 4
+  for (int n = 0; n < D / 16; ++n) {
+    const int chunk = g * (D / 16) + n;
+    const uint4 x = exists ? __ldg(reinterpret_cast<const uint4*>(src) + chunk) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+    *reinterpret_cast<uint4*>(smem + Cfg<D>::kQOff + (chunk >> 3) * Cfg<D>::kSlabBytes + row * 128 +
+                              (((chunk & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  return st;
+}
+
+template <int D>
+__device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem, Segments seg, const Bars& b, Notes& notes,
+                                            const DecodeParams& p) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t tS = tmem + lane_off + C::kTmemS + g * C::kTmemGroup, tP = tmem + lane_off + C::kTmemP + g * C::kTmemGroup;
+  const uint32_t tO = tmem + lane_off + C::kTmemO;  // warpgroup 0's; 1's kTmemGroup further on
+  bool ok = true;
+  uint32_t c = 0, uses = 0, items = 0, done[2] = {0, 0}, number = 0;
+  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(bar, parity, b, p)); };
+  auto arrive = [&](uint32_t bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  seg.skip_empty(p);
+  RowState st{0ull, 1.f};
+  auto load = [&](const Segments& at) {
+    st = load_row<D>(g, row, smem, at, p);
+    fence_proxy_async_smem();
+    arrive(b.q_full);
+  };
+  if (seg.left > 0 && seg.data() > 0) load(seg);
+#pragma unroll 1
+  while (seg.left > 0 && ok) {
+    const int n = seg.data();
+    const int h = seg.item / p.row_tiles, r0 = (seg.item - h * p.row_tiles) * kRows;
+    const bool live = r0 + quad * 32 < p.Lq * p.G;  // the warp has rows
+    const RowState now = st;
+    float m = kNone, l = 0.f;
+    int mine[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mine[i] = (n + (static_cast<int>(c & 1u) == i ? 1 : 0)) / 2;
+    const int first = seg.t0 + (static_cast<int>(c & 1u) == g ? 0 : 1);  // this warpgroup's tiles: every other one
+    const int prefix = seg.len - p.Lq;
+#pragma unroll 1
+    for (int i = 0; i < (g ? mine[1] : mine[0]) && ok; ++i) {
+      const int t = first + 2 * i;
+      wait_voted(b.s_full + 8 * g, uses & 1u);
+      if (!ok) break;
+      ++uses;
+      if (live) {
+        tc_fence_after_sync();
+        const uint32_t number_of_tile = c + static_cast<uint32_t>(t - seg.t0);
+        const volatile uint32_t* refusals = notes.skip[number_of_tile & 3u];
+        const uint2 skip = make_uint2(refusals[0], refusals[1]);
+        const bool masked = (t + 1) * kKeys > prefix || (skip.x | skip.y) != 0;
+        // columns 64 h ... of the tile: bit e set where the row sees key 64 h + e
+        auto seen64 = [&](int h2) {
+          const int node0 = t * kKeys + h2 * 64 - prefix;
+          unsigned long long v = node0 >= 64 ? 0ull : node0 >= 0 ? now.line >> node0
+                                 : node0 <= -64 ? ~0ull : (now.line << -node0) | ((1ull << -node0) - 1ull);
+          const uint32_t refused = h2 ? skip.y : skip.x;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (refused >> (8 * q) & 1u) v &= ~(0xffffull << (16 * q));
+          return v;
+        };
+        auto load64 = [&](int h2, uint32_t* x) {
+          tmem_ld64_wait(tS + h2 * 64, x);
+          if (masked) {
+            const unsigned long long v = seen64(h2);
+            const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+              if (!(hi >> e & 1u)) x[32 + e] = __float_as_uint(-INFINITY);
+            }
+          }
+        };
+        uint32_t x[64];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maxima = [&]() {
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) mx[e >> 1 & 3] = fmax3(mx[e >> 1 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        };
+        load64(1, x);
+        maxima();
+        load64(0, x);
+        maxima();
+        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * now.factor;
+        if (__any_sync(0xffffffffu, top - m > kLift + kMove)) {
+          const float to = fmaxf(m, top - kLift);
+          const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
+          m = to;
+          l *= alpha;
+          if (i > 0) {  // O holds the sum so far: its last product was done before S was
+            const uint32_t mine_o = tO + g * C::kTmemGroup;
+#pragma unroll 1
+            for (int e = 0; e < D / 32; ++e) {
+              uint32_t o[32];
+              tmem_ld32_wait(mine_o + e * 32, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(mine_o + e * 32, o);
+            }
+          }
+        }
+        const uint64_t f2 = f2_pack(now.factor, now.factor), neg_m2 = f2_pack(-m, -m);
+        uint64_t sum2 = f2_pack(0.f, 0.f);
+        auto exponentials = [&](int h2) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float a, d;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * q + 2 * k]), __uint_as_float(x[32 * q + 2 * k + 1])), f2, neg_m2), a, d);
+              a = ex2_approx(a);
+              d = ex2_approx(d);
+              sum2 = f2_add(sum2, f2_pack(a, d));
+              pk[k] = pack_f16x2(a, d);
+            }
+            tmem_st16(tP + h2 * 32 + q * 16, pk);
+          }
+        };
+        exponentials(0);
+        load64(1, x);
+        exponentials(1);
+        float sa, sb;
+        f2_unpack(sum2, sa, sb);
+        l += sa + sb;
+        tmem_st_wait();
+        tc_fence_before_sync();
+      }
+      arrive(b.p_ready + 8 * g);
+    }
+    if (!ok) break;
+    c += n;
+    // both warpgroups' scores of this item are done with: Q may change
+    notes.ml[g][row] = make_float2(m, l);
+    arrive(b.states);
+    wait_voted(b.states, items & 1u);
+    if (!ok) break;
+    const float2 other = notes.ml[g ^ 1][row];
+    const Segments was = seg;
+    seg.next(p);
+    seg.skip_empty(p);
+    if (seg.left > 0 && seg.data() > 0) load(seg);
+
+    // The item's output: this thread writes half of its row's columns.
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (mine[i] > 0) {
+        wait_voted(b.o_done + 8 * i, done[i] & 1u);
+        ++done[i];
+      }
+    if (!ok) break;
+    if (live) {
+      tc_fence_after_sync();
+      const float M = fmaxf(m, other.x);
+      const float f_own = ex2_approx(m - M), f_other = ex2_approx(other.x - M);
+      const float L = now.line == 0 ? 0.f : fmaf(l, f_own, other.y * f_other);
+      const float M_out = now.line == 0 ? kNone : M;
+      const float f[2] = {g ? f_other : f_own, g ? f_own : f_other};
+      const RowPlace rp = row_place(was.s, was.item, row, kRows, p);
+      const float inv = was.whole() ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f;
+      const bool empty = n == 0 || now.line == 0;
+      const uint32_t slot = number & 3u;
+      const bool any_nan = n > 0 && *reinterpret_cast<volatile uint32_t*>(&notes.any_nan[slot]) == number + 1;
+      const long long part_row = (2ll * blockIdx.x + (was.t0 > 0 ? 0 : 1)) * kRows + row;
+      constexpr int kHalf = D / 2;
+#pragma unroll 1
+      for (int e = 0; e < kHalf / 16; ++e) {
+        const int col = g * kHalf + e * 16;
+        float o[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (mine[i] == 0) continue;  // the same for the warp
+          uint32_t x[16];
+          tmem_ld16_wait(tO + i * C::kTmemGroup + col, x);
+          if (f[i] != 0.f) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(__uint_as_float(x[k]), f[i], o[k]);
+          }
+        }
+        if (any_nan) {  // a block of 16 columns of a node that this row sees
+          uint32_t bad = 0;
+#pragma unroll 1
+          for (int j = 0; j < p.Lq; ++j) {
+            const uint32_t note = notes.nan[slot][j];
+            if ((now.line >> j & 1ull) && note >> 8 == (number & 0xffffffu)) bad |= note >> (col / 16) & 1u;
+          }
+          if (bad) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(0x7fffffffu);
+          }
+        }
+        if (!rp.store) continue;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = empty ? 0.f : o[k] * inv;
+        if (was.whole()) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + (rp.token * p.Hq + rp.head) * D + col);
+          dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+          dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * D + col);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (g == 0 && rp.store) {
+        if (was.whole())
+          p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] = (M_out + log2f(L)) * 0.69314718055994531f;
+        else
+          p.part_ml[part_row] = make_float2(M_out, L);
+      }
+    }
+    if (n > 0) ++number;
+    ++items;
+    // the other warpgroup has read this one's O and state, too
+    tc_fence_before_sync();
+    arrive(b.written);
+    wait_voted(b.written, (items - 1) & 1u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Kernel
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Notes notes;
+  __shared__ long long s_sums[kThreads / 32];
+  __shared__ Segments s_seg;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+
+  Bars b;
+  {
+    uint32_t at = sbase + C::kBarOff;
+    auto take = [&](int n) {
+      const uint32_t x = at;
+      at += 8 * n;
+      return x;
+    };
+    b.raw0 = take(kTurnWarps * C::kRing);
+    b.k_full = take(2), b.k_empty = take(2), b.v_full = take(2), b.v_empty = take(2);
+    b.q_full = take(1);
+    b.s_full = take(2), b.p_ready = take(2), b.o_done = take(2);
+    b.states = take(1), b.written = take(1);
+    b.drain = take(1);
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  b.abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTurnWarps * C::kRing; ++i) mbar_init(b.raw0 + 8 * i, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(b.k_full + 8 * g, kTurnWarps);
+      mbar_init(b.v_full + 8 * g, kTurnWarps);
+      mbar_init(b.k_empty + 8 * g, 1);
+      mbar_init(b.v_empty + 8 * g, 1);
+      mbar_init(b.s_full + 8 * g, 1);
+      mbar_init(b.p_ready + 8 * g, 4);
+      mbar_init(b.o_done + 8 * g, 1);
+    }
+    mbar_init(b.q_full, 8);
+    mbar_init(b.states, 8);
+    mbar_init(b.written, 8);
+    mbar_init(b.drain, 2);
+    *b.abort_flag = 0;
+    for (int i = 0; i < 4; ++i) notes.any_nan[i] = 0;
+    s_seg.left = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 4 * kMaxTreeNodes) notes.nan[threadIdx.x / kMaxTreeNodes][threadIdx.x % kMaxTreeNodes] = 0xffffffffu;
+  if (warp == 16) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+
+  // This CTA's range of the concatenated items' cost.
+  const int items = p.Hkv * p.row_tiles;  // of a sequence
+  if (p.split) {
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].s = -1;
+    const int per = (p.n_seqs + kThreads - 1) / kThreads;
+    const int lo = min(static_cast<int>(threadIdx.x) * per, p.n_seqs), hi = min(lo + per, p.n_seqs);
+    long long mine = 0, total;
+    for (int s = lo; s < hi; ++s) mine += tile_cost(tokens_of(s, p));
+    const long long before = block_scan<kThreads / 32>(mine, s_sums, total);
+    const long long all = total * items;
+    const long long ctas = min(static_cast<long long>(gridDim.x), (all + kMinTiles - 1) / kMinTiles);
+    const long long c = blockIdx.x;
+    const long long begin = c < ctas ? all * c / ctas : all;
+    const int n = c < ctas ? static_cast<int>(min(all * (c + 1) / ctas - begin, 0x7fffffffll)) : 0;
+    if (n > 0 && begin >= before * items && begin < (before + mine) * items) {  // this thread's sequences hold the range's start
+      long long at = begin - before * items;
+      Segments w;
+      w.s = lo;
+      int cost;
+      for (;; ++w.s) {
+        w.len = tokens_of(w.s, p);
+        cost = tile_cost(w.len);
+        if (at < static_cast<long long>(cost) * items) break;
+        at -= static_cast<long long>(cost) * items;
+      }
+      w.tiles = tiles_of(w.len);
+      w.left = n;
+      w.item = static_cast<int>(at / cost);
+      const int in_item = static_cast<int>(at - static_cast<long long>(w.item) * cost);
+      w.set(in_item);
+      s_seg = w;
+      if (w.t0 > 0) {
+        // the range starts within an item: is this the item's first cut?
+        const long long a = begin - in_item;  // its start
+        if (all * (c - 1) / ctas <= a + kItemTiles)
+          p.cuts[c] = Cut{w.s, w.item, static_cast<int>(c - 1), static_cast<int>(((a + cost) * ctas + all - 1) / all - 1)};
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    // short items: CTA i takes item i whole
+    Segments w;
+    w.s = blockIdx.x / items;
+    w.item = static_cast<int>(blockIdx.x) - w.s * items;
+    w.len = tokens_of(w.s, p);
+    w.tiles = tiles_of(w.len);
+    w.left = w.tiles + kItemTiles;
+    w.set(0);
+    s_seg = w;
+  }
+  if (p.errors && blockIdx.x == 0) {
+    for (int s = threadIdx.x; s < p.n_seqs; s += kThreads)
+      if (p.seq_lens[s] != tokens_of(s, p)) atomicOr(p.errors, kErrPosition);
+    for (int i = threadIdx.x; i < p.n_seqs * p.Lq; i += kThreads)
+      if (p.parents[i] >= i % p.Lq) atomicOr(p.errors, kErrTree);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  const Segments seg = s_seg;
+
+  if (warp < 8) {
+    setmaxnreg_inc<kRegsSoftmax>();
+    run_softmax<D>(warp >> 2, smem, tmem, seg, b, notes, p);
+  } else if (warp < 16) {
+    setmaxnreg_dec<kRegsTurn>();
+    run_turn<D>(warp - 8, smem, seg, b, notes, p);
+  } else {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, seg, b, p);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace tree
+}  // namespace kv4
+}  // namespace fa
