@@ -34,6 +34,8 @@
 // Warps: 0-7 softmax; 8-15 codes to operands; 16, 17 MMA issuers.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_kv4_decode.cuh"
 
 namespace fa {
@@ -52,6 +54,8 @@ constexpr int kSiteTree = 8;           // status code: a wait gave up
 constexpr uint32_t kRegsSoftmax = 136, kRegsTurn = 72, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsTurn + 128 * kRegsIssue <= kThreads * 96, "register split exceeds the launch");
 
+constexpr int kFixedBars = 18;         // beside the rings'
+
 template <int D>
 struct Cfg {
   static constexpr int kSlabs = D / 64;                 // 64 columns of d each
@@ -64,7 +68,7 @@ struct Cfg {
   static constexpr int kRawOff = kVOff + 2 * kTileBytes;
   static constexpr int kWarpRaw = kRing * group_bytes(D);
   static constexpr int kBarOff = kRawOff + kTurnWarps * kWarpRaw;
-  static constexpr int kNumBars = kTurnWarps * kRing + 4 * 2 + 1 + 3 * 2 + 2 + 1;
+  static constexpr int kNumBars = kFixedBars + kTurnWarps * kRing;
   static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + alignment slack
   static_assert(kSmemBytes + 4096 <= 232448, "227 KB with the static part");
@@ -72,16 +76,23 @@ struct Cfg {
   static constexpr int kTmemS = 0, kTmemO = 256, kTmemP = D == 64 ? kTmemO + 64 : kTmemS, kTmemGroup = 128;
 };
 
+// The barriers' shared addresses, all from one.
 struct Bars {
-  uint32_t raw0;                            // [warp][kRing]
-  uint32_t k_full, k_empty, v_full, v_empty;  // [2] each
-  uint32_t q_full;
-  uint32_t s_full, p_ready, o_done;         // [2] each
-  uint32_t states, written;                 // between the warpgroups: an item's states are there; its O has been read
-  uint32_t drain;
+  uint32_t at;
   volatile int* abort_flag;
+  __device__ __forceinline__ uint32_t k_full(uint32_t g) const { return at + 8 * g; }
+  __device__ __forceinline__ uint32_t k_empty(uint32_t g) const { return at + 16 + 8 * g; }
+  __device__ __forceinline__ uint32_t v_full(uint32_t g) const { return at + 32 + 8 * g; }
+  __device__ __forceinline__ uint32_t v_empty(uint32_t g) const { return at + 48 + 8 * g; }
+  __device__ __forceinline__ uint32_t s_full(uint32_t g) const { return at + 64 + 8 * g; }
+  __device__ __forceinline__ uint32_t p_ready(uint32_t g) const { return at + 80 + 8 * g; }
+  __device__ __forceinline__ uint32_t o_done(uint32_t g) const { return at + 96 + 8 * g; }
+  __device__ __forceinline__ uint32_t q_full() const { return at + 112; }
+  __device__ __forceinline__ uint32_t states() const { return at + 120; }   // between the warpgroups: an item's states are there,
+  __device__ __forceinline__ uint32_t written() const { return at + 128; }  // its O has been read
+  __device__ __forceinline__ uint32_t drain() const { return at + 136; }
+  __device__ __forceinline__ uint32_t raw0() const { return at + 144; }     // [warp][kRing]
 };
-
 // kv4's costs and walk over the concatenated items, in tiles of 128 keys.
 __device__ __forceinline__ int data_tiles(int len) { return (len + kKeys - 1) / kKeys; }
 __device__ __forceinline__ int tiles_of(int len) { return max(1, data_tiles(len)); }
@@ -134,12 +145,20 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& 
   }
 }
 
+// Where a turning warp's loads are: a segment, and its tiles that were looked up.
+struct Ahead {
+  Segments seg;
+  int at;
+};
+
 // What the warps pass each other beside the barriers.
 struct Notes {
   uint32_t skip[4][2];                // a tile's groups whose page was refused (a byte each), by tile number mod 4
   uint32_t nan[4][kMaxTreeNodes];     // by item number mod 4: (item number << 8) | V blocks of a node that are NaN
   uint32_t any_nan[4];                // the item number + 1 where there is one
   float2 ml[2][kRows];                // the warpgroups' running maxima and sums
+  float factor[kRows];                // of the item whose Q is in shared memory
+  Ahead ahead[kTurnWarps];
 };
 
 // ---------------------------------------------------------------------------
@@ -192,33 +211,61 @@ __device__ __forceinline__ void zero_group(uint8_t* tile, int key0) {
   }
 }
 
+// The same for a group that is not all context: keys behind the sequence (live
+// of the 16 are its own) and groups that were not loaded are zeros, a V block
+// that is NaN at a node (the first key's is node0) is zeros, too, and noted.  A
+// call, so that the plain conversion's loop stays short.
+template <int D>
+__device__ __noinline__ void turn_tail(const uint8_t* raw, uint8_t* tile, int key0, bool on, int v, int live, int node0,
+                                       uint32_t number, Notes& notes, const DecodeParams& p) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* noted = notes.nan[number & 3u];
+  if (!on) {
+    zero_group<D>(tile, key0);
+    return;
+  }
+  if (v && lane < kGroup && node0 + lane >= 0 && node0 + lane < p.Lq) noted[node0 + lane] = number << 8;
+  __syncwarp();
+  turn_group<D>(raw, tile, key0, [&](int key, int block, uint32_t s) {
+    if (key >= live) return 0u;
+    if (v && (s & 0x7fu) == 0x7fu && node0 + key >= 0) {
+      atomicOr(noted + node0 + key, 1u << block);
+      notes.any_nan[number & 3u] = number + 1;
+      return 0u;
+    }
+    return s;
+  });
+}
+
 template <int D>
 __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, const Bars& b, Notes& notes, const DecodeParams& p) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   uint8_t* raw = smem + C::kRawOff + w * C::kWarpRaw;
-  const uint32_t raw_u32 = smem_u32(raw), raw_bar = b.raw0 + w * C::kRing * 8;
+  const uint32_t raw_u32 = smem_u32(raw), raw_bar = b.raw0() + w * C::kRing * 8;
   const int group_shift = p.page_shift - 4;
   const long long head_bytes = static_cast<long long>(row_bytes(D)) << p.page_shift, page_bytes = head_bytes * p.Hkv;
 
   // Loads run kRing tiles ahead, across segments.  Up to 32 tiles' groups are
   // looked up together, one by each lane, which later issues its copy.
-  Segments ahead = seg;
-  int ahead_at = 0;                          // tiles of `ahead` that were looked up
+  if (lane == 0) notes.ahead[w] = Ahead{seg, 0};
+  __syncwarp();
   const uint8_t* src = nullptr;
   uint32_t loaded = 0, refused = 0;          // of those looked up
   int batch = 0, next = 0;
-  uint32_t issued = 0;                       // tiles
+  uint32_t issued = 0, issue_at = 0;         // tiles; the ring place of the next one
   uint32_t stage_loaded = 0, stage_refused = 0;  // bit per ring place
   auto look_up = [&]() {
+    Ahead a = notes.ahead[w];
+    Segments& ahead = a.seg;
     batch = next = 0;
-    while (ahead.left > 0 && ahead_at >= ahead.data()) {
+    while (ahead.left > 0 && a.at >= ahead.data()) {
       ahead.next(p);
-      ahead_at = 0;
+      a.at = 0;
     }
     if (ahead.left <= 0) return;
-    batch = min(32, ahead.data() - ahead_at);
-    const int group = (ahead.t0 + ahead_at + lane) * (kKeys / kGroup) + w;
+    batch = min(32, ahead.data() - a.at);
+    const int group = (ahead.t0 + a.at + lane) * (kKeys / kGroup) + w;
     const bool exists = lane < batch && group < (ahead.len + kGroup - 1) / kGroup;
     int page = -1;
     if (exists) page = __ldg(p.page_table + static_cast<long long>(ahead.s) * p.max_pages + (group >> group_shift));
@@ -228,14 +275,17 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
     loaded = __ballot_sync(0xffffffffu, ok);
     refused = __ballot_sync(0xffffffffu, exists && !ok);
     if (p.errors && exists && !ok) atomicOr(p.errors, kErrPage);
-    ahead_at += batch;
+    a.at += batch;
+    __syncwarp();
+    if (lane == 0) notes.ahead[w] = a;
+    __syncwarp();
   };
   auto issue = [&]() {
     if (next == batch) {
       look_up();
       if (batch == 0) return;
     }
-    const uint32_t st = issued % C::kRing, bar = raw_bar + 8 * st;
+    const uint32_t st = issue_at, bar = raw_bar + 8 * st;
     const uint32_t on = loaded >> next & 1u;
     stage_loaded = (stage_loaded & ~(1u << st)) | on << st;
     stage_refused = (stage_refused & ~(1u << st)) | (refused >> next & 1u) << st;
@@ -247,70 +297,46 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
         mbar_arrive(bar);
       }
     }
+    issue_at = st + 1 == C::kRing ? 0 : st + 1;
     ++next;
     ++issued;
   };
 #pragma unroll 1
   for (int i = 0; i < C::kRing; ++i) issue();
 
-  uint32_t c = 0;       // tiles taken
-  uint32_t number = 0;  // items with tiles
+  uint32_t c = 0;             // tiles taken
+  uint32_t st = 0, phase = 0; // the ring place of the next one, and its barrier's phase
+  uint32_t number = 0;        // items with tiles
   bool ok = true;
   const int key0 = w * kGroup;
-  auto arrive = [&](uint32_t bar) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  };
 #pragma unroll 1
   for (; seg.left > 0 && ok; seg.next(p)) {
     const int n = seg.data();
     if (n == 0) continue;
     const int prefix = seg.len - p.Lq;
 #pragma unroll 1
-    for (int t = seg.t0; t < seg.t0 + n; ++t, ++c) {
-      const uint32_t st = c % C::kRing, place = c & 1u, use = c >> 1;
+    for (int t = seg.t0; t < seg.t0 + n && ok; ++t, ++c) {
+      const uint32_t place = c & 1u, empty = (c >> 1 & 1u) ^ 1u;
       const int pos = t * kKeys + key0;
-      const bool on = stage_loaded >> st & 1u;
-      ok = __all_sync(0xffffffffu, wait(raw_bar + 8 * st, c / C::kRing & 1u, b, p) && wait(b.k_empty + 8 * place, (use & 1u) ^ 1u, b, p));
+      const bool on = stage_loaded >> st & 1u, plain = on && pos + kGroup <= prefix;
+      ok = __all_sync(0xffffffffu, wait(raw_bar + 8 * st, phase, b, p));
       if (!ok) break;
       if (lane == 0) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[w] = stage_refused >> st & 1u ? 0xffu : 0u;
       const uint8_t* group = raw + st * group_bytes(D);
-      uint8_t* k_tile = smem + C::kKOff + place * C::kTileBytes;
-      uint8_t* v_tile = smem + C::kVOff + place * C::kTileBytes;
-      const int live = seg.len - pos;  // keys of the group that are the sequence's, if fewer than 16
-      if (!on) {
-        zero_group<D>(k_tile, key0);
-      } else if (live >= kGroup) {
-        turn_group<D>(group, k_tile, key0, [](int, int, uint32_t s) { return s; });
-      } else {
-        turn_group<D>(group, k_tile, key0, [&](int key, int, uint32_t s) { return key < live ? s : 0u; });
-      }
-      arrive(b.k_full + 8 * place);
-      ok = __all_sync(0xffffffffu, wait(b.v_empty + 8 * place, (use & 1u) ^ 1u, b, p));
-      if (!ok) break;
-      if (!on) {
-        zero_group<D>(v_tile, key0);
-      } else if (pos + kGroup <= prefix) {
-        turn_group<D>(group + codes_at(D, 1), v_tile, key0, [](int, int, uint32_t s) { return s; });
-      } else {
-        // the tree's nodes, and keys behind the sequence
-        const int node0 = pos - prefix;
-        uint32_t* noted = notes.nan[number & 3u];
-        if (lane < kGroup && node0 + lane >= 0 && node0 + lane < p.Lq) noted[node0 + lane] = number << 8;
+      // K, then V
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        ok = __all_sync(0xffffffffu, wait(v ? b.v_empty(place) : b.k_empty(place), empty, b, p));
+        if (!ok) break;
+        uint8_t* tile = smem + (v ? C::kVOff : C::kKOff) + place * C::kTileBytes;
+        if (plain) turn_group<D>(group + codes_at(D, v), tile, key0, [](int, int, uint32_t s) { return s; });
+        else turn_tail<D>(group + codes_at(D, v), tile, key0, on, v, seg.len - pos, pos - prefix, number, notes, p);
+        fence_proxy_async_smem();
         __syncwarp();
-        turn_group<D>(group + codes_at(D, 1), v_tile, key0, [&](int key, int block, uint32_t s) {
-          if (key >= live) return 0u;
-          if ((s & 0x7fu) == 0x7fu && node0 + key >= 0) {
-            atomicOr(noted + node0 + key, 1u << block);
-            notes.any_nan[number & 3u] = number + 1;
-            return 0u;
-          }
-          return s;
-        });
+        if (lane == 0) mbar_arrive(v ? b.v_full(place) : b.k_full(place));
       }
-      arrive(b.v_full + 8 * place);  // every lane has read the group
-      issue();
+      if (++st == C::kRing) st = 0, phase ^= 1u;
+      issue();  // every lane has read the group
     }
     ++number;
   }
@@ -326,30 +352,54 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, boo
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// The products with descriptors put together from words: the upper one is a
+// constant of the operand's layout, the lower one the address (>> 4) and the
+// leading offset.  Held as 64-bit values, 24 of them would fill the warp's registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t tmem, Segments seg, const Bars& b, const DecodeParams& p) {
   using C = Cfg<D>;
   const bool leader = (threadIdx.x & 31) == 0;
-  const uint64_t q_desc = sdesc_sw128(sbase + C::kQOff, 16, 1024);
-  const uint64_t k_desc = sdesc_sw128(sbase + C::kKOff + g * C::kTileBytes, 16, 1024);
-  const uint64_t v_desc = sdesc_sw128(sbase + C::kVOff + g * C::kTileBytes, C::kSlabBytes, 1024);
+  const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(0, 0, 1024) >> 32);
+  const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kQOff, 16, 1024));
+  const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kKOff + g * C::kTileBytes, 16, 1024));
+  const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kVOff + g * C::kTileBytes, C::kSlabBytes, 1024));
   const uint32_t tm_s = tmem + C::kTmemS + g * C::kTmemGroup, tm_p = tmem + C::kTmemP + g * C::kTmemGroup;
   const uint32_t tm_o = tmem + C::kTmemO + g * C::kTmemGroup;
   bool ok = true;
   auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(bar, parity, b, p)); };
   uint32_t c = 0, uses = 0, items = 0;  // tiles; this warpgroup's; items with tiles
   auto qk = [&]() {
-    wait_voted(b.k_full + 8 * g, uses & 1u);
+    wait_voted(b.k_full(g), uses & 1u);
     if (!ok) return;
     tc_fence_after_sync();
     if (leader) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
-        umma_ss(tm_s, sdesc_advance(q_desc, off), sdesc_advance(k_desc, off), idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+        mma_ss(tm_s, q_lo + (off >> 4), k_lo + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
       }
-      umma_commit(b.s_full + 8 * g);
-      umma_commit(b.k_empty + 8 * g);
+      umma_commit(b.s_full(g));
+      umma_commit(b.k_empty(g));
     }
     __syncwarp();
   };
@@ -359,21 +409,21 @@ __device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t t
     if (n == 0) continue;
     const int mine = (n + ((c & 1u) == g ? 1 : 0)) / 2;  // of the segment's tiles, dealt in turn
     c += n;
-    wait_voted(b.q_full, items & 1u);
+    wait_voted(b.q_full(), items & 1u);
     ++items;
     if (mine > 0 && ok) qk();
 #pragma unroll 1
     for (int i = 0; i < mine && ok; ++i) {
-      wait_voted(b.v_full + 8 * g, uses & 1u);
-      wait_voted(b.p_ready + 8 * g, uses & 1u);
+      wait_voted(b.v_full(g), uses & 1u);
+      wait_voted(b.p_ready(g), uses & 1u);
       if (!ok) break;
       tc_fence_after_sync();
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(tm_o, tm_p + kk * 8, sdesc_advance(v_desc, kk * 2048), idesc_f16_f32(kRows, D, true), i > 0 || kk > 0 ? 1u : 0u);
-        umma_commit(b.v_empty + 8 * g);
-        if (i == mine - 1) umma_commit(b.o_done + 8 * g);
+          mma_ts(tm_o, tm_p + kk * 8, v_lo + kk * 128, hi, idesc_f16_f32(kRows, D, true), i > 0 || kk > 0 ? 1u : 0u);
+        umma_commit(b.v_empty(g));
+        if (i == mine - 1) umma_commit(b.o_done(g));
       }
       __syncwarp();
       ++uses;
@@ -381,52 +431,88 @@ __device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t t
     }
   }
   // Every MMA this thread issued must finish before tensor memory is released.
-  if (leader) umma_commit(b.drain);
+  if (leader) umma_commit(b.drain());
   __syncwarp();
-  mbar_wait_bounded(b.drain, 0, p.wait_limit_ns);
+  mbar_wait_bounded(b.drain(), 0, p.wait_limit_ns);
 }
 
 // ---------------------------------------------------------------------------
 // Softmax and output (warpgroup g: one row a thread)
 // ---------------------------------------------------------------------------
-// A row of an item: what it sees, and the factor from its scores to log2 units.
-struct RowState {
-  unsigned long long line;  // 0: sees nothing, or no such row
-  float factor;
-};
-
+// Q rows of an item to shared memory as f16 (K-major slabs, 128-byte swizzle),
+// and each row's factor from its scores to log2 units: warp w of eight takes rows
+// 16 w ..., D / 8 lanes a row, all loads in flight at once.
 template <int D>
-__device__ __forceinline__ RowState load_row(int g, int row, uint8_t* smem, const Segments& seg, const DecodeParams& p) {
-  // both warpgroups look for the row's largest element, each writes its half of the row
-  const int h = seg.item / p.row_tiles, r = (seg.item - h * p.row_tiles) * kRows + row, node = r / p.G;
-  const bool exists = node < p.Lq;
-  RowState st{0ull, 1.f};
-  if (exists) st.line = tree_line(p.parents + static_cast<long long>(seg.s) * p.Lq, node, seg.len - p.Lq);
-  const __nv_bfloat16* src = p.q + (static_cast<long long>(seg.s) * p.Lq + node) * p.q_stride +
-                             static_cast<long long>(h * p.G + r - node * p.G) * D;
-  uint32_t m2 = 0;
-#pragma unroll 4
-  for (int n = 0; n < D / 8; ++n) {
-    const uint4 x = exists ? __ldg(reinterpret_cast<const uint4*>(src) + n) : make_uint4(0, 0, 0, 0);
-    m2 = __vmaxu2(m2, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
-    m2 = __vmaxu2(m2, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+__device__ __forceinline__ void load_q(int w, uint8_t* smem, const Segments& seg, Notes& notes, const DecodeParams& p) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 16 / kAtOnce;
+  const int lane = threadIdx.x & 31, chunk = lane % kLanes;
+  const int h = seg.item / p.row_tiles, r0 = (seg.item - h * p.row_tiles) * kRows;
+  const __nv_bfloat16* q = p.q + static_cast<long long>(seg.s) * p.Lq * p.q_stride + static_cast<long long>(h) * p.G * D + chunk * 8;
+  uint4 x[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = r0 + w * 16 + i * kAtOnce + lane / kLanes, node = r / p.G;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (node < p.Lq) x[i] = __ldg(reinterpret_cast<const uint4*>(q + node * p.q_stride + (r - node * p.G) * D));
   }
-  const uint32_t top = max(m2 & 0xffffu, m2 >> 16);
-  const int e = max(static_cast<int>(top >> 7) - 127, -100);  // floor(log2) of the row's largest element
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-  st.factor = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.qk_scale, 1.17549435e-38f);
-#pragma unroll 4
-  for (int n = 0; n < D / 16; ++n) {
-    const int chunk = g * (D / 16) + n;
-    const uint4 x = exists ? __ldg(reinterpret_cast<const uint4*>(src) + chunk) : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int row = w * 16 + i * kAtOnce + lane / kLanes;
+    const uint32_t wds[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, wds[k] & 0x7fff7fffu);
+    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const int e = max(static_cast<int>(top >> 7) - 127, -100);  // floor(log2) of the row's largest element
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
     uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+    for (int k = 0; k < 4; ++k) y[k] = pack_f16x2(__uint_as_float(wds[k] << 16) * up, __uint_as_float(wds[k] & 0xffff0000u) * up);
     *reinterpret_cast<uint4*>(smem + Cfg<D>::kQOff + (chunk >> 3) * Cfg<D>::kSlabBytes + row * 128 +
                               (((chunk & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (chunk == 0)  // positive: a masked score is -inf times it
+      notes.factor[row] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.qk_scale, 1.17549435e-38f);
   }
-  return st;
+}
+
+// tree_line of each lane's node (-1: no such row), the tree's parents two to a lane.
+__device__ __forceinline__ unsigned long long tree_line_warp(const int* parents, int nodes, int node, int first_position) {
+  const int lane = threadIdx.x & 31;
+  const int lo = lane < nodes ? __ldg(parents + lane) : -2, hi = lane + 32 < nodes ? __ldg(parents + lane + 32) : -2;
+  unsigned long long line = 0;
+  bool going = node >= 0;
+  while (__any_sync(0xffffffffu, going)) {
+    const int a = __shfl_sync(0xffffffffu, lo, node & 31), b = __shfl_sync(0xffffffffu, hi, node & 31);
+    if (!going) continue;
+    const int parent = node < 32 ? a : b;
+    line |= 1ull << node;
+    const bool absent = first_position + node < 0 || parent < -1 || parent >= node;
+    if (absent) line = 0;
+    going = !absent && parent >= 0;
+    node = parent;
+  }
+  return line;
+}
+
+// 4 x 4 transpose of 16-byte pieces over four neighbouring lanes: v[k] becomes
+// piece (lane & 3) of the k-th of them.
+__device__ __forceinline__ void transpose_quad(uint4* v) {
+  const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+  auto swap = [](uint4& a, uint4& b, bool low, int off) {  // the one that this lane does not keep
+    uint4 x = low ? a : b;
+    x.x = __shfl_xor_sync(0xffffffffu, x.x, off);
+    x.y = __shfl_xor_sync(0xffffffffu, x.y, off);
+    x.z = __shfl_xor_sync(0xffffffffu, x.z, off);
+    x.w = __shfl_xor_sync(0xffffffffu, x.w, off);
+    if (low) a = x;
+    else b = x;
+  };
+  swap(v[0], v[1], odd, 1);
+  swap(v[2], v[3], odd, 1);
+  swap(v[0], v[2], upper, 2);
+  swap(v[1], v[3], upper, 2);
 }
 
 template <int D>
@@ -445,11 +531,10 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
     if (lane == 0) mbar_arrive(bar);
   };
   seg.skip_empty(p);
-  RowState st{0ull, 1.f};
   auto load = [&](const Segments& at) {
-    st = load_row<D>(g, row, smem, at, p);
+    load_q<D>(g * 4 + quad, smem, at, notes, p);
     fence_proxy_async_smem();
-    arrive(b.q_full);
+    arrive(b.q_full());
   };
   if (seg.left > 0 && seg.data() > 0) load(seg);
 #pragma unroll 1
@@ -457,111 +542,135 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
     const int n = seg.data();
     const int h = seg.item / p.row_tiles, r0 = (seg.item - h * p.row_tiles) * kRows;
     const bool live = r0 + quad * 32 < p.Lq * p.G;  // the warp has rows
-    const RowState now = st;
-    float m = kNone, l = 0.f;
+    float m = kNone, l = 0.f, factor = 1.f;
+    unsigned long long line = 0;
+    if (live) {
+      const int node = (r0 + row) / p.G;
+      line = tree_line_warp(p.parents + static_cast<long long>(seg.s) * p.Lq, p.Lq, node < p.Lq ? node : -1, seg.len - p.Lq);
+    }
+    if (n > 0) {
+      wait_voted(b.q_full(), number & 1u);
+      if (!ok) break;
+      factor = notes.factor[row];
+    }
     int mine[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) mine[i] = (n + (static_cast<int>(c & 1u) == i ? 1 : 0)) / 2;
     const int first = seg.t0 + (static_cast<int>(c & 1u) == g ? 0 : 1);  // this warpgroup's tiles: every other one
     const int prefix = seg.len - p.Lq;
+    const uint64_t f2 = f2_pack(factor, factor);
+    // P and its sum from NC scores, two at a time
+    auto exponentials = [&](auto count, const uint32_t* x, uint32_t* pk, uint64_t neg_m2, uint64_t& sum2) {
+      constexpr int kPairs = decltype(count)::value / 2;
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) {
+        float a, d;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, neg_m2), a, d);
+        a = ex2_approx(a);
+        d = ex2_approx(d);
+        sum2 = f2_add(sum2, f2_pack(a, d));
+        pk[k] = pack_f16x2(a, d);
+      }
+    };
 #pragma unroll 1
     for (int i = 0; i < (g ? mine[1] : mine[0]) && ok; ++i) {
       const int t = first + 2 * i;
-      wait_voted(b.s_full + 8 * g, uses & 1u);
+      wait_voted(b.s_full(g), uses & 1u);
       if (!ok) break;
       ++uses;
       if (live) {
         tc_fence_after_sync();
-        const uint32_t number_of_tile = c + static_cast<uint32_t>(t - seg.t0);
-        const volatile uint32_t* refusals = notes.skip[number_of_tile & 3u];
-        const uint2 skip = make_uint2(refusals[0], refusals[1]);
-        const bool masked = (t + 1) * kKeys > prefix || (skip.x | skip.y) != 0;
-        // columns 64 h ... of the tile: bit e set where the row sees key 64 h + e
-        auto seen64 = [&](int h2) {
-          const int node0 = t * kKeys + h2 * 64 - prefix;
-          unsigned long long v = node0 >= 64 ? 0ull : node0 >= 0 ? now.line >> node0
-                                 : node0 <= -64 ? ~0ull : (now.line << -node0) | ((1ull << -node0) - 1ull);
-          const uint32_t refused = h2 ? skip.y : skip.x;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (refused >> (8 * q) & 1u) v &= ~(0xffffull << (16 * q));
-          return v;
-        };
-        auto load64 = [&](int h2, uint32_t* x) {
-          tmem_ld64_wait(tS + h2 * 64, x);
-          if (masked) {
-            const unsigned long long v = seen64(h2);
-            const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(lo >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
-              if (!(hi >> e & 1u)) x[32 + e] = __float_as_uint(-INFINITY);
-            }
-          }
-        };
-        uint32_t x[64];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto maxima = [&]() {
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) mx[e >> 1 & 3] = fmax3(mx[e >> 1 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-        };
-        load64(1, x);
-        maxima();
-        load64(0, x);
-        maxima();
-        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * now.factor;
-        if (__any_sync(0xffffffffu, top - m > kLift + kMove)) {
-          const float to = fmaxf(m, top - kLift);
-          const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
-          m = to;
-          l *= alpha;
-          if (i > 0) {  // O holds the sum so far: its last product was done before S was
-            const uint32_t mine_o = tO + g * C::kTmemGroup;
-#pragma unroll 1
-            for (int e = 0; e < D / 32; ++e) {
-              uint32_t o[32];
-              tmem_ld32_wait(mine_o + e * 32, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(mine_o + e * 32, o);
-            }
+        const volatile uint32_t* refusals = notes.skip[(c + static_cast<uint32_t>(t - seg.t0)) & 3u];
+        const uint32_t skip_lo = refusals[0], skip_hi = refusals[1];
+        const bool masked = (t + 1) * kKeys > prefix || (skip_lo | skip_hi) != 0;
+        bool done = false, over = false;
+        if (i > 0 && !masked) {
+          // Against the present reference.  A sum within f16's range holds no P
+          // above it, so that the maximum is not asked for.
+          const uint64_t neg_m2 = f2_pack(-m, -m);
+          uint64_t sum2 = f2_pack(0.f, 0.f);
+          uint32_t x[64], pk[64];
+          tmem_ld64_wait(tS, x);
+          exponentials(std::integral_constant<int, 64>{}, x, pk, neg_m2, sum2);
+          tmem_ld64_wait(tS + 64, x);
+          exponentials(std::integral_constant<int, 64>{}, x, pk + 32, neg_m2, sum2);
+          float sa, sb;
+          f2_unpack(sum2, sa, sb);
+          done = __all_sync(0xffffffffu, !(sa + sb > 65504.f));
+          over = !done;
+          if (done) {
+            l += sa + sb;
+            tmem_st32(tP, pk);
+            tmem_st32(tP + 32, pk + 32);
           }
         }
-        const uint64_t f2 = f2_pack(now.factor, now.factor), neg_m2 = f2_pack(-m, -m);
-        uint64_t sum2 = f2_pack(0.f, 0.f);
-        auto exponentials = [&](int h2) {
+        if (!done) {
+          // 32 columns at a time: the maximum first, then the exponentials from S
+          // read again (where P lies over S, its 16 columns over some read before).
+          auto scores = [&](int c4, uint32_t* x) {
+            tmem_ld32_wait(tS + c4 * 32, x);
+            if (!masked) return;
+            // bit e: the row sees key 32 c4 + e
+            const int node0 = t * kKeys + c4 * 32 - prefix;
+            uint32_t v = node0 >= 64 ? 0u : node0 >= 0 ? static_cast<uint32_t>(line >> node0)
+                         : node0 <= -32 ? ~0u : (static_cast<uint32_t>(line) << -node0) | ((1u << -node0) - 1u);
+            const uint32_t refused = (c4 < 2 ? skip_lo : skip_hi) >> (c4 & 1) * 16;
+            if (refused & 1u) v &= 0xffff0000u;
+            if (refused >> 8 & 1u) v &= 0xffffu;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[16];
+            for (int e = 0; e < 32; ++e)
+              if (!(v >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t x[32];
+            scores(c4, x);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float a, d;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * q + 2 * k]), __uint_as_float(x[32 * q + 2 * k + 1])), f2, neg_m2), a, d);
-              a = ex2_approx(a);
-              d = ex2_approx(d);
-              sum2 = f2_add(sum2, f2_pack(a, d));
-              pk[k] = pack_f16x2(a, d);
-            }
-            tmem_st16(tP + h2 * 32 + q * 16, pk);
+            for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           }
-        };
-        exponentials(0);
-        load64(1, x);
-        exponentials(1);
-        float sa, sb;
-        f2_unpack(sum2, sa, sb);
-        l += sa + sb;
+          top *= factor;  // factor > 0: the maximum commutes with it
+          if (__any_sync(0xffffffffu, top - m > (over ? kLift : kLift + kMove))) {
+            const float to = fmaxf(m, top - kLift);
+            const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
+            m = to;
+            l *= alpha;
+            if (i > 0) {  // O holds the sum so far: its last product was done before S was
+              const uint32_t own = tO + g * C::kTmemGroup;
+#pragma unroll 1
+              for (int e = 0; e < D / 32; ++e) {
+                uint32_t o[32];
+                tmem_ld32_wait(own + e * 32, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st32(own + e * 32, o);
+              }
+            }
+          }
+          const uint64_t neg_m2 = f2_pack(-m, -m);
+          uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t x[32], pk[16];
+            scores(c4, x);
+            exponentials(std::integral_constant<int, 32>{}, x, pk, neg_m2, sum2);
+            tmem_st16(tP + c4 * 16, pk);
+          }
+          float sa, sb;
+          f2_unpack(sum2, sa, sb);
+          l += sa + sb;
+        }
         tmem_st_wait();
         tc_fence_before_sync();
       }
-      arrive(b.p_ready + 8 * g);
+      arrive(b.p_ready(g));
     }
     if (!ok) break;
     c += n;
     // both warpgroups' scores of this item are done with: Q may change
     notes.ml[g][row] = make_float2(m, l);
-    arrive(b.states);
-    wait_voted(b.states, items & 1u);
+    arrive(b.states());
+    wait_voted(b.states(), items & 1u);
     if (!ok) break;
     const float2 other = notes.ml[g ^ 1][row];
     const Segments was = seg;
@@ -569,82 +678,99 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
     seg.skip_empty(p);
     if (seg.left > 0 && seg.data() > 0) load(seg);
 
-    // The item's output: this thread writes half of its row's columns.
+    // The item's output: this warpgroup writes half of the columns.
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (mine[i] > 0) {
-        wait_voted(b.o_done + 8 * i, done[i] & 1u);
+        wait_voted(b.o_done(i), done[i] & 1u);
         ++done[i];
       }
     if (!ok) break;
     if (live) {
       tc_fence_after_sync();
-      const float M = fmaxf(m, other.x);
+      const bool whole = was.whole(), none = n == 0 || line == 0;
+      const float M = none ? kNone : fmaxf(m, other.x);
       const float f_own = ex2_approx(m - M), f_other = ex2_approx(other.x - M);
-      const float L = now.line == 0 ? 0.f : fmaf(l, f_own, other.y * f_other);
-      const float M_out = now.line == 0 ? kNone : M;
-      const float f[2] = {g ? f_other : f_own, g ? f_own : f_other};
+      const float L = none ? 0.f : fmaf(l, f_own, other.y * f_other);
+      const float inv = !whole ? 1.f : L == 0.f ? 0.f : p.v_scale / L;
+      float f[2];
+      f[0] = none ? 0.f : (g ? f_other : f_own) * inv, f[1] = none ? 0.f : (g ? f_own : f_other) * inv;
       const RowPlace rp = row_place(was.s, was.item, row, kRows, p);
-      const float inv = was.whole() ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f;
-      const bool empty = n == 0 || now.line == 0;
       const uint32_t slot = number & 3u;
       const bool any_nan = n > 0 && *reinterpret_cast<volatile uint32_t*>(&notes.any_nan[slot]) == number + 1;
+      uint32_t bad = 0;  // blocks that are NaN at a node that this row sees
+      if (any_nan) {
+        for (int j = 0; j < p.Lq; ++j) {
+          const uint32_t note = notes.nan[slot][j];
+          if ((line >> j & 1ull) && note >> 8 == (number & 0xffffffu)) bad |= note & 0xffu;
+        }
+      }
       const long long part_row = (2ll * blockIdx.x + (was.t0 > 0 ? 0 : 1)) * kRows + row;
+      // where this row's piece of 16 bytes goes, and, from the lanes that hold them, the quad's four rows'
       constexpr int kHalf = D / 2;
-#pragma unroll 1
-      for (int e = 0; e < kHalf / 16; ++e) {
-        const int col = g * kHalf + e * 16;
-        float o[16];
+      uint8_t* mine_at = whole ? reinterpret_cast<uint8_t*>(p.o + (rp.token * p.Hq + rp.head) * D + g * kHalf)
+                               : reinterpret_cast<uint8_t*>(p.part_o + part_row * D + g * kHalf);
+      if (!rp.store) mine_at = nullptr;
+      uint8_t* at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        at[k] = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine_at), (lane & ~3) | k));
+      const int piece = (lane & 3) * 16;
+      auto columns = [&](int col, float* o) {  // 16 of them, from column `col` of the half on
+        uint32_t x[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (mine[i] == 0) continue;  // the same for the warp
-          uint32_t x[16];
-          tmem_ld16_wait(tO + i * C::kTmemGroup + col, x);
+          tmem_ld16_wait(tO + i * C::kTmemGroup + g * kHalf + col, x);
           if (f[i] != 0.f) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = fmaf(__uint_as_float(x[k]), f[i], o[k]);
           }
         }
-        if (any_nan) {  // a block of 16 columns of a node that this row sees
-          uint32_t bad = 0;
+        if (bad >> ((g * kHalf + col) / 16) & 1u) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(0x7fffffffu);
+        }
+      };
+      // 64 bytes of a row at a time, transposed within the quad so that four lanes store them together
 #pragma unroll 1
-          for (int j = 0; j < p.Lq; ++j) {
-            const uint32_t note = notes.nan[slot][j];
-            if ((now.line >> j & 1ull) && note >> 8 == (number & 0xffffffu)) bad |= note >> (col / 16) & 1u;
-          }
-          if (bad) {
+      for (int e = 0; e < (whole ? kHalf / 32 : kHalf / 16); ++e) {
+        uint4 v[4];
+        if (whole) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(0x7fffffffu);
+          for (int half = 0; half < 2; ++half) {
+            float o[16];
+            columns(e * 32 + half * 16, o);
+            v[2 * half] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            v[2 * half + 1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
+                                         pack_bf16x2(o[14], o[15]));
           }
-        }
-        if (!rp.store) continue;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = empty ? 0.f : o[k] * inv;
-        if (was.whole()) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + (rp.token * p.Hq + rp.head) * D + col);
-          dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-          dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * D + col);
+          float o[16];
+          columns(e * 16, o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k)
+            v[k] = make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                              __float_as_uint(o[4 * k + 3]));
         }
+        transpose_quad(v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at[k] != nullptr) *reinterpret_cast<uint4*>(at[k] + e * 64 + piece) = v[k];
       }
       if (g == 0 && rp.store) {
-        if (was.whole())
-          p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] = (M_out + log2f(L)) * 0.69314718055994531f;
-        else
-          p.part_ml[part_row] = make_float2(M_out, L);
+        if (whole) p.lse[static_cast<long long>(rp.head) * p.n_seqs * p.Lq + rp.token] = (M + log2f(L)) * 0.69314718055994531f;
+        else p.part_ml[part_row] = make_float2(M, L);
       }
     }
     if (n > 0) ++number;
     ++items;
     // the other warpgroup has read this one's O and state, too
     tc_fence_before_sync();
-    arrive(b.written);
-    wait_voted(b.written, (items - 1) & 1u);
+    arrive(b.written());
+    wait_voted(b.written(), (items - 1) & 1u);
   }
 }
 
@@ -662,38 +788,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
 
-  Bars b;
-  {
-    uint32_t at = sbase + C::kBarOff;
-    auto take = [&](int n) {
-      const uint32_t x = at;
-      at += 8 * n;
-      return x;
-    };
-    b.raw0 = take(kTurnWarps * C::kRing);
-    b.k_full = take(2), b.k_empty = take(2), b.v_full = take(2), b.v_empty = take(2);
-    b.q_full = take(1);
-    b.s_full = take(2), b.p_ready = take(2), b.o_done = take(2);
-    b.states = take(1), b.written = take(1);
-    b.drain = take(1);
-  }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
-  b.abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  const Bars b{sbase + C::kBarOff, reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTurnWarps * C::kRing; ++i) mbar_init(b.raw0 + 8 * i, 1);
+    for (int i = 0; i < kTurnWarps * C::kRing; ++i) mbar_init(b.raw0() + 8 * i, 1);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(b.k_full + 8 * g, kTurnWarps);
-      mbar_init(b.v_full + 8 * g, kTurnWarps);
-      mbar_init(b.k_empty + 8 * g, 1);
-      mbar_init(b.v_empty + 8 * g, 1);
-      mbar_init(b.s_full + 8 * g, 1);
-      mbar_init(b.p_ready + 8 * g, 4);
-      mbar_init(b.o_done + 8 * g, 1);
+      mbar_init(b.k_full(g), kTurnWarps);
+      mbar_init(b.v_full(g), kTurnWarps);
+      mbar_init(b.k_empty(g), 1);
+      mbar_init(b.v_empty(g), 1);
+      mbar_init(b.s_full(g), 1);
+      mbar_init(b.p_ready(g), 4);
+      mbar_init(b.o_done(g), 1);
     }
-    mbar_init(b.q_full, 8);
-    mbar_init(b.states, 8);
-    mbar_init(b.written, 8);
-    mbar_init(b.drain, 2);
+    mbar_init(b.q_full(), 8);
+    mbar_init(b.states(), 8);
+    mbar_init(b.written(), 8);
+    mbar_init(b.drain(), 2);
     *b.abort_flag = 0;
     for (int i = 0; i < 4; ++i) notes.any_nan[i] = 0;
     s_seg.left = 0;
@@ -765,17 +876,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
   tc_fence_after_sync();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
-  const Segments seg = s_seg;
 
   if (warp < 8) {
     setmaxnreg_inc<kRegsSoftmax>();
-    run_softmax<D>(warp >> 2, smem, tmem, seg, b, notes, p);
+    run_softmax<D>(warp >> 2, smem, tmem, s_seg, b, notes, p);
   } else if (warp < 16) {
     setmaxnreg_dec<kRegsTurn>();
-    run_turn<D>(warp - 8, smem, seg, b, notes, p);
+    run_turn<D>(warp - 8, smem, s_seg, b, notes, p);
   } else {
     setmaxnreg_dec<kRegsIssue>();
-    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, seg, b, p);
+    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, s_seg, b, p);
   }
   __syncwarp();
   tc_fence_before_sync();
