@@ -143,11 +143,13 @@ DecodePlan tree_plan(int n_seqs, int nodes, int G, int Hkv, int d, int max_pages
 
 bool tensor_tiles(bool tree, int Lq, int G) { return tree && Lq * G > kTreeRows; }
 
-template <int D>
+// ROWS: of a CTA.  Items of 128 rows are in few parts, so that a row's threads take
+// them one after another (32 contexts of 24 nodes: MERGE).
+template <int D, int ROWS>
 int launch_merge(const kv::DecodeParams& p, const DecodePlan& pl, int rows, cudaStream_t stream) {
   // the merge may be set up while the first kernel runs; its CTAs wait for it
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), rows / kv::kMergeRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), rows / ROWS);
   cfg.blockDim = dim3(kv::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -155,7 +157,7 @@ int launch_merge(const kv::DecodeParams& p, const DecodePlan& pl, int rows, cuda
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv::merge_kernel<D>, p, rows) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return cudaLaunchKernelEx(&cfg, kv::merge_kernel<D, ROWS>, p, rows) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 template <int D>
@@ -173,7 +175,7 @@ int launch_tree(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cudaSt
   }
   kernel<<<static_cast<int>(pl.grid), kv::tree::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  return pl.split ? launch_merge<D>(p, pl, kv::tree::kRows, stream) : FA_OK;
+  return pl.split ? launch_merge<D, 4 * kv::kMergeThreads / D>(p, pl, kv::tree::kRows, stream) : FA_OK;
 }
 
 template <int D, int NT, bool TREE>
@@ -191,7 +193,7 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
   }
   kernel<<<static_cast<int>(pl.grid), kv::DecodeCfg<D, NT>::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  return pl.split ? launch_merge<D>(p, pl, 8 * NT, stream) : FA_OK;
+  return pl.split ? launch_merge<D, 2>(p, pl, 8 * NT, stream) : FA_OK;
 }
 
 template <bool TREE>

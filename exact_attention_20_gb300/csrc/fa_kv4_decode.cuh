@@ -960,23 +960,23 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1) decode_kernel(c
   combine<D, NT>(s_entry, s_group, s_groups, smem, s_shared, p);
 }
 
-constexpr int kMergeRows = 2;  // rows of a CTA of merge_kernel
 constexpr int kMergeThreads = 256;
 
-// Block (c, y): rows 2y, 2y+1 of the item that the start of CTA c's range cuts
+// Block (c, y): rows ROWS y ... of the item that the start of CTA c's range cuts
 // first, if it does: its parts' states are merged as the warps' were.  D / 4
-// threads take a row's part, several parts side by side.
-template <int D>
+// threads take a row's part, and several parts are taken side by side where
+// that leaves threads (ROWS = 2: items of few rows in many parts).
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const DecodeParams p, int rows) {
   constexpr int kLanes = D / 4;                               // threads of one row
-  constexpr int kSide = kMergeThreads / (kMergeRows * kLanes);     // parts side by side
-  __shared__ float4 s_o[kSide][kMergeRows][kLanes];
-  __shared__ float2 s_ml[kSide][kMergeRows];
+  constexpr int kSide = kMergeThreads / (ROWS * kLanes);     // parts side by side
+  __shared__ float4 s_o[kSide][ROWS][kLanes];
+  __shared__ float2 s_ml[kSide][ROWS];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has finished and its writes are here
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.s < 0) return;
-  const int lane = threadIdx.x % kLanes, rr = threadIdx.x / kLanes % kMergeRows, side = threadIdx.x / (kLanes * kMergeRows);
-  const int r = blockIdx.y * kMergeRows + rr;
+  const int lane = threadIdx.x % kLanes, rr = threadIdx.x / kLanes % ROWS, side = threadIdx.x / (kLanes * ROWS);
+  const int r = blockIdx.y * ROWS + rr;
   auto row_of = [&](int c) { return (2ll * c + (c == cut.c0 ? 1 : 0)) * rows + r; };
   float M = kNone, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);

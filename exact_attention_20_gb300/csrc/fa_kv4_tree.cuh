@@ -18,7 +18,7 @@
 //   with its own S, P and O in tensor memory, its own running maximum and sum and
 //   its own issuer, so that one's products overlap the other's exponentials and
 //   neither waits for the other's maximum.  An item's two states meet at its end.
-// - Eight warps turn codes into operands, a group of 16 keys each, from rings of
+// - Eight warps turn codes into operands, K or V of 32 keys each, from rings of
 //   their own (bulk copies some tiles ahead, across items).  A tile's K and V each
 //   have two places in shared memory, one for each warpgroup.
 //
@@ -44,14 +44,14 @@ namespace tree {
 
 constexpr int kRows = 128;             // of an item
 constexpr int kKeys = 128;             // of a tile
-constexpr int kTurnWarps = 8;          // a tile's groups
+constexpr int kTurnWarps = 8;          // four for K, four for V; two groups of a tile each
 constexpr int kThreads = 640;
-constexpr int kItemTiles = 2;          // an item's own cost, in tiles
+constexpr int kItemTiles = 8;          // an item's own cost, in tiles
 constexpr int kMinTiles = 2;           // a CTA takes at least, where there are that many
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSiteTree = 8;           // status code: a wait gave up
 // Registers: the launch gives every thread 96 (65536 / 640, rounded down to 8).
-constexpr uint32_t kRegsSoftmax = 136, kRegsTurn = 72, kRegsIssue = 64;
+constexpr uint32_t kRegsSoftmax = 120, kRegsTurn = 88, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsTurn + 128 * kRegsIssue <= kThreads * 96, "register split exceeds the launch");
 
 constexpr int kFixedBars = 18;         // beside the rings'
@@ -128,21 +128,27 @@ struct Segments {
   __device__ __forceinline__ bool whole() const { return count == tiles; }
 };
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& b, const DecodeParams& p) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Waits of a warp for a barrier's phase, for a limited time; false, in every lane,
+// where one gave up.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, const Bars b, int* status, unsigned long long limit_ns) {
   const uint64_t t0 = global_timer_ns();
   uint32_t polls = 0;
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if ((++polls & 31u) == 0u) {
-      if (*b.abort_flag) return false;
-      if (global_timer_ns() - t0 > p.wait_limit_ns) {
+      bool stop = *b.abort_flag != 0;
+      if (!stop && global_timer_ns() - t0 > limit_ns) {
+        stop = true;
         *b.abort_flag = 1;
-        atomicCAS(p.status, 0, kSiteTree);
-        return false;
+        atomicCAS(status, 0, kSiteTree);
       }
+      if (__any_sync(0xffffffffu, stop)) return false;
     }
   }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& b, const DecodeParams& p) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, b, p.status, p.wait_limit_ns);
 }
 
 // Where a turning warp's loads are: a segment, and its tiles that were looked up.
@@ -159,32 +165,37 @@ struct Notes {
   float2 ml[2][kRows];                // the warpgroups' running maxima and sums
   float factor[kRows];                // of the item whose Q is in shared memory
   Ahead ahead[kTurnWarps];
+  int turn;                           // 1 while an issuer has the tensor core
 };
 
 // ---------------------------------------------------------------------------
-// Codes to operands (one warp: a tile's keys 16 w .. 16 w + 15)
+// Codes to operands (warps 0-3: K of a tile's keys 32 w ...; 4-7: V)
 // ---------------------------------------------------------------------------
-// Half of a group, K or V (16 keys x D), into rows key0 .. of a tile: blocks of 16
-// elements, four or two a lane.  A row is 128 bytes of each 64-column slab, its
-// 16-byte chunks permuted by the row's low bits as the 128-byte swizzle wants;
-// the lanes' blocks are dealt so that eight lanes' chunks fall into all banks.
-// scale_of(key, block, byte) may change a block's scale.
+__host__ __device__ constexpr int half_bytes(int d) { return group_bytes(d) / 2; }  // K or V of a group
+
+// K or V of two groups (32 keys x D, half_bytes apart) into rows key0 .. of a tile,
+// blocks of 16 elements, eight or four a lane.  A row is 128 bytes of each
+// 64-column slab, its 16-byte chunks permuted by the row's low bits as the 128-byte
+// swizzle wants; the lanes' blocks are dealt so that eight lanes' chunks fall into
+// all banks.  scale_of(key, block, byte) may change a block's scale.
 template <int D, class Scale>
-__device__ __forceinline__ void turn_group(const uint8_t* raw, uint8_t* tile, int key0, Scale scale_of) {
-  constexpr int kKeysAtOnce = 32 * 16 / D;
+__device__ __forceinline__ void turn_keys(const uint8_t* raw, uint8_t* tile, int key0, Scale scale_of) {
+  constexpr int kKeysAtOnce = 32 * 16 / D, kSteps = 32 / kKeysAtOnce;
   const int lane = threadIdx.x & 31;
   const int block = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
   const int key_in = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
-  uint2 codes[kGroup / kKeysAtOnce];
-  uint32_t scales[kGroup / kKeysAtOnce];
+  uint2 codes[kSteps];
+  uint32_t scales[kSteps];
 #pragma unroll
-  for (int i = 0; i < kGroup / kKeysAtOnce; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int key = i * kKeysAtOnce + key_in;
-    codes[i] = *reinterpret_cast<const uint2*>(raw + key * (D / 2) + block * 8);
-    scales[i] = raw[kGroup * D / 2 + key * (D / 16) + block];
+    const uint8_t* half = raw + (i * kKeysAtOnce >= kGroup ? half_bytes(D) - kGroup * (D / 2) : 0);
+    const uint8_t* half_s = raw + (i * kKeysAtOnce >= kGroup ? half_bytes(D) - kGroup * (D / 16) : 0);
+    codes[i] = *reinterpret_cast<const uint2*>(half + key * (D / 2) + block * 8);
+    scales[i] = half_s[kGroup * D / 2 + key * (D / 16) + block];
   }
 #pragma unroll
-  for (int i = 0; i < kGroup / kKeysAtOnce; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int key = i * kKeysAtOnce + key_in, row = key0 + key;
     const uint32_t sb = scale_of(key, block, scales[i]);
     const uint32_t s = e4m3x2_to_f16x2(sb | (sb << 8));
@@ -200,34 +211,19 @@ __device__ __forceinline__ void turn_group(const uint8_t* raw, uint8_t* tile, in
   }
 }
 
-// Zeros in place of a group that was not loaded.
-template <int D>
-__device__ __forceinline__ void zero_group(uint8_t* tile, int key0) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < Cfg<D>::kSlabs * kGroup * 8 / 32; ++i) {
-    const int n = i * 32 + lane;
-    *reinterpret_cast<uint4*>(tile + n / (kGroup * 8) * Cfg<D>::kSlabBytes + key0 * 128 + n % (kGroup * 8) * 16) = make_uint4(0, 0, 0, 0);
-  }
-}
-
-// The same for a group that is not all context: keys behind the sequence (live
-// of the 16 are its own) and groups that were not loaded are zeros, a V block
+// The same where not all keys are context: keys that are not in `on` (bit per
+// group: behind the sequence or refused) or not below `live` are zeros; a V block
 // that is NaN at a node (the first key's is node0) is zeros, too, and noted.  A
 // call, so that the plain conversion's loop stays short.
 template <int D>
-__device__ __noinline__ void turn_tail(const uint8_t* raw, uint8_t* tile, int key0, bool on, int v, int live, int node0,
-                                       uint32_t number, Notes& notes, const DecodeParams& p) {
+__device__ __noinline__ void turn_tail(const uint8_t* raw, uint8_t* tile, int key0, uint32_t on, int v, int live, int node0,
+                                       uint32_t number, Notes& notes, int nodes) {
   const int lane = threadIdx.x & 31;
   uint32_t* noted = notes.nan[number & 3u];
-  if (!on) {
-    zero_group<D>(tile, key0);
-    return;
-  }
-  if (v && lane < kGroup && node0 + lane >= 0 && node0 + lane < p.Lq) noted[node0 + lane] = number << 8;
+  if (v && node0 + lane >= 0 && node0 + lane < nodes) noted[node0 + lane] = number << 8;
   __syncwarp();
-  turn_group<D>(raw, tile, key0, [&](int key, int block, uint32_t s) {
-    if (key >= live) return 0u;
+  turn_keys<D>(raw, tile, key0, [&](int key, int block, uint32_t s) {
+    if (key >= live || !(on >> (key >> 4) & 1u)) return 0u;
     if (v && (s & 0x7fu) == 0x7fu && node0 + key >= 0) {
       atomicOr(noted + node0 + key, 1u << block);
       notes.any_nan[number & 3u] = number + 1;
@@ -240,21 +236,21 @@ __device__ __noinline__ void turn_tail(const uint8_t* raw, uint8_t* tile, int ke
 template <int D>
 __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, const Bars& b, Notes& notes, const DecodeParams& p) {
   using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, v = w >> 2, pair = w & 3;
   uint8_t* raw = smem + C::kRawOff + w * C::kWarpRaw;
   const uint32_t raw_u32 = smem_u32(raw), raw_bar = b.raw0() + w * C::kRing * 8;
   const int group_shift = p.page_shift - 4;
   const long long head_bytes = static_cast<long long>(row_bytes(D)) << p.page_shift, page_bytes = head_bytes * p.Hkv;
 
   // Loads run kRing tiles ahead, across segments.  Up to 32 tiles' groups are
-  // looked up together, one by each lane, which later issues its copy.
+  // looked up together, one tile's by each lane, which later issues its copies.
   if (lane == 0) notes.ahead[w] = Ahead{seg, 0};
   __syncwarp();
-  const uint8_t* src = nullptr;
-  uint32_t loaded = 0, refused = 0;          // of those looked up
+  const uint8_t *src0 = nullptr, *src1 = nullptr;  // the lane's tile: its two groups
+  uint32_t have = 0;                         // lanes: bit 0, 1: loaded; bit 2, 3: refused (the lane's own)
   int batch = 0, next = 0;
   uint32_t issued = 0, issue_at = 0;         // tiles; the ring place of the next one
-  uint32_t stage_loaded = 0, stage_refused = 0;  // bit per ring place
+  uint32_t stages = 0;                       // `have` of each ring place, four bits each
   auto look_up = [&]() {
     Ahead a = notes.ahead[w];
     Segments& ahead = a.seg;
@@ -265,16 +261,19 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
     }
     if (ahead.left <= 0) return;
     batch = min(32, ahead.data() - a.at);
-    const int group = (ahead.t0 + a.at + lane) * (kKeys / kGroup) + w;
-    const bool exists = lane < batch && group < (ahead.len + kGroup - 1) / kGroup;
-    int page = -1;
-    if (exists) page = __ldg(p.page_table + static_cast<long long>(ahead.s) * p.max_pages + (group >> group_shift));
-    const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages);
-    src = p.cache + page * page_bytes + head_bytes * (ahead.item / p.row_tiles) +
-          static_cast<long long>(group & ((1 << group_shift) - 1)) * group_bytes(D);
-    loaded = __ballot_sync(0xffffffffu, ok);
-    refused = __ballot_sync(0xffffffffu, exists && !ok);
-    if (p.errors && exists && !ok) atomicOr(p.errors, kErrPage);
+    const int group = (ahead.t0 + a.at + lane) * (kKeys / kGroup) + 2 * pair, groups = (ahead.len + kGroup - 1) / kGroup;
+    const bool exists0 = lane < batch && group < groups, exists1 = lane < batch && group + 1 < groups;
+    int page0 = -1, page1 = -1;
+    const int* table = p.page_table + static_cast<long long>(ahead.s) * p.max_pages;
+    if (exists0) page0 = __ldg(table + (group >> group_shift));
+    if (exists1) page1 = group_shift > 0 ? page0 : __ldg(table + group + 1);
+    const bool ok0 = static_cast<uint32_t>(page0) < static_cast<uint32_t>(p.num_pages);
+    const bool ok1 = static_cast<uint32_t>(page1) < static_cast<uint32_t>(p.num_pages);
+    const uint8_t* head = p.cache + head_bytes * (ahead.item / p.row_tiles) + codes_at(D, v);
+    src0 = head + page0 * page_bytes + static_cast<long long>(group & ((1 << group_shift) - 1)) * group_bytes(D);
+    src1 = group_shift > 0 ? src0 + group_bytes(D) : head + page1 * page_bytes;
+    have = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u) | (exists0 && !ok0 ? 4u : 0u) | (exists1 && !ok1 ? 8u : 0u);
+    if (p.errors && (have & 12u)) atomicOr(p.errors, kErrPage);
     a.at += batch;
     __syncwarp();
     if (lane == 0) notes.ahead[w] = a;
@@ -286,16 +285,13 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
       if (batch == 0) return;
     }
     const uint32_t st = issue_at, bar = raw_bar + 8 * st;
-    const uint32_t on = loaded >> next & 1u;
-    stage_loaded = (stage_loaded & ~(1u << st)) | on << st;
-    stage_refused = (stage_refused & ~(1u << st)) | (refused >> next & 1u) << st;
+    const uint32_t has = __shfl_sync(0xffffffffu, have, next);
+    stages = (stages & ~(15u << (4 * st))) | has << (4 * st);
     if (lane == next) {
-      if (on) {
-        mbar_arrive_expect_tx(bar, group_bytes(D));
-        bulk_load(raw_u32 + st * group_bytes(D), src, group_bytes(D), bar);
-      } else {
-        mbar_arrive(bar);
-      }
+      const uint32_t dst = raw_u32 + st * group_bytes(D);
+      mbar_arrive_expect_tx(bar, ((has & 1u) + (has >> 1 & 1u)) * half_bytes(D));
+      if (has & 1u) bulk_load(dst, src0, half_bytes(D), bar);
+      if (has & 2u) bulk_load(dst + half_bytes(D), src1, half_bytes(D), bar);
     }
     issue_at = st + 1 == C::kRing ? 0 : st + 1;
     ++next;
@@ -308,35 +304,31 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
   uint32_t st = 0, phase = 0; // the ring place of the next one, and its barrier's phase
   uint32_t number = 0;        // items with tiles
   bool ok = true;
-  const int key0 = w * kGroup;
+  const int key0 = pair * 2 * kGroup;
+  const uint32_t full = v ? b.v_full(0) : b.k_full(0), empty = v ? b.v_empty(0) : b.k_empty(0);
+  uint8_t* tiles = smem + (v ? C::kVOff : C::kKOff);
 #pragma unroll 1
   for (; seg.left > 0 && ok; seg.next(p)) {
     const int n = seg.data();
     if (n == 0) continue;
     const int prefix = seg.len - p.Lq;
 #pragma unroll 1
-    for (int t = seg.t0; t < seg.t0 + n && ok; ++t, ++c) {
-      const uint32_t place = c & 1u, empty = (c >> 1 & 1u) ^ 1u;
+    for (int t = seg.t0; t < seg.t0 + n; ++t, ++c) {
+      const uint32_t place = c & 1u;
       const int pos = t * kKeys + key0;
-      const bool on = stage_loaded >> st & 1u, plain = on && pos + kGroup <= prefix;
-      ok = __all_sync(0xffffffffu, wait(raw_bar + 8 * st, phase, b, p));
+      const uint32_t has = stages >> (4 * st) & 15u;
+      ok = wait(raw_bar + 8 * st, phase, b, p) && wait(empty + 8 * place, (c >> 1 & 1u) ^ 1u, b, p);
       if (!ok) break;
-      if (lane == 0) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[w] = stage_refused >> st & 1u ? 0xffu : 0u;
-      const uint8_t* group = raw + st * group_bytes(D);
-      // K, then V
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        ok = __all_sync(0xffffffffu, wait(v ? b.v_empty(place) : b.k_empty(place), empty, b, p));
-        if (!ok) break;
-        uint8_t* tile = smem + (v ? C::kVOff : C::kKOff) + place * C::kTileBytes;
-        if (plain) turn_group<D>(group + codes_at(D, v), tile, key0, [](int, int, uint32_t s) { return s; });
-        else turn_tail<D>(group + codes_at(D, v), tile, key0, on, v, seg.len - pos, pos - prefix, number, notes, p);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v ? b.v_full(place) : b.k_full(place));
-      }
+      if (v == 0 && lane < 2) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[2 * pair + lane] = has >> (2 + lane) & 1u ? 0xffu : 0u;
+      const uint8_t* keys = raw + st * group_bytes(D);
+      uint8_t* tile = tiles + place * C::kTileBytes;
+      if ((has & 3u) == 3u && pos + 2 * kGroup <= prefix) turn_keys<D>(keys, tile, key0, [](int, int, uint32_t s) { return s; });
+      else turn_tail<D>(keys, tile, key0, has & 3u, v, seg.len - pos, pos - prefix, number, notes, p.Lq);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * place);
       if (++st == C::kRing) st = 0, phase ^= 1u;
-      issue();  // every lane has read the group
+      issue();  // every lane has read the keys
     }
     ++number;
   }
@@ -376,7 +368,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
 }
 
 template <int D>
-__device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t tmem, Segments seg, const Bars& b, const DecodeParams& p) {
+__device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t tmem, int* turn, Segments seg, const Bars& b, const DecodeParams& p) {
   using C = Cfg<D>;
   const bool leader = (threadIdx.x & 31) == 0;
   const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(0, 0, 1024) >> 32);
@@ -386,22 +378,28 @@ __device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t t
   const uint32_t tm_s = tmem + C::kTmemS + g * C::kTmemGroup, tm_p = tmem + C::kTmemP + g * C::kTmemGroup;
   const uint32_t tm_o = tmem + C::kTmemO + g * C::kTmemGroup;
   bool ok = true;
-  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(bar, parity, b, p)); };
+  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = ok && wait(bar, parity, b, p); };
   uint32_t c = 0, uses = 0, items = 0;  // tiles; this warpgroup's; items with tiles
-  auto qk = [&]() {
-    wait_voted(b.k_full(g), uses & 1u);
-    if (!ok) return;
-    tc_fence_after_sync();
+  // O += P V of this warpgroup's tile and S = Q K^T of its next go to the tensor
+  // core in one piece: with the two issuers' products mixed both warpgroups get
+  // their scores at the same time, and the tensor core waits for both softmaxes.
+  auto take_turn = [&]() {
+    int free = 0;
     if (leader) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
-        mma_ss(tm_s, q_lo + (off >> 4), k_lo + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+      free = atomicExch(turn, 1) == 0;
+      if (!free) {
+        const uint64_t t0 = global_timer_ns();
+        while (!(free = atomicExch(turn, 1) == 0)) {
+          if (*b.abort_flag) break;
+          if (global_timer_ns() - t0 > p.wait_limit_ns) {
+            *b.abort_flag = 1;
+            atomicCAS(p.status, 0, kSiteTree);
+            break;
+          }
+        }
       }
-      umma_commit(b.s_full(g));
-      umma_commit(b.k_empty(g));
     }
-    __syncwarp();
+    ok = __shfl_sync(0xffffffffu, free, 0) != 0;
   };
 #pragma unroll 1
   for (; seg.left > 0 && ok; seg.next(p)) {
@@ -411,23 +409,41 @@ __device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t t
     c += n;
     wait_voted(b.q_full(), items & 1u);
     ++items;
-    if (mine > 0 && ok) qk();
 #pragma unroll 1
-    for (int i = 0; i < mine && ok; ++i) {
-      wait_voted(b.v_full(g), uses & 1u);
-      wait_voted(b.p_ready(g), uses & 1u);
+    for (int i = 0; i <= mine && mine > 0 && ok; ++i) {
+      const bool pv = i > 0, qk = i < mine;
+      if (qk) wait_voted(b.k_full(g), (uses + (pv ? 1u : 0u)) & 1u);
+      if (pv) {
+        wait_voted(b.v_full(g), uses & 1u);
+        wait_voted(b.p_ready(g), uses & 1u);
+      }
+      if (ok) take_turn();
       if (!ok) break;
       tc_fence_after_sync();
       if (leader) {
+        if (pv) {
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tm_o, tm_p + kk * 8, v_lo + kk * 128, hi, idesc_f16_f32(kRows, D, true), i > 0 || kk > 0 ? 1u : 0u);
-        umma_commit(b.v_empty(g));
-        if (i == mine - 1) umma_commit(b.o_done(g));
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(tm_o, tm_p + kk * 8, v_lo + kk * 128, hi, idesc_f16_f32(kRows, D, true), i > 1 || kk > 0 ? 1u : 0u);
+          umma_commit(b.v_empty(g));
+        }
+        if (qk) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
+            mma_ss(tm_s, q_lo + (off >> 4), k_lo + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+          }
+        }
+        atomicExch(turn, 0);
+        if (qk) {
+          umma_commit(b.s_full(g));
+          umma_commit(b.k_empty(g));
+        } else {
+          umma_commit(b.o_done(g));
+        }
       }
       __syncwarp();
-      ++uses;
-      if (i < mine - 1) qk();
+      if (pv) ++uses;
     }
   }
   // Every MMA this thread issued must finish before tensor memory is released.
@@ -525,7 +541,7 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
   const uint32_t tO = tmem + lane_off + C::kTmemO;  // warpgroup 0's; 1's kTmemGroup further on
   bool ok = true;
   uint32_t c = 0, uses = 0, items = 0, done[2] = {0, 0}, number = 0;
-  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(bar, parity, b, p)); };
+  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = ok && wait(bar, parity, b, p); };
   auto arrive = [&](uint32_t bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -559,19 +575,6 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
     const int first = seg.t0 + (static_cast<int>(c & 1u) == g ? 0 : 1);  // this warpgroup's tiles: every other one
     const int prefix = seg.len - p.Lq;
     const uint64_t f2 = f2_pack(factor, factor);
-    // P and its sum from NC scores, two at a time
-    auto exponentials = [&](auto count, const uint32_t* x, uint32_t* pk, uint64_t neg_m2, uint64_t& sum2) {
-      constexpr int kPairs = decltype(count)::value / 2;
-#pragma unroll
-      for (int k = 0; k < kPairs; ++k) {
-        float a, d;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, neg_m2), a, d);
-        a = ex2_approx(a);
-        d = ex2_approx(d);
-        sum2 = f2_add(sum2, f2_pack(a, d));
-        pk[k] = pack_f16x2(a, d);
-      }
-    };
 #pragma unroll 1
     for (int i = 0; i < (g ? mine[1] : mine[0]) && ok; ++i) {
       const int t = first + 2 * i;
@@ -583,83 +586,87 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
         const volatile uint32_t* refusals = notes.skip[(c + static_cast<uint32_t>(t - seg.t0)) & 3u];
         const uint32_t skip_lo = refusals[0], skip_hi = refusals[1];
         const bool masked = (t + 1) * kKeys > prefix || (skip_lo | skip_hi) != 0;
-        bool done = false, over = false;
-        if (i > 0 && !masked) {
-          // Against the present reference.  A sum within f16's range holds no P
-          // above it, so that the maximum is not asked for.
-          const uint64_t neg_m2 = f2_pack(-m, -m);
-          uint64_t sum2 = f2_pack(0.f, 0.f);
-          uint32_t x[64], pk[64];
-          tmem_ld64_wait(tS, x);
-          exponentials(std::integral_constant<int, 64>{}, x, pk, neg_m2, sum2);
-          tmem_ld64_wait(tS + 64, x);
-          exponentials(std::integral_constant<int, 64>{}, x, pk + 32, neg_m2, sum2);
-          float sa, sb;
-          f2_unpack(sum2, sa, sb);
-          done = __all_sync(0xffffffffu, !(sa + sb > 65504.f));
-          over = !done;
-          if (done) {
-            l += sa + sb;
-            tmem_st32(tP, pk);
-            tmem_st32(tP + 32, pk + 32);
-          }
-        }
-        if (!done) {
-          // 32 columns at a time: the maximum first, then the exponentials from S
-          // read again (where P lies over S, its 16 columns over some read before).
-          auto scores = [&](int c4, uint32_t* x) {
-            tmem_ld32_wait(tS + c4 * 32, x);
-            if (!masked) return;
-            // bit e: the row sees key 32 c4 + e
-            const int node0 = t * kKeys + c4 * 32 - prefix;
-            uint32_t v = node0 >= 64 ? 0u : node0 >= 0 ? static_cast<uint32_t>(line >> node0)
-                         : node0 <= -32 ? ~0u : (static_cast<uint32_t>(line) << -node0) | ((1u << -node0) - 1u);
-            const uint32_t refused = (c4 < 2 ? skip_lo : skip_hi) >> (c4 & 1) * 16;
-            if (refused & 1u) v &= 0xffff0000u;
-            if (refused >> 8 & 1u) v &= 0xffffu;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(v >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
-          };
-          float top = -INFINITY;
+        // Half of the tile at a time, in a loop: code that the instruction cache
+        // holds beside the other warps'.  (Where P lies over S, its columns go over
+        // some read before.)
+        float sum = 0.f;
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t x[32];
-            scores(c4, x);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[64];
+          tmem_ld64_wait(tS + half * 64, x);
+          if (masked) {
+            // bit e: the row sees key 64 half + e
+            const int node0 = t * kKeys + half * 64 - prefix;
+            unsigned long long v = node0 >= 64 ? 0ull : node0 >= 0 ? line >> node0
+                                   : node0 <= -64 ? ~0ull : (line << -node0) | ((1ull << -node0) - 1ull);
+            const uint32_t refused = half ? skip_hi : skip_lo;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            for (int q = 0; q < 4; ++q)
+              if (refused >> (8 * q) & 1u) v &= ~(0xffffull << (16 * q));
+            const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+              if (!(hi >> e & 1u)) x[32 + e] = __float_as_uint(-INFINITY);
+            }
           }
-          top *= factor;  // factor > 0: the maximum commutes with it
-          if (__any_sync(0xffffffffu, top - m > (over ? kLift : kLift + kMove))) {
-            const float to = fmaxf(m, top - kLift);
+          float top[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            top[q] = fmaxf(__uint_as_float(x[16 * q]), __uint_as_float(x[16 * q + 1]));
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) top[q] = fmax3(top[q], __uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1]));
+          }
+          const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * factor;  // factor > 0: the maximum commutes with it
+          if (__any_sync(0xffffffffu, most - m > kLift + kMove)) {
+            // The reference moves: what was summed with the old one is brought to the new.
+            const float to = fmaxf(m, most - kLift);
             const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
             m = to;
             l *= alpha;
-            if (i > 0) {  // O holds the sum so far: its last product was done before S was
+            sum *= alpha;
+            if (i > 0) {  // O: its last product was done before S was
               const uint32_t own = tO + g * C::kTmemGroup;
 #pragma unroll 1
-              for (int e = 0; e < D / 32; ++e) {
-                uint32_t o[32];
-                tmem_ld32_wait(own + e * 32, o);
+              for (int e = 0; e < D / 16; ++e) {
+                uint32_t o[16];
+                tmem_ld16_wait(own + e * 16, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st32(own + e * 32, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st16(own + e * 16, o);
               }
+            }
+            if (half > 0) tmem_st_wait();
+#pragma unroll 1
+            for (int e = 0; e < 2 * half; ++e) {  // P of the columns before
+              uint32_t o[16];
+              tmem_ld16_wait(tP + e * 16, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                o[k] = pack_f16x2(f.x * alpha, f.y * alpha);
+              }
+              tmem_st16(tP + e * 16, o);
             }
           }
           const uint64_t neg_m2 = f2_pack(-m, -m);
-          uint64_t sum2 = f2_pack(0.f, 0.f);
-#pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t x[32], pk[16];
-            scores(c4, x);
-            exponentials(std::integral_constant<int, 32>{}, x, pk, neg_m2, sum2);
-            tmem_st16(tP + c4 * 16, pk);
+          uint64_t sum2 = f2_pack(sum, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float a, d;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, neg_m2), a, d);
+            a = ex2_approx(a);
+            d = ex2_approx(d);
+            sum2 = f2_add(sum2, f2_pack(a, d));
+            pk[k] = pack_f16x2(a, d);
           }
+          tmem_st32(tP + half * 32, pk);
           float sa, sb;
           f2_unpack(sum2, sa, sb);
-          l += sa + sb;
+          sum = sa + sb;
         }
+        l += sum;
         tmem_st_wait();
         tc_fence_before_sync();
       }
@@ -793,8 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTurnWarps * C::kRing; ++i) mbar_init(b.raw0() + 8 * i, 1);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(b.k_full(g), kTurnWarps);
-      mbar_init(b.v_full(g), kTurnWarps);
+      mbar_init(b.k_full(g), kTurnWarps / 2);
+      mbar_init(b.v_full(g), kTurnWarps / 2);
       mbar_init(b.k_empty(g), 1);
       mbar_init(b.v_empty(g), 1);
       mbar_init(b.s_full(g), 1);
@@ -807,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     mbar_init(b.drain(), 2);
     *b.abort_flag = 0;
     for (int i = 0; i < 4; ++i) notes.any_nan[i] = 0;
+    notes.turn = 0;
     s_seg.left = 0;
     fence_barrier_init();
   }
@@ -885,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     run_turn<D>(warp - 8, smem, s_seg, b, notes, p);
   } else {
     setmaxnreg_dec<kRegsIssue>();
-    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, s_seg, b, p);
+    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, &notes.turn, s_seg, b, p);
   }
   __syncwarp();
   tc_fence_before_sync();
