@@ -31,7 +31,7 @@
 // into ranges of equal cost, one per CTA, from the lengths on the device; an item
 // cut between CTAs is merged by merge_kernel (fa_kv4_decode.cuh).
 //
-// Warps: 0-7 softmax; 8-15 codes to operands; 16, 17 MMA issuers.
+// Warps: 0-7 softmax; 8-15 codes to operands; 16 MMA issuer.
 #pragma once
 
 #include <type_traits>
@@ -51,7 +51,7 @@ constexpr int kMinTiles = 2;           // a CTA takes at least, where there are 
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSiteTree = 8;           // status code: a wait gave up
 // Registers: the launch gives every thread 96 (65536 / 640, rounded down to 8).
-constexpr uint32_t kRegsSoftmax = 120, kRegsTurn = 88, kRegsIssue = 64;
+constexpr uint32_t kRegsSoftmax = 128, kRegsTurn = 80, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsTurn + 128 * kRegsIssue <= kThreads * 96, "register split exceeds the launch");
 
 constexpr int kFixedBars = 18;         // beside the rings'
@@ -165,7 +165,6 @@ struct Notes {
   float2 ml[2][kRows];                // the warpgroups' running maxima and sums
   float factor[kRows];                // of the item whose Q is in shared memory
   Ahead ahead[kTurnWarps];
-  int turn;                           // 1 while an issuer has the tensor core
 };
 
 // ---------------------------------------------------------------------------
@@ -337,7 +336,7 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuers (warp g: the products of softmax warpgroup g)
+// MMA issuer
 // ---------------------------------------------------------------------------
 // Instruction descriptor for kind::f16 with f16 A and B and an fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn_major) {
@@ -367,84 +366,64 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
+// One warp for both warpgroups, tile after tile: O += P V of the tile before the
+// last (the same warpgroup's) and S = Q K^T of this one go to the tensor core in
+// one piece, so that one warpgroup has its softmax while the other has the tensor
+// core.  (Two warps, each for one of them, drifted into step: both softmaxes at
+// the same time, with the tensor core idle.)
 template <int D>
-__device__ __forceinline__ void run_issue(uint32_t g, uint32_t sbase, uint32_t tmem, int* turn, Segments seg, const Bars& b, const DecodeParams& p) {
+__device__ __forceinline__ void run_issue(uint32_t sbase, uint32_t tmem, Segments seg, const Bars& b, const DecodeParams& p) {
   using C = Cfg<D>;
   const bool leader = (threadIdx.x & 31) == 0;
   const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(0, 0, 1024) >> 32);
   const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kQOff, 16, 1024));
-  const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kKOff + g * C::kTileBytes, 16, 1024));
-  const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kVOff + g * C::kTileBytes, C::kSlabBytes, 1024));
-  const uint32_t tm_s = tmem + C::kTmemS + g * C::kTmemGroup, tm_p = tmem + C::kTmemP + g * C::kTmemGroup;
-  const uint32_t tm_o = tmem + C::kTmemO + g * C::kTmemGroup;
+  const uint32_t k_lo0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kKOff, 16, 1024));
+  const uint32_t v_lo0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kVOff, C::kSlabBytes, 1024));
   bool ok = true;
   auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = ok && wait(bar, parity, b, p); };
-  uint32_t c = 0, uses = 0, items = 0;  // tiles; this warpgroup's; items with tiles
-  // O += P V of this warpgroup's tile and S = Q K^T of its next go to the tensor
-  // core in one piece: with the two issuers' products mixed both warpgroups get
-  // their scores at the same time, and the tensor core waits for both softmaxes.
-  auto take_turn = [&]() {
-    int free = 0;
-    if (leader) {
-      free = atomicExch(turn, 1) == 0;
-      if (!free) {
-        const uint64_t t0 = global_timer_ns();
-        while (!(free = atomicExch(turn, 1) == 0)) {
-          if (*b.abort_flag) break;
-          if (global_timer_ns() - t0 > p.wait_limit_ns) {
-            *b.abort_flag = 1;
-            atomicCAS(p.status, 0, kSiteTree);
-            break;
-          }
-        }
-      }
-    }
-    ok = __shfl_sync(0xffffffffu, free, 0) != 0;
-  };
+  uint32_t c = 0, items = 0;  // tiles; items with tiles
 #pragma unroll 1
   for (; seg.left > 0 && ok; seg.next(p)) {
     const int n = seg.data();
     if (n == 0) continue;
-    const int mine = (n + ((c & 1u) == g ? 1 : 0)) / 2;  // of the segment's tiles, dealt in turn
-    c += n;
     wait_voted(b.q_full(), items & 1u);
     ++items;
+    // step i: P V of tile i - 2 and Q K^T of tile i, where there are such
 #pragma unroll 1
-    for (int i = 0; i <= mine && mine > 0 && ok; ++i) {
-      const bool pv = i > 0, qk = i < mine;
-      if (qk) wait_voted(b.k_full(g), (uses + (pv ? 1u : 0u)) & 1u);
+    for (int i = 0; i < n + 2 && ok; ++i, ++c) {
+      const bool pv = i >= 2, qk = i < n;
+      if (i == 1 && n == 1) continue;  // nothing of the other warpgroup
+      const uint32_t g = c & 1u;  // of tile i, and of tile i - 2
+      if (qk) wait_voted(b.k_full(g), c >> 1 & 1u);
       if (pv) {
-        wait_voted(b.v_full(g), uses & 1u);
-        wait_voted(b.p_ready(g), uses & 1u);
+        wait_voted(b.v_full(g), (c - 2) >> 1 & 1u);
+        wait_voted(b.p_ready(g), (c - 2) >> 1 & 1u);
       }
-      if (ok) take_turn();
       if (!ok) break;
       tc_fence_after_sync();
       if (leader) {
+        const uint32_t tm = tmem + g * C::kTmemGroup, place = g * (C::kTileBytes >> 4);
         if (pv) {
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tm_o, tm_p + kk * 8, v_lo + kk * 128, hi, idesc_f16_f32(kRows, D, true), i > 1 || kk > 0 ? 1u : 0u);
+            mma_ts(tm + C::kTmemO, tm + C::kTmemP + kk * 8, v_lo0 + place + kk * 128, hi, idesc_f16_f32(kRows, D, true),
+                   i > 3 || kk > 0 ? 1u : 0u);
           umma_commit(b.v_empty(g));
         }
         if (qk) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
-            mma_ss(tm_s, q_lo + (off >> 4), k_lo + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+            mma_ss(tm + C::kTmemS, q_lo + (off >> 4), k_lo0 + place + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
           }
-        }
-        atomicExch(turn, 0);
-        if (qk) {
           umma_commit(b.s_full(g));
           umma_commit(b.k_empty(g));
-        } else {
-          umma_commit(b.o_done(g));
         }
+        if (pv && !qk) umma_commit(b.o_done(g));
       }
       __syncwarp();
-      if (pv) ++uses;
     }
+    c -= 2;
   }
   // Every MMA this thread issued must finish before tensor memory is released.
   if (leader) umma_commit(b.drain());
@@ -592,79 +571,94 @@ __device__ __forceinline__ void run_softmax(int g, uint8_t* smem, uint32_t tmem,
         float sum = 0.f;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t x[64];
-          tmem_ld64_wait(tS + half * 64, x);
-          if (masked) {
-            // bit e: the row sees key 64 half + e
-            const int node0 = t * kKeys + half * 64 - prefix;
-            unsigned long long v = node0 >= 64 ? 0ull : node0 >= 0 ? line >> node0
-                                   : node0 <= -64 ? ~0ull : (line << -node0) | ((1ull << -node0) - 1ull);
-            const uint32_t refused = half ? skip_hi : skip_lo;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (refused >> (8 * q) & 1u) v &= ~(0xffffull << (16 * q));
-            const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(lo >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
-              if (!(hi >> e & 1u)) x[32 + e] = __float_as_uint(-INFINITY);
-            }
-          }
-          float top[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            top[q] = fmaxf(__uint_as_float(x[16 * q]), __uint_as_float(x[16 * q + 1]));
-#pragma unroll
-            for (int e = 2; e < 16; e += 2) top[q] = fmax3(top[q], __uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1]));
-          }
-          const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * factor;  // factor > 0: the maximum commutes with it
-          if (__any_sync(0xffffffffu, most - m > kLift + kMove)) {
-            // The reference moves: what was summed with the old one is brought to the new.
-            const float to = fmaxf(m, most - kLift);
-            const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
-            m = to;
-            l *= alpha;
-            sum *= alpha;
-            if (i > 0) {  // O: its last product was done before S was
-              const uint32_t own = tO + g * C::kTmemGroup;
-#pragma unroll 1
-              for (int e = 0; e < D / 16; ++e) {
-                uint32_t o[16];
-                tmem_ld16_wait(own + e * 16, o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st16(own + e * 16, o);
-              }
-            }
-            if (half > 0) tmem_st_wait();
-#pragma unroll 1
-            for (int e = 0; e < 2 * half; ++e) {  // P of the columns before
-              uint32_t o[16];
-              tmem_ld16_wait(tP + e * 16, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
-                o[k] = pack_f16x2(f.x * alpha, f.y * alpha);
-              }
-              tmem_st16(tP + e * 16, o);
-            }
-          }
-          const uint64_t neg_m2 = f2_pack(-m, -m);
-          uint64_t sum2 = f2_pack(sum, 0.f);
+          // Against the present reference first: a sum within f16's range holds no P
+          // above it.  Else the half's maximum is found, the reference moved, and P
+          // taken again (an item's first tile, and later hardly ever).
           uint32_t pk[32];
+          uint64_t sum2;
+          bool again = false;
+#pragma unroll 1
+          for (;;) {
+            uint32_t x[64];
+            tmem_ld64_wait(tS + half * 64, x);
+            if (masked) {
+              // bit e: the row sees key 64 half + e
+              const int node0 = t * kKeys + half * 64 - prefix;
+              unsigned long long v = node0 >= 64 ? 0ull : node0 >= 0 ? line >> node0
+                                     : node0 <= -64 ? ~0ull : (line << -node0) | ((1ull << -node0) - 1ull);
+              const uint32_t refused = half ? skip_hi : skip_lo;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float a, d;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, neg_m2), a, d);
-            a = ex2_approx(a);
-            d = ex2_approx(d);
-            sum2 = f2_add(sum2, f2_pack(a, d));
-            pk[k] = pack_f16x2(a, d);
+              for (int q = 0; q < 4; ++q)
+                if (refused >> (8 * q) & 1u) v &= ~(0xffffull << (16 * q));
+              const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (!(lo >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+                if (!(hi >> e & 1u)) x[32 + e] = __float_as_uint(-INFINITY);
+              }
+            }
+            if (again) {
+              float top[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                top[q] = fmaxf(__uint_as_float(x[16 * q]), __uint_as_float(x[16 * q + 1]));
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) top[q] = fmax3(top[q], __uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1]));
+              }
+              const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * factor;  // factor > 0: the maximum commutes with it
+              const float to = fmaxf(m, most - kLift);
+              const float alpha = to == m ? 1.f : ex2_approx(m - to);  // 0 from kNone
+              m = to;
+              l *= alpha;
+              sum *= alpha;
+              // what was summed with the old reference is brought to the new:
+              if (i > 0) {  // O, whose last product was done before S was,
+                const uint32_t own = tO + g * C::kTmemGroup;
+#pragma unroll 1
+                for (int e = 0; e < D / 16; ++e) {
+                  uint32_t o[16];
+                  tmem_ld16_wait(own + e * 16, o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                  tmem_st16(own + e * 16, o);
+                }
+              }
+              if (half > 0) {  // and P of the first half
+                tmem_st_wait();
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t o[16];
+                  tmem_ld16_wait(tP + e * 16, o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                    o[k] = pack_f16x2(f.x * alpha, f.y * alpha);
+                  }
+                  tmem_st16(tP + e * 16, o);
+                }
+              }
+            }
+            const uint64_t neg_m2 = f2_pack(-m, -m);
+            sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float a, d;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, neg_m2), a, d);
+              a = ex2_approx(a);
+              d = ex2_approx(d);
+              sum2 = f2_add(sum2, f2_pack(a, d));
+              pk[k] = pack_f16x2(a, d);
+            }
+            if (again) break;
+            float sa, sb;
+            f2_unpack(sum2, sa, sb);
+            again = __any_sync(0xffffffffu, sa + sb > 65504.f);
+            if (!again) break;
           }
           tmem_st32(tP + half * 32, pk);
           float sa, sb;
           f2_unpack(sum2, sa, sb);
-          sum = sa + sb;
+          sum += sa + sb;
         }
         l += sum;
         tmem_st_wait();
@@ -811,10 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     mbar_init(b.q_full(), 8);
     mbar_init(b.states(), 8);
     mbar_init(b.written(), 8);
-    mbar_init(b.drain(), 2);
+    mbar_init(b.drain(), 1);
     *b.abort_flag = 0;
     for (int i = 0; i < 4; ++i) notes.any_nan[i] = 0;
-    notes.turn = 0;
     s_seg.left = 0;
     fence_barrier_init();
   }
@@ -893,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     run_turn<D>(warp - 8, smem, s_seg, b, notes, p);
   } else {
     setmaxnreg_dec<kRegsIssue>();
-    if (warp < 18) run_issue<D>(warp - 16, sbase, tmem, &notes.turn, s_seg, b, p);
+    if (warp == 16) run_issue<D>(sbase, tmem, s_seg, b, p);
   }
   __syncwarp();
   tc_fence_before_sync();
