@@ -18,8 +18,8 @@
 //   with its own S, P and O in tensor memory, its own running maximum and sum and
 //   its own issuer, so that one's products overlap the other's exponentials and
 //   neither waits for the other's maximum.  An item's two states meet at its end.
-// - Eight warps turn codes into operands, K or V of 32 keys each, from rings of
-//   their own (bulk copies some tiles ahead, across items).  A tile's K and V each
+// - Eight warps turn codes into operands, K or V of 32 keys each, from a ring that
+//   one warp fills (bulk copies some tiles ahead, across items).  A tile's K and V each
 //   have two places in shared memory, one for each warpgroup.
 //
 // What a row does not see must not reach it: scores are replaced by -inf, bit by
@@ -31,7 +31,7 @@
 // into ranges of equal cost, one per CTA, from the lengths on the device; an item
 // cut between CTAs is merged by merge_kernel (fa_kv4_decode.cuh).
 //
-// Warps: 0-7 softmax; 8-15 codes to operands; 16 MMA issuer.
+// Warps: 0-7 softmax; 8-15 codes to operands; 16 MMA issuer; 17 loads.
 #pragma once
 
 #include <type_traits>
@@ -61,14 +61,14 @@ struct Cfg {
   static constexpr int kSlabs = D / 64;                 // 64 columns of d each
   static constexpr int kSlabBytes = 128 * 128;          // 128 rows of 128 bytes
   static constexpr int kTileBytes = kSlabs * kSlabBytes;
-  static constexpr int kRing = D == 128 ? 3 : 6;        // tiles ahead, of a turning warp's group
+  static constexpr int kRing = D == 128 ? 3 : 6;        // tiles of codes and scales
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTileBytes;              // two places
   static constexpr int kVOff = kKOff + 2 * kTileBytes;  // two places
   static constexpr int kRawOff = kVOff + 2 * kTileBytes;
-  static constexpr int kWarpRaw = kRing * group_bytes(D);
-  static constexpr int kBarOff = kRawOff + kTurnWarps * kWarpRaw;
-  static constexpr int kNumBars = kFixedBars + kTurnWarps * kRing;
+  static constexpr int kRawTile = kKeys / kGroup * group_bytes(D);
+  static constexpr int kBarOff = kRawOff + kRing * kRawTile;
+  static constexpr int kNumBars = kFixedBars + 2 * kRing;
   static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + alignment slack
   static_assert(kSmemBytes + 4096 <= 232448, "227 KB with the static part");
@@ -91,7 +91,8 @@ struct Bars {
   __device__ __forceinline__ uint32_t states() const { return at + 120; }   // between the warpgroups: an item's states are there,
   __device__ __forceinline__ uint32_t written() const { return at + 128; }  // its O has been read
   __device__ __forceinline__ uint32_t drain() const { return at + 136; }
-  __device__ __forceinline__ uint32_t raw0() const { return at + 144; }     // [warp][kRing]
+  __device__ __forceinline__ uint32_t raw(uint32_t st) const { return at + 144 + 16 * st; }  // a ring place is full, empty
+  __device__ __forceinline__ uint32_t raw_empty(uint32_t st) const { return at + 152 + 16 * st; }
 };
 // kv4's costs and walk over the concatenated items, in tiles of 128 keys.
 __device__ __forceinline__ int data_tiles(int len) { return (len + kKeys - 1) / kKeys; }
@@ -151,12 +152,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& 
   return wait_on(bar, parity, b, p.status, p.wait_limit_ns);
 }
 
-// Where a turning warp's loads are: a segment, and its tiles that were looked up.
-struct Ahead {
-  Segments seg;
-  int at;
-};
-
 // What the warps pass each other beside the barriers.
 struct Notes {
   uint32_t skip[4][2];                // a tile's groups whose page was refused (a byte each), by tile number mod 4
@@ -164,15 +159,13 @@ struct Notes {
   uint32_t any_nan[4];                // the item number + 1 where there is one
   float2 ml[2][kRows];                // the warpgroups' running maxima and sums
   float factor[kRows];                // of the item whose Q is in shared memory
-  Ahead ahead[kTurnWarps];
+  uint32_t raw[8];                    // by ring place: a bit for each group that was loaded, and from bit 8 for each refused
 };
 
 // ---------------------------------------------------------------------------
 // Codes to operands (warps 0-3: K of a tile's keys 32 w ...; 4-7: V)
 // ---------------------------------------------------------------------------
-__host__ __device__ constexpr int half_bytes(int d) { return group_bytes(d) / 2; }  // K or V of a group
-
-// K or V of two groups (32 keys x D, half_bytes apart) into rows key0 .. of a tile,
+// K or V of two groups (32 keys x D) into rows key0 .. of a tile,
 // blocks of 16 elements, eight or four a lane.  A row is 128 bytes of each
 // 64-column slab, its 16-byte chunks permuted by the row's low bits as the 128-byte
 // swizzle wants; the lanes' blocks are dealt so that eight lanes' chunks fall into
@@ -188,8 +181,8 @@ __device__ __forceinline__ void turn_keys(const uint8_t* raw, uint8_t* tile, int
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int key = i * kKeysAtOnce + key_in;
-    const uint8_t* half = raw + (i * kKeysAtOnce >= kGroup ? half_bytes(D) - kGroup * (D / 2) : 0);
-    const uint8_t* half_s = raw + (i * kKeysAtOnce >= kGroup ? half_bytes(D) - kGroup * (D / 16) : 0);
+    const uint8_t* half = raw + (i * kKeysAtOnce >= kGroup ? group_bytes(D) - kGroup * (D / 2) : 0);
+    const uint8_t* half_s = raw + (i * kKeysAtOnce >= kGroup ? group_bytes(D) - kGroup * (D / 16) : 0);
     codes[i] = *reinterpret_cast<const uint2*>(half + key * (D / 2) + block * 8);
     scales[i] = half_s[kGroup * D / 2 + key * (D / 16) + block];
   }
@@ -236,74 +229,12 @@ template <int D>
 __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, const Bars& b, Notes& notes, const DecodeParams& p) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31, v = w >> 2, pair = w & 3;
-  uint8_t* raw = smem + C::kRawOff + w * C::kWarpRaw;
-  const uint32_t raw_u32 = smem_u32(raw), raw_bar = b.raw0() + w * C::kRing * 8;
-  const int group_shift = p.page_shift - 4;
-  const long long head_bytes = static_cast<long long>(row_bytes(D)) << p.page_shift, page_bytes = head_bytes * p.Hkv;
-
-  // Loads run kRing tiles ahead, across segments.  Up to 32 tiles' groups are
-  // looked up together, one tile's by each lane, which later issues its copies.
-  if (lane == 0) notes.ahead[w] = Ahead{seg, 0};
-  __syncwarp();
-  const uint8_t *src0 = nullptr, *src1 = nullptr;  // the lane's tile: its two groups
-  uint32_t have = 0;                         // lanes: bit 0, 1: loaded; bit 2, 3: refused (the lane's own)
-  int batch = 0, next = 0;
-  uint32_t issued = 0, issue_at = 0;         // tiles; the ring place of the next one
-  uint32_t stages = 0;                       // `have` of each ring place, four bits each
-  auto look_up = [&]() {
-    Ahead a = notes.ahead[w];
-    Segments& ahead = a.seg;
-    batch = next = 0;
-    while (ahead.left > 0 && a.at >= ahead.data()) {
-      ahead.next(p);
-      a.at = 0;
-    }
-    if (ahead.left <= 0) return;
-    batch = min(32, ahead.data() - a.at);
-    const int group = (ahead.t0 + a.at + lane) * (kKeys / kGroup) + 2 * pair, groups = (ahead.len + kGroup - 1) / kGroup;
-    const bool exists0 = lane < batch && group < groups, exists1 = lane < batch && group + 1 < groups;
-    int page0 = -1, page1 = -1;
-    const int* table = p.page_table + static_cast<long long>(ahead.s) * p.max_pages;
-    if (exists0) page0 = __ldg(table + (group >> group_shift));
-    if (exists1) page1 = group_shift > 0 ? page0 : __ldg(table + group + 1);
-    const bool ok0 = static_cast<uint32_t>(page0) < static_cast<uint32_t>(p.num_pages);
-    const bool ok1 = static_cast<uint32_t>(page1) < static_cast<uint32_t>(p.num_pages);
-    const uint8_t* head = p.cache + head_bytes * (ahead.item / p.row_tiles) + codes_at(D, v);
-    src0 = head + page0 * page_bytes + static_cast<long long>(group & ((1 << group_shift) - 1)) * group_bytes(D);
-    src1 = group_shift > 0 ? src0 + group_bytes(D) : head + page1 * page_bytes;
-    have = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u) | (exists0 && !ok0 ? 4u : 0u) | (exists1 && !ok1 ? 8u : 0u);
-    if (p.errors && (have & 12u)) atomicOr(p.errors, kErrPage);
-    a.at += batch;
-    __syncwarp();
-    if (lane == 0) notes.ahead[w] = a;
-    __syncwarp();
-  };
-  auto issue = [&]() {
-    if (next == batch) {
-      look_up();
-      if (batch == 0) return;
-    }
-    const uint32_t st = issue_at, bar = raw_bar + 8 * st;
-    const uint32_t has = __shfl_sync(0xffffffffu, have, next);
-    stages = (stages & ~(15u << (4 * st))) | has << (4 * st);
-    if (lane == next) {
-      const uint32_t dst = raw_u32 + st * group_bytes(D);
-      mbar_arrive_expect_tx(bar, ((has & 1u) + (has >> 1 & 1u)) * half_bytes(D));
-      if (has & 1u) bulk_load(dst, src0, half_bytes(D), bar);
-      if (has & 2u) bulk_load(dst + half_bytes(D), src1, half_bytes(D), bar);
-    }
-    issue_at = st + 1 == C::kRing ? 0 : st + 1;
-    ++next;
-    ++issued;
-  };
-#pragma unroll 1
-  for (int i = 0; i < C::kRing; ++i) issue();
-
   uint32_t c = 0;             // tiles taken
   uint32_t st = 0, phase = 0; // the ring place of the next one, and its barrier's phase
   uint32_t number = 0;        // items with tiles
   bool ok = true;
   const int key0 = pair * 2 * kGroup;
+  const uint8_t* raw = smem + C::kRawOff + pair * 2 * group_bytes(D) + codes_at(D, v);
   const uint32_t full = v ? b.v_full(0) : b.k_full(0), empty = v ? b.v_empty(0) : b.k_empty(0);
   uint8_t* tiles = smem + (v ? C::kVOff : C::kKOff);
 #pragma unroll 1
@@ -315,24 +246,86 @@ __device__ __forceinline__ void run_turn(int w, uint8_t* smem, Segments seg, con
     for (int t = seg.t0; t < seg.t0 + n; ++t, ++c) {
       const uint32_t place = c & 1u;
       const int pos = t * kKeys + key0;
-      const uint32_t has = stages >> (4 * st) & 15u;
-      ok = wait(raw_bar + 8 * st, phase, b, p) && wait(empty + 8 * place, (c >> 1 & 1u) ^ 1u, b, p);
+      ok = wait(b.raw(st), phase, b, p) && wait(empty + 8 * place, (c >> 1 & 1u) ^ 1u, b, p);
       if (!ok) break;
-      if (v == 0 && lane < 2) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[2 * pair + lane] = has >> (2 + lane) & 1u ? 0xffu : 0u;
-      const uint8_t* keys = raw + st * group_bytes(D);
+      const uint32_t has = notes.raw[st] >> (2 * pair);
+      if (v == 0 && lane < 2) reinterpret_cast<uint8_t*>(notes.skip[c & 3u])[2 * pair + lane] = has >> (8 + lane) & 1u ? 0xffu : 0u;
+      const uint8_t* keys = raw + st * C::kRawTile;
       uint8_t* tile = tiles + place * C::kTileBytes;
       if ((has & 3u) == 3u && pos + 2 * kGroup <= prefix) turn_keys<D>(keys, tile, key0, [](int, int, uint32_t s) { return s; });
       else turn_tail<D>(keys, tile, key0, has & 3u, v, seg.len - pos, pos - prefix, number, notes, p.Lq);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + 8 * place);
+      if (lane == 0) {
+        mbar_arrive(full + 8 * place);
+        mbar_arrive(b.raw_empty(st));
+      }
       if (++st == C::kRing) st = 0, phase ^= 1u;
-      issue();  // every lane has read the keys
     }
     ++number;
   }
-  // Copies still in flight land before the CTA exits (only after a wait gave up).
-  for (uint32_t i = c; i < issued; ++i) mbar_wait_bounded(raw_bar + 8 * (i % C::kRing), i / C::kRing & 1u, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// Loads (one warp): tiles of codes and scales, a copy for each group
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void run_load(uint32_t sbase, Segments seg, const Bars& b, Notes& notes, const DecodeParams& p) {
+  using C = Cfg<D>;
+  constexpr int kGroups = kKeys / kGroup, kAtOnce = 32 / kGroups;  // tiles looked up together
+  const int lane = threadIdx.x & 31, group_in = lane % kGroups, tile_in = lane / kGroups;
+  const int group_shift = p.page_shift - 4;
+  const long long head_bytes = static_cast<long long>(row_bytes(D)) << p.page_shift, page_bytes = head_bytes * p.Hkv;
+  // a batch: up to kAtOnce tiles of one segment, and what this lane has to copy of them
+  struct Batch {
+    const uint8_t* head;  // the KV head's part of page 0
+    int count, group, page;
+    bool exists;
+  };
+  int at = 0;  // tiles of the segment that were looked up
+  auto look_up = [&]() {
+    Batch x{nullptr, 0, 0, -1, false};
+    while (seg.left > 0 && at >= seg.data()) {
+      seg.next(p);
+      at = 0;
+    }
+    if (seg.left <= 0) return x;
+    x.count = min(kAtOnce, seg.data() - at);
+    x.group = (seg.t0 + at + tile_in) * kGroups + group_in;
+    x.exists = tile_in < x.count && x.group * kGroup < seg.len;
+    if (x.exists) x.page = __ldg(p.page_table + static_cast<long long>(seg.s) * p.max_pages + (x.group >> group_shift));
+    x.head = p.cache + head_bytes * (seg.item / p.row_tiles);
+    at += x.count;
+    return x;
+  };
+  uint32_t st = 0, phase = 0, issued = 0;
+  bool ok = true;
+  Batch now = look_up();
+#pragma unroll 1
+  while (now.count > 0 && ok) {
+    const Batch next = look_up();  // on its way while this one is issued
+    const bool on = static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.num_pages);
+    const uint32_t loaded = __ballot_sync(0xffffffffu, on), refused = __ballot_sync(0xffffffffu, now.exists && !on);
+    if (p.errors && now.exists && !on) atomicOr(p.errors, kErrPage);
+    const uint8_t* src = now.head + now.page * page_bytes + static_cast<long long>(now.group & ((1 << group_shift) - 1)) * group_bytes(D);
+#pragma unroll 1
+    for (int i = 0; i < now.count; ++i, ++issued) {
+      ok = wait(b.raw_empty(st), phase ^ 1u, b, p);
+      if (!ok) break;
+      const uint32_t has = loaded >> (i * kGroups) & 0xffu;
+      if (lane == 0) {
+        notes.raw[st] = has | (refused >> (i * kGroups) & 0xffu) << 8;
+        mbar_arrive_expect_tx(b.raw(st), __popc(has) * group_bytes(D));
+      }
+      __syncwarp();
+      if (tile_in == i && on) bulk_load(sbase + C::kRawOff + st * C::kRawTile + group_in * group_bytes(D), src, group_bytes(D), b.raw(st));
+      if (++st == C::kRing) st = 0, phase ^= 1u;
+    }
+    now = next;
+  }
+  // Every copy that was started lands before the CTA exits, also after a wait gave up.
+  const uint32_t first = issued > static_cast<uint32_t>(C::kRing) ? issued - C::kRing : 0;
+  for (uint32_t i = first; i < issued; ++i) mbar_wait_bounded(b.raw(i % C::kRing), i / C::kRing & 1u, p.wait_limit_ns);
 }
 
 // ---------------------------------------------------------------------------
@@ -791,8 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   const Bars b{sbase + C::kBarOff, reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4)};
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kTurnWarps * C::kRing; ++i) mbar_init(b.raw0() + 8 * i, 1);
+  if (threadIdx.x == 0) s_seg.left = 0;
+  if (threadIdx.x == 18 * 32) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(b.raw(i), 1);
+      mbar_init(b.raw_empty(i), kTurnWarps);
+    }
     for (int g = 0; g < 2; ++g) {
       mbar_init(b.k_full(g), kTurnWarps / 2);
       mbar_init(b.v_full(g), kTurnWarps / 2);
@@ -808,10 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     mbar_init(b.drain(), 1);
     *b.abort_flag = 0;
     for (int i = 0; i < 4; ++i) notes.any_nan[i] = 0;
-    s_seg.left = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x < 4 * kMaxTreeNodes) notes.nan[threadIdx.x / kMaxTreeNodes][threadIdx.x % kMaxTreeNodes] = 0xffffffffu;
+  if (threadIdx.x >= 256 && threadIdx.x < 256 + 4 * kMaxTreeNodes) notes.nan[(threadIdx.x - 256) / kMaxTreeNodes][threadIdx.x % kMaxTreeNodes] = 0xffffffffu;
   if (warp == 16) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_alloc_permit();
@@ -829,8 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     const long long all = total * items;
     const long long ctas = min(static_cast<long long>(gridDim.x), (all + kMinTiles - 1) / kMinTiles);
     const long long c = blockIdx.x;
-    const long long begin = c < ctas ? all * c / ctas : all;
-    const int n = c < ctas ? static_cast<int>(min(all * (c + 1) / ctas - begin, 0x7fffffffll)) : 0;
+    auto share = [&](long long i) {  // all * i / ctas; a 64-bit division takes a few hundred cycles
+      const long long x = all * i;
+      return x <= 0xffffffffll ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(ctas)) : x / ctas;
+    };
+    const long long begin = c < ctas ? share(c) : all;
+    const int n = c < ctas ? static_cast<int>(min(share(c + 1) - begin, 0x7fffffffll)) : 0;
     if (n > 0 && begin >= before * items && begin < (before + mine) * items) {  // this thread's sequences hold the range's start
       long long at = begin - before * items;
       Segments w;
@@ -844,14 +844,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
       }
       w.tiles = tiles_of(w.len);
       w.left = n;
-      w.item = static_cast<int>(at / cost);
+      w.item = at <= 0x7fffffffll ? static_cast<int>(at) / cost : static_cast<int>(at / cost);
       const int in_item = static_cast<int>(at - static_cast<long long>(w.item) * cost);
       w.set(in_item);
       s_seg = w;
       if (w.t0 > 0) {
         // the range starts within an item: is this the item's first cut?
         const long long a = begin - in_item;  // its start
-        if (all * (c - 1) / ctas <= a + kItemTiles)
+        if (share(c - 1) <= a + kItemTiles)
           p.cuts[c] = Cut{w.s, w.item, static_cast<int>(c - 1), static_cast<int>(((a + cost) * ctas + all - 1) / all - 1)};
       }
     }
@@ -887,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
   } else {
     setmaxnreg_dec<kRegsIssue>();
     if (warp == 16) run_issue<D>(sbase, tmem, s_seg, b, p);
+    else if (warp == 17) run_load<D>(sbase, s_seg, b, notes, p);
   }
   __syncwarp();
   tc_fence_before_sync();
