@@ -147,6 +147,23 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, const Bar
     }
   }
 }
+// The same of one thread.
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, const Bars& b, const DecodeParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t polls = 0;
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((++polls & 31u) == 0u) {
+      if (*b.abort_flag) return false;
+      if (global_timer_ns() - t0 > p.wait_limit_ns) {
+        *b.abort_flag = 1;
+        atomicCAS(p.status, 0, kSiteTree);
+        return false;
+      }
+    }
+  }
+}
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Bars& b, const DecodeParams& p) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return wait_on(bar, parity, b, p.status, p.wait_limit_ns);
@@ -359,27 +376,25 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
-// One warp for both warpgroups, tile after tile: O += P V of the tile before the
+// One thread for both warpgroups, tile after tile: O += P V of the tile before the
 // last (the same warpgroup's) and S = Q K^T of this one go to the tensor core in
 // one piece, so that one warpgroup has its softmax while the other has the tensor
-// core.  (Two warps, each for one of them, drifted into step: both softmaxes at
+// core.  (Two issuers, each for one of them, drifted into step: both softmaxes at
 // the same time, with the tensor core idle.)
 template <int D>
 __device__ __forceinline__ void run_issue(uint32_t sbase, uint32_t tmem, Segments seg, const Bars& b, const DecodeParams& p) {
   using C = Cfg<D>;
-  const bool leader = (threadIdx.x & 31) == 0;
   const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(0, 0, 1024) >> 32);
   const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kQOff, 16, 1024));
   const uint32_t k_lo0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kKOff, 16, 1024));
   const uint32_t v_lo0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kVOff, C::kSlabBytes, 1024));
   bool ok = true;
-  auto wait_voted = [&](uint32_t bar, uint32_t parity) { ok = ok && wait(bar, parity, b, p); };
   uint32_t c = 0, items = 0;  // tiles; items with tiles
 #pragma unroll 1
   for (; seg.left > 0 && ok; seg.next(p)) {
     const int n = seg.data();
     if (n == 0) continue;
-    wait_voted(b.q_full(), items & 1u);
+    ok = wait_alone(b.q_full(), items & 1u, b, p);
     ++items;
     // step i: P V of tile i - 2 and Q K^T of tile i, where there are such
 #pragma unroll 1
@@ -387,40 +402,34 @@ __device__ __forceinline__ void run_issue(uint32_t sbase, uint32_t tmem, Segment
       const bool pv = i >= 2, qk = i < n;
       if (i == 1 && n == 1) continue;  // nothing of the other warpgroup
       const uint32_t g = c & 1u;  // of tile i, and of tile i - 2
-      if (qk) wait_voted(b.k_full(g), c >> 1 & 1u);
-      if (pv) {
-        wait_voted(b.v_full(g), (c - 2) >> 1 & 1u);
-        wait_voted(b.p_ready(g), (c - 2) >> 1 & 1u);
-      }
+      if (qk) ok = wait_alone(b.k_full(g), c >> 1 & 1u, b, p);
+      if (pv) ok = ok && wait_alone(b.v_full(g), (c - 2) >> 1 & 1u, b, p) && wait_alone(b.p_ready(g), (c - 2) >> 1 & 1u, b, p);
       if (!ok) break;
       tc_fence_after_sync();
-      if (leader) {
-        const uint32_t tm = tmem + g * C::kTmemGroup, place = g * (C::kTileBytes >> 4);
-        if (pv) {
+      const uint32_t tm = tmem + g * C::kTmemGroup, place = g * (C::kTileBytes >> 4);
+      if (pv) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tm + C::kTmemO, tm + C::kTmemP + kk * 8, v_lo0 + place + kk * 128, hi, idesc_f16_f32(kRows, D, true),
-                   i > 3 || kk > 0 ? 1u : 0u);
-          umma_commit(b.v_empty(g));
-        }
-        if (qk) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
-            mma_ss(tm + C::kTmemS, q_lo + (off >> 4), k_lo0 + place + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
-          }
-          umma_commit(b.s_full(g));
-          umma_commit(b.k_empty(g));
-        }
-        if (pv && !qk) umma_commit(b.o_done(g));
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts(tm + C::kTmemO, tm + C::kTmemP + kk * 8, v_lo0 + place + kk * 128, hi, idesc_f16_f32(kRows, D, true),
+                 i > 3 || kk > 0 ? 1u : 0u);
+        umma_commit(b.v_empty(g));
       }
-      __syncwarp();
+      if (qk) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::kSlabBytes + (kk % 4) * 32;
+          mma_ss(tm + C::kTmemS, q_lo + (off >> 4), k_lo0 + place + (off >> 4), hi, idesc_f16_f32(kRows, kKeys, false), kk > 0 ? 1u : 0u);
+        }
+        umma_commit(b.s_full(g));
+        umma_commit(b.k_empty(g));
+      } else {
+        umma_commit(b.o_done(g));
+      }
     }
     c -= 2;
   }
   // Every MMA this thread issued must finish before tensor memory is released.
-  if (leader) umma_commit(b.drain());
-  __syncwarp();
+  umma_commit(b.drain());
   mbar_wait_bounded(b.drain(), 0, p.wait_limit_ns);
 }
 
@@ -886,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const DecodeParams p)
     run_turn<D>(warp - 8, smem, s_seg, b, notes, p);
   } else {
     setmaxnreg_dec<kRegsIssue>();
-    if (warp == 16) run_issue<D>(sbase, tmem, s_seg, b, p);
+    if (warp == 16 && (threadIdx.x & 31) == 0) run_issue<D>(sbase, tmem, s_seg, b, p);
     else if (warp == 17) run_load<D>(sbase, s_seg, b, notes, p);
   }
   __syncwarp();
