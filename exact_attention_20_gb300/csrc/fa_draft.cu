@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "fa_gb300_draft.h"
 #include "fa_keep.cuh"
@@ -16,11 +17,32 @@ namespace {
 namespace vf = fa::verify;
 using namespace fa_internal;
 
-// CTAs of a sequence's cluster: as many as leave each warp a tile, while all
-// sequences' CTAs fit the card at two an SM.
-int cluster_size(int n_seqs, int V, int num_sms) {
-  int c = vf::kMaxCluster;
-  while (c > 1 && (static_cast<long long>(n_seqs) * c > 2ll * num_sms || V < vf::kTile * vf::kWarps * (c - 1))) c /= 2;
+std::mutex g_mu;
+int g_cluster[kMaxDevices];  // the largest cluster of verify_kernel; 0: not asked yet
+
+// CTAs of a sequence's cluster: as many as leave each warp a tile.  (CLUSTERS)
+int cluster_size(int dev, int V) {
+  int c = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (g_cluster[dev] == 0) {
+      g_cluster[dev] = 8;
+      if (cudaFuncSetAttribute(vf::verify_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+          cudaFuncSetAttribute(vf::verify_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(vf::kMaxCluster);
+        cfg.blockDim = dim3(vf::kThreads);
+        int most[2] = {0, 0};
+        if (cudaOccupancyMaxPotentialClusterSize(&most[0], vf::verify_kernel<true>, &cfg) == cudaSuccess &&
+            cudaOccupancyMaxPotentialClusterSize(&most[1], vf::verify_kernel<false>, &cfg) == cudaSuccess &&
+            std::min(most[0], most[1]) >= vf::kMaxCluster)
+          g_cluster[dev] = vf::kMaxCluster;
+      }
+      cudaGetLastError();  // what was refused there is no error of this call
+    }
+    c = g_cluster[dev];
+  }
+  while (c > 1 && V < vf::kTile * vf::kWarps * (c - 1)) c /= 2;
   return c;
 }
 
@@ -77,7 +99,7 @@ int fa_verify_tree(const void* logits, int logits_fp32, const int* tokens, const
     p.c_hi = static_cast<float>(c);
     p.c_lo = static_cast<float>(c - static_cast<double>(p.c_hi));
   }
-  const int size = cluster_size(n_seqs, V, view.num_sms);
+  const int size = cluster_size(dev, V);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(n_seqs) * size);
   cfg.blockDim = dim3(vf::kThreads);

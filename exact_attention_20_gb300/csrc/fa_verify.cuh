@@ -19,11 +19,17 @@
 // a multiple of 2^-44; sums of those are 64-bit integers, exact, and the same
 // however the row is cut.
 //
-// Work: a node costs a pass over its row for M, one for T, and one more for each
-// drawn child that is not accepted.  CTA r of the cluster takes the r-th part of
-// the row's tiles of 256 tokens, a warp a tile at a time, a lane eight tokens,
-// and every CTA takes every decision from the same numbers.  Tiles' sums stay in
-// shared memory, so that the token is found by looking at one tile again.
+// Whether a child is accepted is one comparison, which T's error of about 2^-24
+// decides otherwise once in ten million: a node's first child is judged by a T
+// from one quick pass over the row, fp32 exponentials against running maxima,
+// which finds M, too.  Where that child is accepted nothing more is asked of the row.
+//
+// Work: a quick pass a node; where its first child is not accepted, or there is
+// none, a pass for the exact T, and one more for each drawn child that is not
+// accepted.  CTA r of the cluster takes the r-th part of the row's tiles of 256
+// tokens, a warp a tile at a time, a lane eight tokens, and every CTA takes every
+// decision from the same numbers.  Tiles' sums stay in shared memory, so that the
+// token is found by looking at one tile again.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,13 +41,14 @@
 namespace fa {
 namespace verify {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 3;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
 constexpr int kMaxTiles = kMaxVocab / kTile + 1;  // of a row that starts within a tile
-constexpr int kMaxCluster = 8;
-constexpr float kMinLog = -46.f;                  // 2^-46 is rounded to 0
+constexpr int kMaxCluster = 16;  // (more than 8 has to be asked for)
+constexpr float kMinLog = -60.f;                  // what is below is rounded to 0 as 2^-60 is
 
 // 2^(k / 128) as a sum of two floats.
 __device__ const float2 kExp2[128] = {
@@ -124,11 +131,11 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
 // ln 2.  What the polynomial leaves out is below 2^-49.
 __device__ __forceinline__ Pair weight(float x, float M, const Params& p, const float2* table) {
   const Pair d = two_sum(x, -M);
-  const float z = d.hi * p.c_hi;
-  if (!(z > kMinLog)) return Pair{0.f, 0.f};
-  const float z_lo = fmaf(d.hi, p.c_hi, -z) + fmaf(d.hi, p.c_lo, d.lo * p.c_hi);
+  // no branch, so that a lane's eight tokens overlap: what is far below is taken as 2^-60 and rounded to 0
+  const float z0 = d.hi * p.c_hi, z = fmaxf(z0, kMinLog);
+  const float z_lo = z0 > kMinLog ? fmaf(d.hi, p.c_hi, -z) + fmaf(d.hi, p.c_lo, d.lo * p.c_hi) : 0.f;
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-  const float t = __fadd_rn(z * 128.f, kRound);
+  const float t = fmaf(z, 128.f, kRound);
   const int n = __float_as_int(t) - __float_as_int(kRound);
   const float r = fmaf(__fsub_rn(t, kRound), -1.f / 128.f, z);  // exact
   constexpr float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
@@ -137,9 +144,7 @@ __device__ __forceinline__ Pair weight(float x, float M, const Params& p, const 
   const float more = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y_lo);  // 2^z / 2^(n/128) - 1 - y
   const float2 e = table[n & 127];
   const float q = e.x * y;
-  const float low = fmaf(e.x, y, -q) + fmaf(e.x, more, fmaf(e.y, y, e.y));
-  const Pair s = quick_sum(e.x, q);
-  const Pair v = quick_sum(s.hi, s.lo + low);
+  const Pair v = quick_sum(e.x, q + (fmaf(e.x, y, -q) + fmaf(e.x, more, e.y)));
   const float scale = __int_as_float((127 + (n >> 7)) << 23);
   return Pair{v.hi * scale, v.lo * scale};
 }
@@ -152,14 +157,18 @@ __device__ __forceinline__ Pair without(const Pair& a, float q, const float2& T)
   return v.hi > 0.f ? v : Pair{0.f, 0.f};  // not where it is NaN
 }
 
-// A value from 0 to 1 to a multiple of 2^-44, in those: first to 2^-22, then the rest.
-__device__ __forceinline__ long long fixed44(const Pair& a) {
+// A value from 0 to 1 to a multiple of 2^-44: first to 2^-22, in those, then the
+// rest.  256 tokens' parts can be summed in 32 bits each.
+struct Fixed {
+  int hi, lo;
+  __device__ __forceinline__ long long value() const { return (static_cast<long long>(hi) << 22) + lo; }
+};
+__device__ __forceinline__ Fixed fixed44(const Pair& a) {
   constexpr float kHi = 3.f;           // sums near it are multiples of 2^-22
   constexpr float kLo = 0x1.8p-21f;    // of 2^-44
   const float h = __fadd_rn(a.hi, kHi);
   const float rest = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(h, kHi)), a.lo);
-  const int low = __float_as_int(__fadd_rn(rest, kLo)) - __float_as_int(kLo);
-  return (static_cast<long long>(__float_as_int(h) - __float_as_int(kHi)) << 22) + low;
+  return Fixed{__float_as_int(h) - __float_as_int(kHi), __float_as_int(__fadd_rn(rest, kLo)) - __float_as_int(kLo)};
 }
 
 __device__ __forceinline__ float2 from_fixed44(long long T) {
@@ -253,29 +262,26 @@ struct Shared {
   float2 T[kMaxNodes];             // what q was multiplied with, child by child
   long long tile[kMaxTiles];       // this CTA's tiles' sums
   long long total[kMaxCluster];    // each CTA's sum
-  long long gather[2][kMaxCluster];
-  long long warp[kWarps];
+  long long gather[2][2][kMaxCluster];  // [exchange, by turns][value]
+  long long warp[2][kWarps];
   int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
   float u[kMaxNodes];
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
-// Every CTA's value to every CTA, in gather[phase]; whole CTA.  A buffer is
+// Every CTA's two values to every CTA, in gather[phase]; whole CTA.  A buffer is
 // written again after the barrier of the exchange between, which every CTA
 // enters only when it is done reading this one.
-__device__ __forceinline__ void exchange(long long v, Shared& s, int& phase, uint32_t rank, uint32_t size) {
+__device__ __forceinline__ void exchange(long long v, long long w, Shared& s, int& phase, uint32_t rank, uint32_t size) {
   phase ^= 1;
   if (size == 1) {
-    if (threadIdx.x == 0) s.gather[phase][0] = v;
+    if (threadIdx.x < 2) s.gather[phase][threadIdx.x][0] = threadIdx.x ? w : v;
     __syncthreads();
     return;
   }
-  if (threadIdx.x < size) store_to(threadIdx.x, &s.gather[phase][rank], v);
+  if (threadIdx.x < 2 * size) {
+    const uint32_t to = threadIdx.x >> 1, which = threadIdx.x & 1;
+    store_to(to, &s.gather[phase][which][rank], which ? w : v);
+  }
   cluster_sync();
 }
 
@@ -292,50 +298,107 @@ __device__ __forceinline__ float key_value(long long key) {
 }
 __device__ __forceinline__ int key_token(long long key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 
+// The quick pass: the row's maximum (as a key) and, unless greedy, the sum of
+// its weights to about 2^-24, in 2^-44.
 template <bool FP32>
-__device__ __forceinline__ long long row_max(const Row<FP32>& row, Shared& s, int& phase, uint32_t rank, uint32_t size) {
+__device__ __forceinline__ long long row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
+                                               uint32_t size, long long& T) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float best = -INFINITY;
+  constexpr int kAtOnce = 2;  // tiles whose loads are in flight together
+  float best = -INFINITY, sum = 0.f;  // the sum against `best`
   int where = 0x7fffffff;
-  for (int t = row.begin + warp; t < row.end; t += kWarps) {
-    float v[8];
-    const int x = row.first(t);
-    row.load(x, v);
+#pragma unroll 1
+  for (int t = row.begin + warp; t < row.end; t += kAtOnce * kWarps) {
+    float v[kAtOnce][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (v[i] > best) best = v[i], where = x + i;  // ascending tokens: the first of equals stays
+    for (int n = 0; n < kAtOnce; ++n) {
+      if (t + n * kWarps < row.end) {
+        row.load(row.first(t + n * kWarps), v[n]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[n][i] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      float top = fmax3(v[n][0], v[n][1], v[n][2]);
+      top = fmax3(top, v[n][3], v[n][4]);
+      top = fmax3(top, v[n][5], v[n][6]);
+      top = fmaxf(top, v[n][7]);
+      if (top > best) {  // ascending tokens: the first of equals stays
+        sum *= ex2_approx((best - top) * p.c_hi);
+        best = top;
+        const int x = row.first(t + n * kWarps);
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+          if (v[n][i] == top) where = x + i;
+      }
+      if (!p.greedy) {
+        const float shift = best == -INFINITY ? 0.f : best;
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          a += ex2_approx((v[n][i] - shift) * p.c_hi);
+          b += ex2_approx((v[n][i + 1] - shift) * p.c_hi);
+        }
+        sum += a + b;
+      }
+    }
   }
+  // the warp's, the CTA's, the cluster's
+  auto join = [&](long long key, float S, long long other, float So, long long& k, float& out) {
+    const float a = key_value(key), b = key_value(other), m = fmaxf(a, b);
+    const float base = m == -INFINITY ? 0.f : m;
+    out = S * ex2_approx((a - base) * p.c_hi) + So * ex2_approx((b - base) * p.c_hi);
+    k = max(key, other);
+  };
   long long key = max_key(best, where);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
-  if (lane == 0) s.warp[warp] = key;
+  for (int off = 16; off > 0; off >>= 1) {
+    const long long other = __shfl_xor_sync(0xffffffffu, key, off);
+    const float So = __shfl_xor_sync(0xffffffffu, sum, off);
+    // in the lanes' order, so that both sides have the same sum
+    if (lane & off) join(other, So, key, sum, key, sum);
+    else join(key, sum, other, So, key, sum);
+  }
+  if (lane == 0) s.warp[0][warp] = key, s.warp[1][warp] = __float_as_uint(sum);
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) key = max(key, s.warp[w]);
-  exchange(key, s, phase, rank, size);
-  for (uint32_t r = 0; r < size; ++r) key = max(key, s.gather[phase][r]);
+  key = s.warp[0][0], sum = __uint_as_float(static_cast<uint32_t>(s.warp[1][0]));
+#pragma unroll 1
+  for (int w = 1; w < kWarps; ++w) join(key, sum, s.warp[0][w], __uint_as_float(static_cast<uint32_t>(s.warp[1][w])), key, sum);
+  exchange(key, __float_as_uint(sum), s, phase, rank, size);
+  key = s.gather[phase][0][0], sum = __uint_as_float(static_cast<uint32_t>(s.gather[phase][1][0]));
+#pragma unroll 1
+  for (uint32_t r = 1; r < size; ++r)
+    join(key, sum, s.gather[phase][0][r], __uint_as_float(static_cast<uint32_t>(s.gather[phase][1][r])), key, sum);
+  T = __float2ll_rn(sum * 0x1p44f);
   return key;
 }
 
 // What is left of the weights of tokens x .. x + 7 after m drawn children.
 template <bool FP32>
 __device__ __forceinline__ void left8(const Row<FP32>& row, int x, float M, int m, int gone, const Params& p, const Shared& s,
-                                      long long* out) {
+                                      Fixed* out) {
   float v[8], q[8];
   row.load(x, v);
   if (m > 0) row.load_draft(x, q);
+  Pair a[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    Pair a = weight(v[i], M, p, s.table);
-    if (m > 0)
-      for (int n = 0; n < m; ++n) a = without(a, q[i], s.T[n]);
-    out[i] = fixed44(a);
+  for (int i = 0; i < 8; ++i) a[i] = weight(v[i], M, p, s.table);
+#pragma unroll 1
+  for (int n = 0; n < m; ++n) {
+    const float2 T = s.T[n];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = without(a[i], q[i], T);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = fixed44(a[i]);
+#pragma unroll 1
   for (int n = 0; n < gone; ++n) {
     const int i = s.gone[n] - x;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (i == e) out[e] = 0;
+      if (i == e) out[e] = Fixed{0, 0};
   }
 }
 
@@ -346,23 +409,25 @@ __device__ __forceinline__ long long row_sum(const Row<FP32>& row, float M, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long mine = 0;
   for (int t = row.begin + warp; t < row.end; t += kWarps) {
-    long long w[8], sum = 0;
+    Fixed w[8], part{0, 0};
     left8(row, row.first(t), M, m, 0, p, s, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += w[i];
-    sum = warp_sum(sum);
+    for (int i = 0; i < 8; ++i) part.hi += w[i].hi, part.lo += w[i].lo;
+    part.hi = __reduce_add_sync(0xffffffffu, part.hi);
+    part.lo = __reduce_add_sync(0xffffffffu, part.lo);
+    const long long sum = part.value();
     if (lane == 0) s.tile[t - row.begin] = sum;
     mine += sum;
   }
-  if (lane == 0) s.warp[warp] = mine;
+  if (lane == 0) s.warp[0][warp] = mine;
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s.warp[w];
-  exchange(total, s, phase, rank, size);
-  if (threadIdx.x < size) s.total[threadIdx.x] = s.gather[phase][threadIdx.x];
+  for (int w = 0; w < kWarps; ++w) total += s.warp[0][w];
+  exchange(total, 0, s, phase, rank, size);
+  if (threadIdx.x < size) s.total[threadIdx.x] = s.gather[phase][0][threadIdx.x];
   total = 0;
-  for (uint32_t r = 0; r < size; ++r) total += s.gather[phase][r];
+  for (uint32_t r = 0; r < size; ++r) total += s.gather[phase][0][r];
   __syncthreads();
   return total;
 }
@@ -394,16 +459,17 @@ __device__ __forceinline__ void find_token(const Row<FP32>& row, long long targe
     }
     const int l = __ffs(past) - 1;
     before = __shfl_sync(0xffffffffu, c - v, l);
-    long long w[8], sum = 0;
+    Fixed w[8];
+    long long sum = 0;
     const int x = row.first(t0 + l);
     left8(row, x, M, m, gone, p, s, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += w[i];
+    for (int i = 0; i < 8; ++i) sum += w[i].value();
     long long at = before + scan(sum) - sum;
     int found = -1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      at += w[i];
+      at += w[i].value();
       if (found < 0 && at > target) found = x + i;
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, found >= 0);
@@ -413,7 +479,7 @@ __device__ __forceinline__ void find_token(const Row<FP32>& row, long long targe
 }
 
 template <bool FP32>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Params p) {
   __shared__ Shared s;
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const long long seq = blockIdx.x / size, node0 = seq * p.n_nodes;
@@ -433,7 +499,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
     if (writer) p.path[node0 + kept] = cur;
     ++kept;
     const Row<FP32> row(p, node0 + cur, rank, size);
-    const long long top = row_max(row, s, phase, rank, size);
+    long long T;
+    const long long top = row_quick(row, p, s, phase, rank, size, T);
     const float M = key_value(top);
     int accepted = -1;
     if (M == -INFINITY) break;
@@ -445,8 +512,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
       continue;
     }
     int m = 0, gone = 0;
-    bool stale = false;  // the sums in shared memory are not those of m
-    long long T = row_sum(row, M, 0, p, s, phase, rank, size);
+    bool exact = false;  // T and the sums in shared memory are
+    bool stale = false;  // ... but not those of m
+    bool first = true;
     for (int j = cur + 1; j < p.n_nodes; ++j) {
       const int x = s.tokens[j];
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
@@ -462,19 +530,27 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
           accepted = j;
           break;
         }
+        if (first) {  // not accepted: from here on T is the exact one
+          first = false;
+          T = row_sum(row, M, 0, p, s, phase, rank, size), exact = true;
+        }
         __syncthreads();
-        if (threadIdx.x == 0) s.T[m] = t;
+        if (threadIdx.x == 0) s.T[m] = from_fixed44(T);
         __syncthreads();
         const long long left = row_sum(row, M, m + 1, p, s, phase, rank, size);
         stale = left <= 0;
         if (!stale) T = left, ++m;
       } else {
-        long long w = fixed44(a);
+        long long w = fixed44(a).value();
         for (int n = 0; n < gone; ++n)
           if (s.gone[n] == x) w = 0;
         if (static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T))) < w) {
           accepted = j;
           break;
+        }
+        if (first) {
+          first = false;
+          T = row_sum(row, M, 0, p, s, phase, rank, size), exact = true;
         }
         if (w == 0 || T - w <= 0) continue;
         T -= w;
@@ -490,6 +566,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p) {
       }
     }
     if (accepted < 0) {
+      if (!exact) T = row_sum(row, M, 0, p, s, phase, rank, size);
       if (stale) row_sum(row, M, m, p, s, phase, rank, size);
       const long long target = static_cast<long long>(__umul64hi(fraction64(s.u[0]), static_cast<unsigned long long>(T)));
       find_token(row, target, M, m, gone, p, s, rank, p.next_token + seq);
