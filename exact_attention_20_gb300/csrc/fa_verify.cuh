@@ -41,8 +41,8 @@
 namespace fa {
 namespace verify {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 3;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 5;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step

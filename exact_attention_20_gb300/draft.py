@@ -17,6 +17,7 @@ import math
 import torch
 
 from . import fa
+from .fa import FA_OK, FAError
 from .serve import BAD_PAGE, BAD_POSITION, _Cache, _check, _check_tokens, _checked, _Target  # noqa: F401
 
 _P = ctypes.c_void_p
@@ -53,9 +54,10 @@ def lib() -> ctypes.CDLL:
 
 def _nodes(name, t, n, device) -> int:
     """Checks an int32 [sequences, nodes] tensor; returns the number of nodes."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError(f"{name} must be an int32 tensor [sequences, nodes]")
-    nodes = t.shape[1]
+    nodes = shape[1]
     if not 1 <= nodes <= MAX_NODES:
         raise ValueError(f"a tree has 1 to {MAX_NODES} places for nodes, got {nodes}")
     _check(name, t, torch.int32, (n, nodes), device)
@@ -91,12 +93,15 @@ def _tree_attention(q, cache, page_table, seq_lens, parents, o, lse, scale, k_sc
             lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
         need = _attention_workspace(dev.index, c.n, nodes, Hq, c.heads, d, c.max_pages, c.page_size)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _checked(lib().fa_kv4_tree_attention(
+        rc = lib().fa_kv4_tree_attention(
             q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(), o.data_ptr(),
             lse.data_ptr(), c.n, nodes, Hq, c.heads, d, c.max_pages, c.pages, c.page_size, stride,
             1.0 / math.sqrt(d) if scale is None else scale, k_scale, v_scale, c.errors, None if ws is None else ws.data_ptr(),
-            need, handle))
-    target.uses(q, parents, *c.tensors)
+            need, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    if target.other is not None:
+        target.uses(q, parents, *c.tensors)
     return target, o, lse
 
 
@@ -130,19 +135,21 @@ def kv4_tree_attention(q, cache, page_table, seq_lens, parents, scale: float | N
 # ---------------------------------------------------------------------------
 def _rows(name, t, dtypes, n, nodes, V, device):
     """Checks [n, nodes, V] or [n * nodes, V] rows of contiguous elements, evenly spaced; (V, row stride)."""
-    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if len(shape) not in (2, 3):
         raise ValueError(f"{name} must be [sequences, nodes, V] or [sequences * nodes, V]")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    V = t.shape[-1] if V is None else V
-    if t.shape != ((n, nodes, V) if t.dim() == 3 else (n * nodes, V)):
-        raise ValueError(f"{name} must have rows of {V} for {n} x {nodes} nodes, got {tuple(t.shape)}")
-    if t.device != device:
+    V = shape[-1] if V is None else V
+    if shape != ((n, nodes, V) if len(shape) == 3 else (n * nodes, V)):
+        raise ValueError(f"{name} must have rows of {V} for {n} x {nodes} nodes, got {tuple(shape)}")
+    if t.get_device() != device.index and t.device != device:  # (a CPU tensor's are -1 and None)
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    stride = t.stride(-2) if nodes > 1 or t.dim() == 2 else t.stride(0)
-    if V > 1 and t.stride(-1) != 1 or t.dim() == 3 and n > 1 and t.stride(0) != nodes * stride:
+    s = t.stride()
+    row = s[-2] if nodes > 1 or len(s) == 2 else s[0]
+    if V > 1 and s[-1] != 1 or len(s) == 3 and n > 1 and s[0] != nodes * row:
         raise ValueError(f"{name} must have contiguous rows, evenly spaced")
-    return V, stride if n * nodes > 1 else V
+    return V, row if n * nodes > 1 else V
 
 
 def _verify(logits, tokens, parents, uniforms, draft_probs, path, n_kept, next_token, temperature, stream):
@@ -169,11 +176,14 @@ def _verify(logits, tokens, parents, uniforms, draft_probs, path, n_kept, next_t
             path = torch.empty((n, nodes), dtype=torch.int32, device=dev)
             n_kept = torch.empty(n, dtype=torch.int32, device=dev)
             next_token = torch.empty(n, dtype=torch.int32, device=dev)
-        _checked(lib().fa_verify_tree(
+        rc = lib().fa_verify_tree(
             logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0, tokens.data_ptr(), parents.data_ptr(),
             uniforms.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), path.data_ptr(), n_kept.data_ptr(),
-            next_token.data_ptr(), n, nodes, V, stride, draft_stride, temperature, handle))
-    target.uses(logits, tokens, parents, uniforms, *(() if draft_probs is None else (draft_probs,)))
+            next_token.data_ptr(), n, nodes, V, stride, draft_stride, temperature, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    if target.other is not None:
+        target.uses(*(t for t in (logits, tokens, parents, uniforms, draft_probs) if t is not None))
     return target, path, n_kept, next_token
 
 
@@ -218,10 +228,13 @@ def _keep(cache, page_table, seq_lens, path, n_kept, new_lens, d, errors, stream
     with target as handle:
         if new_lens is None:
             new_lens = torch.empty(c.n, dtype=torch.int32, device=dev)
-        _checked(lib().fa_kv4_keep(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), path.data_ptr(),
-                                   n_kept.data_ptr(), new_lens.data_ptr(), c.n, nodes, c.max_pages, c.pages, c.page_size,
-                                   c.heads, d, c.errors, handle))
-    target.uses(path, n_kept, *c.tensors)
+        rc = lib().fa_kv4_keep(cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), path.data_ptr(),
+                               n_kept.data_ptr(), new_lens.data_ptr(), c.n, nodes, c.max_pages, c.pages, c.page_size,
+                               c.heads, d, c.errors, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    if target.other is not None:
+        target.uses(path, n_kept, *c.tensors)
     return target, new_lens
 
 

@@ -16,7 +16,8 @@ from typing import NamedTuple
 import torch
 
 from . import fa, serve
-from .serve import _checked, _Cache, _check, _check_tokens, _Target
+from .fa import FA_OK, FAError
+from .serve import _Cache, _check, _check_tokens, _Target
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -113,10 +114,13 @@ def _rope(r, d, device) -> int:
     """Checks a Rope; returns rot_dim."""
     if not isinstance(r, Rope):
         raise TypeError("rope must be a Rope")
-    _check("rope.turns", r.turns, torch.int64, r.turns.shape if isinstance(r.turns, torch.Tensor) else (), device)
-    if r.turns.dim() != 1 or r.turns.numel() % 8 or not 16 <= 2 * r.turns.numel() <= d:
-        raise ValueError(f"rope must turn a multiple of 16 elements, at most {d}")
-    return 2 * r.turns.numel()
+    t = r.turns
+    if isinstance(t, torch.Tensor) and t.dim() == 1:
+        rot = 2 * t.shape[0]
+        if rot % 16 == 0 and 16 <= rot <= d:
+            _check("rope.turns", t, torch.int64, t.shape, device)
+            return rot
+    raise ValueError(f"rope.turns must be int64 [rot_dim / 2] for a multiple of 16 elements, at most {d}")
 
 
 def _strides(name, x, shape, device):
@@ -127,49 +131,65 @@ def _strides(name, x, shape, device):
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.device != device:
+    if x.get_device() != device.index and x.device != device:  # (a CPU tensor's are -1 and None)
         raise ValueError(f"{name} must be on {device}, got {x.device}")
-    if x.numel() and x.stride(-1) != 1:
-        raise ValueError(f"{name} must have a head's elements contiguous")
     s = x.stride()
-    return (s[0], s[2], s[1]) if x.dim() == 4 else (0, s[0], s[1])
+    if s[-1] != 1 and x.numel():
+        raise ValueError(f"{name} must have a head's elements contiguous")
+    return (s[0], s[2], s[1]) if len(s) == 4 else (0, s[0], s[1])
+
+
+_Strides = _L * 12
 
 
 def _rotate(q, k, q_out, k_out, r, positions, backward, stream):
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
-        raise ValueError("q must be [B, H, N, d] or [T, H, d]")
-    dev, shape, d = q.device, q.shape, q.shape[-1]
-    B, N = (shape[0], shape[2]) if q.dim() == 4 else (1, shape[0])
-    rot = _rope(r, d, dev)
-    strides = list(_strides("q", q, shape, dev))
-    kshape = None
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
-            raise ValueError("k must have as many dimensions as q")
-        kshape = (B, k.shape[1], N, d) if q.dim() == 4 else (N, k.shape[1], d)
-        strides += _strides("k", k, kshape, dev)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev, shape = q.device, q.shape
+    if len(shape) == 4:
+        B, hq, N, d = shape
+    elif len(shape) == 3:
+        B, (N, hq, d) = 1, shape
     else:
+        raise ValueError("q must be [B, H, N, d] or [T, H, d]")
+    dense = len(shape) == 4
+    rot = _rope(r, d, dev)
+    strides = _strides("q", q, shape, dev)
+    hk = 0
+    if k is None:
         strides += (0, 0, 0)
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != len(shape):
+            raise ValueError("k must have as many dimensions as q")
+        hk = k.shape[1]
+        kshape = (B, hk, N, d) if dense else (N, hk, d)
+        strides += _strides("k", k, kshape, dev)
     position_stride = 0
     if positions is not None:
         # one row for every batch entry, or a row each
-        each = q.dim() == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 2
-        _check("positions", positions, torch.int32, (B, N) if each else (N,), dev)
-        position_stride = N if each else 0
+        if dense and isinstance(positions, torch.Tensor) and positions.dim() == 2:
+            _check("positions", positions, torch.int32, (B, N), dev)
+            position_stride = N
+        else:
+            _check("positions", positions, torch.int32, (N,), dev)
     if q_out is not None:
-        outs = _strides("q_out", q_out, shape, dev) + (_strides("k_out", k_out, kshape, dev) if k is not None else (0, 0, 0))
+        strides += _strides("q_out", q_out, shape, dev)
+        strides += _strides("k_out", k_out, kshape, dev) if k is not None else (0, 0, 0)
+    else:
+        strides += (hq * N * d, d, N * d, hk * N * d, d, N * d) if dense else (0, hq * d, d, 0, hk * d, d)
     target = _Target(dev, stream)
     with target as handle:
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            k_out = torch.empty(kshape, dtype=torch.bfloat16, device=dev) if k is not None else None
-            outs = _strides("q_out", q_out, shape, dev) + (_strides("k_out", k_out, kshape, dev) if k is not None else (0, 0, 0))
-        _checked(lib().fa_rotate(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                                 None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
-                                 r.turns.data_ptr(), B, N, shape[1], 0 if k is None else kshape[1], d, rot,
-                                 1 if r.interleaved else 0, r.magnitude, backward, (_L * 12)(*strides, *outs),
-                                 position_stride, handle))
-    target.uses(q, r.turns, *(() if k is None else (k,)), *(() if positions is None else (positions,)))
+            if k is not None:
+                k_out = torch.empty(kshape, dtype=torch.bfloat16, device=dev)
+        rc = lib().fa_rotate(q.data_ptr(), k.data_ptr() if hk else None, q_out.data_ptr(), k_out.data_ptr() if hk else None,
+                             None if positions is None else positions.data_ptr(), r.turns.data_ptr(), B, N, hq, hk, d, rot,
+                             1 if r.interleaved else 0, r.magnitude, backward, _Strides(*strides), position_stride, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    if target.other is not None:
+        target.uses(*(t for t in (q, k, positions, r.turns) if t is not None))
     return target, q_out, k_out
 
 
@@ -189,9 +209,7 @@ def fa_rotate(q, k, q_out, k_out, rope: Rope, positions=None, backward: bool = F
 
 
 def _gives(target, q, k):
-    if k is None:
-        return target.gives(q)[0]
-    return target.gives(q, k)
+    return target.gives(q, k) if k is not None else target.gives(q)[0]
 
 
 def rotate(q, k, rope: Rope, positions=None, stream=None):
@@ -232,14 +250,16 @@ def _append(cache, q, k, v, r, page_table, seq_lens, cu_seqlens, q_out, k_out, w
             q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
         if want_k and k_out is None:
             k_out = torch.empty((T, c.heads, d), dtype=torch.bfloat16, device=dev)
-        _checked(lib().fa_kv4_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
-                                     cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
-                                     None if positions is None else positions.data_ptr(), r.turns.data_ptr(), T, c.n,
-                                     c.max_pages, c.pages, c.page_size, hq, c.heads, d, rot, 1 if r.interleaved else 0,
-                                     r.magnitude, qs, ks, vs, k_scale, v_scale, c.errors, handle))
-    target.uses(k, v, cu_seqlens, r.turns, *c.tensors, *(() if q is None else (q,)),
-                *(() if positions is None else (positions,)))
+        rc = lib().fa_kv4_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                 None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+                                 cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+                                 None if positions is None else positions.data_ptr(), r.turns.data_ptr(), T, c.n,
+                                 c.max_pages, c.pages, c.page_size, hq, c.heads, d, rot, 1 if r.interleaved else 0,
+                                 r.magnitude, qs, ks, vs, k_scale, v_scale, c.errors, handle)
+        if rc != FA_OK:
+            raise FAError(rc)
+    if target.other is not None:
+        target.uses(k, v, cu_seqlens, r.turns, *c.tensors, *(t for t in (q, positions) if t is not None))
     return target, q_out, k_out
 
 
@@ -268,5 +288,6 @@ def kv4_append(cache, q, k, v, rope: Rope, page_table, seq_lens, cu_seqlens, pos
     """
     target, q_out, k_out = _append(cache, q, k, v, rope, page_table, seq_lens, cu_seqlens, None, None, return_k, positions,
                                    k_scale, v_scale, errors, stream)
-    target.gives(*(t for t in (q_out, k_out) if t is not None))
+    if target.other is not None:
+        target.gives(*(t for t in (q_out, k_out) if t is not None))
     return (q_out, k_out) if return_k else q_out
