@@ -174,10 +174,35 @@ struct RotateParams {
 
 constexpr int kMaxTokens = 16;  // of a CTA
 
+// cos and sin of eight pairs, to turn sixteen elements x, y.
+struct Eight {
+  float c[8], s[8];
+  // HALVES: pair i is element i of x and of y; else elements 2i and 2i + 1 of the two together
+  template <bool HALVES>
+  __device__ __forceinline__ void turn(uint4& x, uint4& y) const {
+    uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float a0 = bf16_lo(a[n]), a1 = bf16_hi(a[n]), b0 = bf16_lo(b[n]), b1 = bf16_hi(b[n]);
+      if constexpr (HALVES) {
+        a[n] = pack_bf16x2(turned(a0, -b0, c[2 * n], s[2 * n]), turned(a1, -b1, c[2 * n + 1], s[2 * n + 1]));
+        b[n] = pack_bf16x2(turned(b0, a0, c[2 * n], s[2 * n]), turned(b1, a1, c[2 * n + 1], s[2 * n + 1]));
+      } else {
+        a[n] = pack_bf16x2(turned(a0, -a1, c[n], s[n]), turned(a1, a0, c[n], s[n]));
+        b[n] = pack_bf16x2(turned(b0, -b1, c[4 + n], s[4 + n]), turned(b1, b0, c[4 + n], s[4 + n]));
+      }
+    }
+    x = make_uint4(a[0], a[1], a[2], a[3]), y = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+};
+
+constexpr int kAhead = 4;  // heads whose loads are in flight together
+
 // Block (x, b): tokens_per_cta tokens of batch entry b, all heads.  cos and sin
-// of the tokens' pairs go to shared memory first, once for all heads; then a
-// thread takes 16 elements at a time, eight pairs, with two 16-byte loads and
-// stores (of neighbouring elements if interleaved, else rot / 2 apart).
+// of the tokens' pairs go to shared memory once; then a thread has the eight
+// pairs of one token to itself and goes through the heads with them in registers,
+// two 16-byte loads and stores each (of neighbouring elements if interleaved,
+// else rot / 2 apart), four heads' loads in flight.  Bound by the bytes: FIGURES
 template <int D>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
   __shared__ float2 s_cs[kMaxTokens * (D / 2)];
@@ -192,45 +217,47 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
   }
   __syncthreads();
   constexpr int kUnits = D / 16;  // of a head
-  const int rotating = p.rot / 16, used = p.copy_rest ? kUnits : rotating;
-  const int units = count * p.H * kUnits;
-  for (int i = threadIdx.x; i < units; i += kThreads) {
-    const int u = i % kUnits, row = i / kUnits;
-    if (u >= used) continue;
-    const int outer = row / (p.heads_outer ? count : p.H), inner = row - outer * (p.heads_outer ? count : p.H);
-    const int t = p.heads_outer ? inner : outer, head = p.heads_outer ? outer : inner;
-    const bool is_k = head >= p.Hq;
-    const View& v = is_k ? p.k : p.q;
-    const int h = is_k ? head - p.Hq : head;
-    const __nv_bfloat16* src = v.src + b * v.src_batch + (first + t) * v.src_token + h * v.src_head;
-    __nv_bfloat16* dst = v.dst + b * v.dst_batch + (first + t) * v.dst_token + h * v.dst_head;
-    const bool halves = u < rotating && !p.interleaved;
-    const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? e0 + pairs : e0 + 8;
-    uint4 x = *reinterpret_cast<const uint4*>(src + e0), y = *reinterpret_cast<const uint4*>(src + e1);
-    if (u < rotating) {
-      const float2* cs = s_cs + t * (D / 2) + 8 * u;
-      uint32_t a[4] = {x.x, x.y, x.z, x.w}, c[4] = {y.x, y.y, y.z, y.w};
-      if (halves) {
+  const int places = p.tokens_per_cta * kUnits;  // a power of two up to kThreads
+  const int place = threadIdx.x & (places - 1), group = threadIdx.x / places, groups = kThreads / places;
+  const int t = place / kUnits, u = place % kUnits;
+  const int rotating = p.rot / 16;
+  if (t >= count || (u >= rotating && !p.copy_rest)) return;
+  Eight cs;
+  if (u < rotating) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float2 f = cs[2 * n], g = cs[2 * n + 1];
-          const float a0 = bf16_lo(a[n]), a1 = bf16_hi(a[n]), c0 = bf16_lo(c[n]), c1 = bf16_hi(c[n]);
-          a[n] = pack_bf16x2(turned(a0, -c0, f.x, f.y), turned(a1, -c1, g.x, g.y));
-          c[n] = pack_bf16x2(turned(c0, a0, f.x, f.y), turned(c1, a1, g.x, g.y));
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float2 f = cs[n], g = cs[4 + n];
-          const float a0 = bf16_lo(a[n]), a1 = bf16_hi(a[n]), c0 = bf16_lo(c[n]), c1 = bf16_hi(c[n]);
-          a[n] = pack_bf16x2(turned(a0, -a1, f.x, f.y), turned(a1, a0, f.x, f.y));
-          c[n] = pack_bf16x2(turned(c0, -c1, g.x, g.y), turned(c1, c0, g.x, g.y));
-        }
-      }
-      x = make_uint4(a[0], a[1], a[2], a[3]), y = make_uint4(c[0], c[1], c[2], c[3]);
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = s_cs[t * (D / 2) + 8 * u + i];
+      cs.c[i] = f.x, cs.s[i] = f.y;
     }
-    *reinterpret_cast<uint4*>(dst + e0) = x;
-    *reinterpret_cast<uint4*>(dst + e1) = y;
+  }
+  const bool halves = u < rotating && !p.interleaved;
+  const int e0 = halves ? 8 * u : 16 * u, apart = halves ? pairs : 8;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const View& v = which ? p.k : p.q;
+    const int heads = which ? p.H - p.Hq : p.Hq;
+    const __nv_bfloat16* src = v.src + b * v.src_batch + (first + t) * v.src_token + e0;
+    __nv_bfloat16* dst = v.dst + b * v.dst_batch + (first + t) * v.dst_token + e0;
+#pragma unroll 1
+    for (int h = group; h < heads; h += kAhead * groups) {
+      uint4 x[kAhead], y[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        if (h + n * groups >= heads) break;
+        const __nv_bfloat16* at = src + (h + n * groups) * v.src_head;
+        x[n] = *reinterpret_cast<const uint4*>(at);
+        y[n] = *reinterpret_cast<const uint4*>(at + apart);
+      }
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        if (h + n * groups >= heads) break;
+        if (halves) cs.turn<true>(x[n], y[n]);
+        else if (u < rotating) cs.turn<false>(x[n], y[n]);
+        __nv_bfloat16* at = dst + (h + n * groups) * v.dst_head;
+        *reinterpret_cast<uint4*>(at) = x[n];
+        *reinterpret_cast<uint4*>(at + apart) = y[n];
+      }
+    }
   }
 }
 
@@ -249,12 +276,12 @@ struct AppendParams {
   float scale;              // of cos and sin
 };
 
-// A turn's cos and sin in shared memory.  Lanes that read pairs 16 apart, one
-// block each, find them in other banks.
+// A turn's cos and sin in shared memory.  Lanes that read pairs 8 or 16 apart find
+// them in other banks.
 template <int D>
 struct TurnTable {
-  static constexpr int kRow = D / 2 + D / 32;
-  __device__ static __forceinline__ int at(int t, int pair) { return t * kRow + pair + (pair >> 4); }
+  static constexpr int kRow = D / 2 + D / 16;
+  __device__ static __forceinline__ int at(int t, int pair) { return t * kRow + pair + (pair >> 3); }
 };
 
 // Elements 8 e .. 8 e + 7 of a head's row `src`, turned, as fp32 values with bf16's bits.
@@ -294,8 +321,7 @@ __device__ __forceinline__ void turned_vector(const __nv_bfloat16* src, int e, c
 }
 
 // As storing (kv4::store_kernel), with the keys' blocks turned first, and q
-// turned as by rotate_kernel beside them: a thread takes one block of 16
-// elements of a key, of a value, or of q.
+// turned as by rotate_kernel before them.
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
   using kv4::kBlock;
@@ -327,45 +353,53 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     s_turn[TurnTable<D>::at(t, pair)] = make_float4(turn.c.hi, turn.c.lo, turn.s.hi, turn.s.lo);
   }
   __syncthreads();
-  const int kv_units = 2 * m.Hkv * count * kBlocks;             // [tensor][head][token][block]
-  const int units = kv_units + p.Hq * count * kBlocks;          // then q: [head][token][block]
+  // q: as in rotate_kernel
+  if (p.Hq > 0) {
+    const int places = m.tokens_per_cta * kBlocks;
+    const int place = threadIdx.x & (places - 1), group = threadIdx.x / places, groups = kThreads / places;
+    const int i = place / kBlocks, u = place % kBlocks;
+    if (i < count && s_place[i] != -1) {
+      const bool turning = 16 * u < p.rot, halves = turning && !p.interleaved;
+      Eight cs;
+      if (turning) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float4 f = s_turn[TurnTable<D>::at(i, 8 * u + n)];
+          cs.c[n] = f.x, cs.s[n] = f.z;
+        }
+      }
+      const int e0 = halves ? 8 * u : 16 * u, apart = halves ? pairs : 8;
+      const long long tok = first + i;
+      const __nv_bfloat16* src = p.q + tok * p.q_stride + e0;
+      __nv_bfloat16* dst = p.q_out + tok * p.Hq * D + e0;
+#pragma unroll 1
+      for (int h = group; h < p.Hq; h += kAhead * groups) {
+        uint4 x[kAhead], y[kAhead];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+          if (h + n * groups >= p.Hq) break;
+          x[n] = __ldg(reinterpret_cast<const uint4*>(src + (h + n * groups) * D));
+          y[n] = __ldg(reinterpret_cast<const uint4*>(src + (h + n * groups) * D + apart));
+        }
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+          if (h + n * groups >= p.Hq) break;
+          if (halves) cs.turn<true>(x[n], y[n]);
+          else if (turning) cs.turn<false>(x[n], y[n]);
+          *reinterpret_cast<uint4*>(dst + (h + n * groups) * D) = x[n];
+          *reinterpret_cast<uint4*>(dst + (h + n * groups) * D + apart) = y[n];
+        }
+      }
+    }
+  }
+  const int units = 2 * m.Hkv * count * kBlocks;  // [tensor][head][token][block]
   const int head_bytes = kv4::row_bytes(D) << m.page_shift;
   for (int u = threadIdx.x; u < units; u += kThreads) {
-    const bool is_q = u >= kv_units;
-    const int x = is_q ? u - kv_units : u;
-    const int block = x % kBlocks, rest = x / kBlocks;
+    const int block = u % kBlocks, rest = u / kBlocks;
     const int i = rest % count, hv = rest / count;
     const long long place = s_place[i];
     if (place == -1) continue;  // of no sequence
     const long long tok = first + i;
-    if (is_q) {
-      // eight pairs, as in rotate_kernel
-      const __nv_bfloat16* src = p.q + tok * p.q_stride + static_cast<long long>(hv) * D;
-      __nv_bfloat16* dst = p.q_out + (tok * p.Hq + hv) * D;
-      const bool turning = 16 * block < p.rot, halves = turning && !p.interleaved;
-      const int e0 = halves ? 8 * block : 16 * block, e1 = halves ? e0 + pairs : e0 + 8;
-      uint4 v = __ldg(reinterpret_cast<const uint4*>(src + e0)), w = __ldg(reinterpret_cast<const uint4*>(src + e1));
-      if (turning) {
-        uint32_t a[4] = {v.x, v.y, v.z, v.w}, c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float4 f = s_turn[TurnTable<D>::at(i, 8 * block + (halves ? 2 * n : n))];
-          const float4 g = s_turn[TurnTable<D>::at(i, 8 * block + (halves ? 2 * n + 1 : 4 + n))];
-          const float a0 = bf16_lo(a[n]), a1 = bf16_hi(a[n]), c0 = bf16_lo(c[n]), c1 = bf16_hi(c[n]);
-          if (halves) {
-            a[n] = pack_bf16x2(turned(a0, -c0, f.x, f.z), turned(a1, -c1, g.x, g.z));
-            c[n] = pack_bf16x2(turned(c0, a0, f.x, f.z), turned(c1, a1, g.x, g.z));
-          } else {
-            a[n] = pack_bf16x2(turned(a0, -a1, f.x, f.z), turned(a1, a0, f.x, f.z));
-            c[n] = pack_bf16x2(turned(c0, -c1, g.x, g.z), turned(c1, c0, g.x, g.z));
-          }
-        }
-        v = make_uint4(a[0], a[1], a[2], a[3]), w = make_uint4(c[0], c[1], c[2], c[3]);
-      }
-      *reinterpret_cast<uint4*>(dst + e0) = v;
-      *reinterpret_cast<uint4*>(dst + e1) = w;
-      continue;
-    }
     const int is_v = hv >= m.Hkv;
     const int h = is_v ? hv - m.Hkv : hv;
     uint32_t w[8];
