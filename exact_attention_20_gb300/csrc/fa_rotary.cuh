@@ -284,46 +284,67 @@ struct TurnTable {
   __device__ static __forceinline__ int at(int t, int pair) { return t * kRow + pair + (pair >> 3); }
 };
 
-// Elements 8 e .. 8 e + 7 of a head's row `src`, turned, as fp32 values with bf16's bits.
-template <int D>
-__device__ __forceinline__ void turned_vector(const __nv_bfloat16* src, int e, const AppendParams& p, const float4* s_turn,
-                                              int t, float* out) {
-  const int e0 = 8 * e, half = p.rot / 2;
-  const uint4 x4 = __ldg(reinterpret_cast<const uint4*>(src + e0));
-  const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-  if (e0 >= p.rot) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) out[2 * n] = bf16_lo(x[n]), out[2 * n + 1] = bf16_hi(x[n]);
-    return;
-  }
-  if (p.interleaved) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float4 f = s_turn[TurnTable<D>::at(t, e0 / 2 + n)];
-      const Float2 c{f.x, f.y}, s{f.z, f.w};
-      const float a = bf16_lo(x[n]), b = bf16_hi(x[n]);
-      out[2 * n] = turned(a, b, c, s, -1.f);
-      out[2 * n + 1] = turned(b, a, c, s, 1.f);
-    }
-    return;
-  }
-  const bool upper = e0 >= half;
-  const int pair = upper ? e0 - half : e0;
-  const uint4 y4 = __ldg(reinterpret_cast<const uint4*>(src + (upper ? e0 - half : e0 + half)));
-  const uint32_t y[4] = {y4.x, y4.y, y4.z, y4.w};
-  const float sign = upper ? 1.f : -1.f;
+// Eight elements of a row, w, turned, as four words of bf16; z: their partners (w
+// itself where INTERLEAVED), f: their pairs' cos and sin.  x c + sign y s in fp32
+// first, which is off by less than 2^-22 m (|x| + |y|), the bound: where both ends
+// of that round to the same bf16 value, so does the exact sum.  Two ends in 4000
+// do not, and eight elements that have such are taken again with two floats each.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turned_eight(const uint32_t* w, const uint32_t* z, float sign, const float4* f, float bound,
+                                             uint32_t* out) {
+  uint32_t differ = 0;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const float4 f = s_turn[TurnTable<D>::at(t, pair + 2 * n)], g = s_turn[TurnTable<D>::at(t, pair + 2 * n + 1)];
-    out[2 * n] = turned(bf16_lo(x[n]), bf16_lo(y[n]), Float2{f.x, f.y}, Float2{f.z, f.w}, sign);
-    out[2 * n + 1] = turned(bf16_hi(x[n]), bf16_hi(y[n]), Float2{g.x, g.y}, Float2{g.z, g.w}, sign);
+    const float4 f0 = f[INTERLEAVED ? n : 2 * n], f1 = f[INTERLEAVED ? n : 2 * n + 1];
+    const float x0 = bf16_lo(w[n]), x1 = bf16_hi(w[n]);
+    const float y0 = INTERLEAVED ? -x1 : bf16_lo(z[n]) * sign, y1 = INTERLEAVED ? x0 : bf16_hi(z[n]) * sign;
+    const float v0 = fmaf(x0, f0.x, y0 * f0.z), v1 = fmaf(x1, f1.x, y1 * f1.z);
+    const float e0 = (fabsf(x0) + fabsf(y0)) * bound, e1 = (fabsf(x1) + fabsf(y1)) * bound;
+    out[n] = pack_bf16x2(v0 - e0, v1 - e1);
+    differ |= out[n] ^ pack_bf16x2(v0 + e0, v1 + e1);
+  }
+  if (differ == 0) return;
+#pragma unroll 1
+  for (int n = 0; n < 4; ++n) {
+    const float4 f0 = f[INTERLEAVED ? n : 2 * n], f1 = f[INTERLEAVED ? n : 2 * n + 1];
+    const uint32_t a = n == 0 ? w[0] : n == 1 ? w[1] : n == 2 ? w[2] : w[3];
+    const uint32_t b = INTERLEAVED ? a : n == 0 ? z[0] : n == 1 ? z[1] : n == 2 ? z[2] : z[3];
+    const float x0 = bf16_lo(a), x1 = bf16_hi(a);
+    const float y0 = INTERLEAVED ? -x1 : bf16_lo(b) * sign, y1 = INTERLEAVED ? x0 : bf16_hi(b) * sign;
+    const uint32_t r = pack_bf16x2(turned(x0, y0, Float2{f0.x, f0.y}, Float2{f0.z, f0.w}, 1.f),
+                                   turned(x1, y1, Float2{f1.x, f1.y}, Float2{f1.z, f1.w}, 1.f));
+    if (n == 0) out[0] = r;
+    else if (n == 1) out[1] = r;
+    else if (n == 2) out[2] = r;
+    else out[3] = r;
+  }
+}
+
+// Elements 8 e .. 8 e + 7 of a head's row `src`, turned, as four words of bf16.
+template <int D>
+__device__ __forceinline__ void turned_vector(const __nv_bfloat16* src, int e, const AppendParams& p, const float4* s_turn,
+                                              int t, uint32_t* out) {
+  const int e0 = 8 * e, half = p.rot / 2;
+  const uint4 x4 = __ldg(reinterpret_cast<const uint4*>(src + e0));
+  const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+  const float bound = p.scale * 0x1p-22f;
+  if (e0 >= p.rot) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) out[n] = w[n];
+  } else if (p.interleaved) {
+    turned_eight<true>(w, w, 1.f, s_turn + TurnTable<D>::at(t, e0 / 2), bound, out);
+  } else {
+    const bool upper = e0 >= half;
+    const uint4 y4 = __ldg(reinterpret_cast<const uint4*>(src + (upper ? e0 - half : e0 + half)));
+    const uint32_t z[4] = {y4.x, y4.y, y4.z, y4.w};
+    turned_eight<false>(w, z, upper ? 1.f : -1.f, s_turn + TurnTable<D>::at(t, upper ? e0 - half : e0), bound, out);
   }
 }
 
 // As storing (kv4::store_kernel), with the keys' blocks turned first, and q
 // turned as by rotate_kernel before them.
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
   using kv4::kBlock;
   using kv4::kGroup;
   constexpr int kBlocks = D / kBlock;
@@ -409,11 +430,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
       w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     } else {
       const __nv_bfloat16* src = m.k + tok * m.k_stride + static_cast<long long>(h) * D;
-      float y[16];
-      turned_vector<D>(src, 2 * block, p, s_turn, i, y);
-      turned_vector<D>(src, 2 * block + 1, p, s_turn, i, y + 8);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) w[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+      turned_vector<D>(src, 2 * block, p, s_turn, i, w);
+      turned_vector<D>(src, 2 * block + 1, p, s_turn, i, w + 4);
       if (p.k_out) {
         uint4* dst = reinterpret_cast<uint4*>(p.k_out + (tok * m.Hkv + h) * D + block * kBlock);
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
