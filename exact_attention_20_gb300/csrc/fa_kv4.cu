@@ -19,7 +19,16 @@ namespace kv = fa::kv4;
 using namespace fa_internal;
 
 constexpr int kMaxNodes = kv::kMaxTreeNodes;
-constexpr int kTreeRows = 16;  // rows of a KV head above which a tree goes to the tensor core's 128-row tiles
+// Rows of a KV head above which a tree goes to the tensor core's 128-row tiles.
+// 32 contexts of 250 to 12000 tokens, 8 KV heads, tiles against kv4::decode_kernel:
+// 16 rows 65.2 and 47.8 us at d = 128, 55.1 and 29.5 at d = 64; 24 rows 66.9 and
+// 78.5, 55.5 and 52.8; one context of 20000, d = 128: 16 rows 26.5 and 23.9, 24
+// rows 26.3 and 28.8.
+constexpr int kTreeRows = 16;
+// Key tiles up to which a tree's items are taken whole, one by each CTA, where
+// all are on the card at once: 16 nodes, 8 KV heads, five tiles 13.2 us and 14.4
+// in parts that are merged; six tiles 15.0 and 14.4.
+constexpr int kWholeTiles = 5;
 
 std::mutex g_mu;
 bool g_tree_attr[kMaxDevices][2];  // of tree_kernel: [d == 128]
@@ -128,8 +137,7 @@ DecodePlan tree_plan(int n_seqs, int nodes, int G, int Hkv, int d, int max_pages
   pl.row_tiles = (nodes * G + tr::kRows - 1) / tr::kRows;
   const long long items = static_cast<long long>(n_seqs) * Hkv * pl.row_tiles;
   const long long tiles = (static_cast<long long>(max_pages) * page_size + tr::kKeys - 1) / tr::kKeys;  // of an item, at most
-  // Few short items are taken whole, one by each CTA: nothing to merge.
-  pl.split = items > num_sms || tiles > 2 * tr::kMinTiles;
+  pl.split = items > num_sms || tiles > kWholeTiles;
   if (!pl.split) {
     pl.grid = items;
     return pl;
@@ -144,7 +152,8 @@ DecodePlan tree_plan(int n_seqs, int nodes, int G, int Hkv, int d, int max_pages
 bool tensor_tiles(bool tree, int Lq, int G) { return tree && Lq * G > kTreeRows; }
 
 // ROWS: of a CTA.  Items of 128 rows are in few parts, so that a row's threads take
-// them one after another (32 contexts of 24 nodes: MERGE).
+// them one after another: with two rows a CTA, as for small items, 32 contexts of
+// 24 nodes took 8 us longer.
 template <int D, int ROWS>
 int launch_merge(const kv::DecodeParams& p, const DecodePlan& pl, int rows, cudaStream_t stream) {
   // the merge may be set up while the first kernel runs; its CTAs wait for it
