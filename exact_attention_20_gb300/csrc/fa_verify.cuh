@@ -183,7 +183,8 @@ __device__ __forceinline__ unsigned long long fraction64(float u) {
   return __float2ull_rd(u * 0x1p40f) << 24 | __float2ull_rd((u * 0x1p40f - __ull2float_rz(__float2ull_rd(u * 0x1p40f))) * 0x1p24f);
 }
 
-__device__ __forceinline__ float usable(float x) { return x != x ? -INFINITY : fminf(x, 3.40282347e38f) + 0.f; }  // + 0: -0 orders as 0
+// NaN counts as -inf (a maximum takes the other operand), +inf as the largest finite value.
+__device__ __forceinline__ float usable(float x) { return fminf(fmaxf(x, -INFINITY), 3.40282347e38f); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -257,13 +258,21 @@ struct Row {
   }
 };
 
+// A maximum, the lowest token that has it, and the sum of weights against it.
+struct Top {
+  float max;
+  int token;
+  float sum;
+};
+
 struct Shared {
   float2 table[128];
   float2 T[kMaxNodes];             // what q was multiplied with, child by child
   long long tile[kMaxTiles];       // this CTA's tiles' sums
   long long total[kMaxCluster];    // each CTA's sum
   long long gather[2][2][kMaxCluster];  // [exchange, by turns][value]
-  long long warp[2][kWarps];
+  long long warp[kWarps];
+  Top tops[kWarps];
   int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
   float u[kMaxNodes];
 };
@@ -285,24 +294,25 @@ __device__ __forceinline__ void exchange(long long v, long long w, Shared& s, in
   cluster_sync();
 }
 
-// A row's maximum as an integer key that orders as (value, lowest token first):
-// the value's bits made monotonic above the inverted token.
-__device__ __forceinline__ long long max_key(float v, int x) {
-  const uint32_t b = __float_as_uint(v);
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return static_cast<long long>(static_cast<unsigned long long>(k) << 32 | (0xffffffffu - static_cast<uint32_t>(x))) ^ (1ll << 63);
+// The lanes' Tops as one, the same in every lane (and in every warp that has the same lanes).
+__device__ __forceinline__ Top join(const Top& mine, float c) {
+  // the value's bits made monotonic (-0 as 0)
+  const uint32_t b = __float_as_uint(mine.max + 0.f);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+  Top all;
+  all.max = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+  all.token = __reduce_min_sync(0xffffffffu, mine.max == all.max ? mine.token : 0x7fffffff);
+  all.sum = mine.sum == 0.f ? 0.f : mine.sum * ex2_approx((mine.max - all.max) * c);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) all.sum += __shfl_xor_sync(0xffffffffu, all.sum, off);
+  return all;
 }
-__device__ __forceinline__ float key_value(long long key) {
-  const uint32_t k = static_cast<uint32_t>(static_cast<unsigned long long>(key ^ (1ll << 63)) >> 32);
-  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-__device__ __forceinline__ int key_token(long long key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 
-// The quick pass: the row's maximum (as a key) and, unless greedy, the sum of
-// its weights to about 2^-24, in 2^-44.
+// The quick pass: the row's maximum and the lowest token that has it, and, unless
+// greedy, the sum of its weights to about 2^-24.
 template <bool FP32>
-__device__ __forceinline__ long long row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
-                                               uint32_t size, long long& T) {
+__device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
+                                         uint32_t size) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kAtOnce = 2;  // tiles whose loads are in flight together
   float best = -INFINITY, sum = 0.f;  // the sum against `best`
@@ -346,33 +356,21 @@ __device__ __forceinline__ long long row_quick(const Row<FP32>& row, const Param
     }
   }
   // the warp's, the CTA's, the cluster's
-  auto join = [&](long long key, float S, long long other, float So, long long& k, float& out) {
-    const float a = key_value(key), b = key_value(other), m = fmaxf(a, b);
-    const float base = m == -INFINITY ? 0.f : m;
-    out = S * ex2_approx((a - base) * p.c_hi) + So * ex2_approx((b - base) * p.c_hi);
-    k = max(key, other);
-  };
-  long long key = max_key(best, where);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const long long other = __shfl_xor_sync(0xffffffffu, key, off);
-    const float So = __shfl_xor_sync(0xffffffffu, sum, off);
-    // in the lanes' order, so that both sides have the same sum
-    if (lane & off) join(other, So, key, sum, key, sum);
-    else join(key, sum, other, So, key, sum);
-  }
-  if (lane == 0) s.warp[0][warp] = key, s.warp[1][warp] = __float_as_uint(sum);
+  const Top none{-INFINITY, 0x7fffffff, 0.f};
+  const float c = p.greedy ? 0.f : p.c_hi;
+  Top top = join(Top{best, where, sum}, c);
+  if (lane == 0) s.tops[warp] = top;
   __syncthreads();
-  key = s.warp[0][0], sum = __uint_as_float(static_cast<uint32_t>(s.warp[1][0]));
-#pragma unroll 1
-  for (int w = 1; w < kWarps; ++w) join(key, sum, s.warp[0][w], __uint_as_float(static_cast<uint32_t>(s.warp[1][w])), key, sum);
-  exchange(key, __float_as_uint(sum), s, phase, rank, size);
-  key = s.gather[phase][0][0], sum = __uint_as_float(static_cast<uint32_t>(s.gather[phase][1][0]));
-#pragma unroll 1
-  for (uint32_t r = 1; r < size; ++r)
-    join(key, sum, s.gather[phase][0][r], __uint_as_float(static_cast<uint32_t>(s.gather[phase][1][r])), key, sum);
-  T = __float2ll_rn(sum * 0x1p44f);
-  return key;
+  top = join(lane < kWarps ? s.tops[lane] : none, c);
+  exchange(static_cast<long long>(static_cast<unsigned long long>(__float_as_uint(top.max)) << 32 | static_cast<uint32_t>(top.token)),
+           __float_as_uint(top.sum), s, phase, rank, size);
+  top = none;
+  if (lane < size) {
+    const unsigned long long v = static_cast<unsigned long long>(s.gather[phase][0][lane]);
+    top = Top{__uint_as_float(static_cast<uint32_t>(v >> 32)), static_cast<int>(v & 0xffffffffu),
+              __uint_as_float(static_cast<uint32_t>(s.gather[phase][1][lane]))};
+  }
+  return join(top, c);
 }
 
 // What is left of the weights of tokens x .. x + 7 after m drawn children.
@@ -419,11 +417,11 @@ __device__ __forceinline__ long long row_sum(const Row<FP32>& row, float M, int 
     if (lane == 0) s.tile[t - row.begin] = sum;
     mine += sum;
   }
-  if (lane == 0) s.warp[0][warp] = mine;
+  if (lane == 0) s.warp[warp] = mine;
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s.warp[0][w];
+  for (int w = 0; w < kWarps; ++w) total += s.warp[w];
   exchange(total, 0, s, phase, rank, size);
   if (threadIdx.x < size) s.total[threadIdx.x] = s.gather[phase][0][threadIdx.x];
   total = 0;
@@ -499,15 +497,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     if (writer) p.path[node0 + kept] = cur;
     ++kept;
     const Row<FP32> row(p, node0 + cur, rank, size);
-    long long T;
-    const long long top = row_quick(row, p, s, phase, rank, size, T);
-    const float M = key_value(top);
+    const Top top = row_quick(row, p, s, phase, rank, size);
+    const float M = top.max;
+    long long T = __float2ll_rn(top.sum * 0x1p44f);
     int accepted = -1;
     if (M == -INFINITY) break;
     if (p.greedy) {
       for (int j = cur + 1; j < p.n_nodes && accepted < 0; ++j)
-        if (s.parents[j] == cur && s.tokens[j] == key_token(top)) accepted = j;
-      if (accepted < 0 && writer) p.next_token[seq] = key_token(top);
+        if (s.parents[j] == cur && s.tokens[j] == top.token) accepted = j;
+      if (accepted < 0 && writer) p.next_token[seq] = top.token;
       cur = accepted;
       continue;
     }
