@@ -302,14 +302,19 @@ struct State {
   const uint2* q_shared;     // this lane's words in shared memory, steps and row tiles 32 apart
   unsigned long long* lines; // TREE: [kRows], the warp's
 
-  // Whether row r of the item's row tile at row0 sees a position (one of the sequence's, where TREE).
-  __device__ __forceinline__ bool sees(int r, int row0, int position, const Walk& w, const DecodeParams& p) const {
+  // What row r of the item's row tile at row0 sees: its line (TREE), or up to its own
+  // position (a row past the item's last is as its last).
+  __device__ __forceinline__ unsigned long long sight(int r, int row0, const Walk& w, const DecodeParams& p) const {
+    if constexpr (TREE) return lines[r];
+    return static_cast<unsigned>(w.len - p.Lq + min(row0 + r, p.Lq * p.G - 1) / p.G);
+  }
+  // Whether that has a position (one of the sequence's, where TREE) in it.
+  __device__ __forceinline__ bool sees(unsigned long long sight, int position, const Walk& w, const DecodeParams& p) const {
     if constexpr (TREE) {
       const int node = position - (w.len - p.Lq);
-      return node < 0 || (node < 64 && ((lines[r] >> node) & 1ull));
+      return node < 0 || (node < 64 && ((sight >> node) & 1ull));
     } else {
-      // a row past the item's last is as its last
-      return position <= w.len - p.Lq + min(row0 + r, p.Lq * p.G - 1) / p.G;  // the row's own position
+      return position <= static_cast<int>(sight);
     }
   }
 
@@ -514,7 +519,7 @@ struct State {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (!sees(nt * 8 + 2 * t + e, row0, pos + k, w, p)) continue;
+              if (!sees(sight(nt * 8 + 2 * t + e, row0, w, p), pos + k, w, p)) continue;
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) acc[nt][j][e] = acc[nt][j][2 + e] = __uint_as_float(0x7fffffffu);
             }
@@ -585,11 +590,11 @@ struct State {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = nt * 8 + 2 * t + e;
+          const unsigned long long seen = sight(nt * 8 + 2 * t + e, row0, w, p);
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            if (((skip >> n) & 1u) || !sees(r, row0, pos + n * kGroup + key, w, p)) c[n][nt][e] = -INFINITY;
-            if (((skip >> n) & 1u) || !sees(r, row0, pos + n * kGroup + key + 8, w, p)) c[n][nt][2 + e] = -INFINITY;
+            if (((skip >> n) & 1u) || !sees(seen, pos + n * kGroup + key, w, p)) c[n][nt][e] = -INFINITY;
+            if (((skip >> n) & 1u) || !sees(seen, pos + n * kGroup + key + 8, w, p)) c[n][nt][2 + e] = -INFINITY;
           }
         }
     }
