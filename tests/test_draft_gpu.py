@@ -569,3 +569,76 @@ def test_nothing_to_do(draft, serve):
     out = draft.verify_tree(torch.empty((0, 4, 10), device=DEV), none, none, torch.empty((0, 4), device=DEV))
     assert [t.shape[0] for t in out] == [0, 0, 0]
     assert draft.kv4_keep(cache, table, kv4.int32([]), none, kv4.int32([]), 64).shape == (0,)
+
+
+@pytest.mark.parametrize("nodes", [4, 40])
+def test_offsets_beyond_32_bits(draft, serve, nodes):
+    lens, page, hq, hkv, d = [333, 40], 64, 8, 2, 128
+    near, table, _, _ = kv4.fill(serve, lens, hkv, d, page, 95)
+    n = near.shape[0]
+    far = torch.empty((1 << 18, *near.shape[1:]), dtype=near.dtype, device=DEV)
+    shift = far.shape[0] - n
+    assert far[shift:].data_ptr() - far.data_ptr() > 1 << 32
+    far[shift:] = near
+    q = torch.randn((2 * nodes, hq, d), generator=kv4.generator(96), device=DEV).bfloat16()
+    parents = kv4.int32([ref.tree(cpu_generator(97), nodes)] * 2)
+    path = kv4.int32([[0, 2, 3] + [-1] * (nodes - 3)] * 2)
+    got = []
+    for c, t in ((near, table), (far, table + shift)):
+        got.append(draft.kv4_tree_attention(q, c, t, kv4.int32(lens), parents))
+        draft.kv4_keep(c, t, kv4.int32(lens), path, kv4.int32([3, 3]), d)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(far[shift:], near)
+
+
+def test_logits_beyond_32_bits(draft):
+    nodes, V, step = 40, 1000, 1 << 26  # the last node's row starts 5.2 GB behind the first's
+    g = kv4.generator(98)
+    logits = torch.randn((1, nodes, V), generator=g, device=DEV).bfloat16()
+    probs = torch.softmax(torch.randn((1, nodes, V), generator=g, device=DEV), -1)
+    far = torch.empty((nodes - 1) * step + V, dtype=torch.bfloat16, device=DEV).as_strided((1, nodes, V), (nodes * step, step, 1))
+    far_probs = torch.empty((nodes - 1) * step + V, device=DEV).as_strided((1, nodes, V), (nodes * step, step, 1))
+    far.copy_(logits), far_probs.copy_(probs)
+    parents = kv4.int32([[-1] + list(range(nodes - 1))])  # one line: the walk may reach the last row
+    tokens = kv4.int32([[0] + logits[0, :-1].argmax(-1).tolist()])
+    for p, fp, u in ((None, None, 0.0), (probs, far_probs, 0.0), (None, None, 0.999), (probs, far_probs, 0.999)):
+        us = torch.full((1, nodes), u, device=DEV)
+        a, b = draft.verify_tree(logits, tokens, parents, us, p), draft.verify_tree(far, tokens, parents, us, fp)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        assert u > 0 or a[1].tolist() == [nodes]
+
+
+@pytest.mark.parametrize("nodes,hq", [(4, 4), (24, 8)])
+def test_a_padded_batch_is_the_batch(draft, serve, nodes, hq):
+    hkv, d, page, V = 2, 64, 16, 500
+    lens = [130, 57]
+    cache, table, _, _ = kv4.fill(serve, lens, hkv, d, page, 99)
+    g = kv4.generator(100)
+    q = torch.randn((2 * nodes, hq, d), generator=g, device=DEV).bfloat16()
+    logits = torch.randn((2, nodes, V), generator=g, device=DEV)
+    tokens = torch.randint(0, V, (2, nodes), generator=g, device=DEV).int()
+    u = torch.rand((2, nodes), generator=g, device=DEV)
+    parents = kv4.int32([ref.tree(cpu_generator(s), nodes) for s in (101, 102)])
+    twin = cache.clone()
+    errors = kv4.int32([0])
+
+    def step(cache, q, table, lens, parents, logits, tokens, u):
+        o, lse = draft.kv4_tree_attention(q, cache, table, lens, parents, errors=errors)
+        path, kept, nxt = draft.verify_tree(logits, tokens, parents, u)
+        return o, lse, path, kept, nxt, draft.kv4_keep(cache, table, lens, path, kept, d, errors=errors)
+
+    def padded(x, fill, rows=1):  # the sequences at 1 and 3 of 5
+        out = torch.full((5 * rows, *x.shape[1:]), fill, dtype=x.dtype, device=DEV)
+        out[rows:2 * rows], out[3 * rows:4 * rows] = x[:rows], x[rows:]
+        return out
+
+    want = step(cache, q, table, kv4.int32(lens), parents, logits, tokens, u)
+    got = step(twin, padded(q, math.nan, nodes), padded(table, -1), padded(kv4.int32(lens), 0), padded(parents, -2),
+               padded(logits, math.nan), padded(tokens, -7), padded(u, math.nan))
+    assert errors.item() == 0 and torch.equal(twin, cache)
+    for i, (a, b) in enumerate(zip(want, got)):
+        axis, rows = (1, nodes) if i == 1 else (0, nodes if i == 0 else 1)
+        a, b = a.movedim(axis, 0), b.movedim(axis, 0)
+        assert torch.equal(a, torch.cat([b[rows:2 * rows], b[3 * rows:4 * rows]]))
+        rest = torch.cat([b[:rows], b[2 * rows:3 * rows], b[4 * rows:]])
+        assert (rest == (0, -math.inf, -1, 0, -1, 0)[i]).all()

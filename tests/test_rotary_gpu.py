@@ -278,3 +278,30 @@ def test_streams_and_a_captured_step(rotary, serve):
     lens += 1
     g.replay()
     assert torch.equal(out, rotary.rotate(q, None, rope, lens - 1))
+
+
+def test_offsets_beyond_32_bits(rotary, serve):
+    T, step = 140, 1 << 24  # the last token's row starts 4.7 GB behind the first's
+    rope = rotary.rope(64, interleaved=True)
+    q, k = normal(90, T, 3, 128), normal(91, T, 2, 128)
+    far = torch.empty((T - 1) * step + 5 * 128, dtype=torch.bfloat16, device=DEV)
+    far_q, far_k = far.as_strided((T, 3, 128), (step, 128, 1)), far.as_strided((T, 2, 128), (step, 128, 1), 3 * 128)
+    far_q.copy_(q), far_k.copy_(k)
+    want = rotary.rotate(q, k, rope)
+    assert all(torch.equal(a, b) for a, b in zip(rotary.rotate(far_q, far_k, rope), want))
+    # appended from there to pages behind 4 GB of the cache, and read back
+    pages = 1 << 18
+    near = serve.kv4_cache(3, 2, 128, 64, device=DEV)
+    cache = torch.empty((pages, *near.shape[1:]), dtype=near.dtype, device=DEV)
+    assert cache[-3:].data_ptr() - cache.data_ptr() > 1 << 32
+    args = kv4.int32([T]), kv4.int32([0, T])
+    qs = []
+    for c, first, a, b in ((near, 0, q, k), (cache, pages - 3, far_q, far_k)):
+        c[-3:].fill_(0xA5)
+        table = kv4.int32([[first + 2, first, first + 1]])
+        qs.append(rotary.kv4_append(c, a, b, b, rope, table, *args))
+        qs += serve.kv4_load(c, table, *args, T, 128)
+    assert torch.equal(near, cache[-3:]) and all(torch.equal(a, b) for a, b in zip(qs[:3], qs[3:]))
+    # and in place
+    rotary.fa_rotate(far_q, far_k, far_q, far_k, rope)
+    assert torch.equal(far_q, want[0]) and torch.equal(far_k, want[1])
