@@ -11,13 +11,13 @@
 // once, in shared memory, for 128 rows:
 //
 // - Codes times scales are exact in f16 (fa_kv4.cuh).  Q rows are brought to
-//   [2^14, 2^15) by a power of two, P lies in [0, 2^15) with a maximum at 2^8 when
-//   the reference is set: as in fa_kv4_decode.cuh, f16 then loses nothing above
-//   2^-33 of the maximum, P's rounding is 2^-11, every sum is fp32.
+//   [2^14, 2^15) by a power of two, and P to a maximum of 2^8 when the reference is
+//   set, which moves when P would leave f16's range: as in fa_kv4_decode.cuh, f16 then
+//   loses nothing above 2^-33 of the maximum, P's rounding is 2^-11, every sum is fp32.
 // - Two softmax warpgroups, one row a thread, take a CTA's tiles in turn, each
-//   with its own S, P and O in tensor memory, its own running maximum and sum and
-//   its own issuer, so that one's products overlap the other's exponentials and
-//   neither waits for the other's maximum.  An item's two states meet at its end.
+//   with its own S, P and O in tensor memory and its own running maximum and sum, so
+//   that one's products overlap the other's exponentials and neither waits for the
+//   other's maximum.  An item's two states meet at its end.
 // - Eight warps turn codes into operands, K or V of 32 keys each, from a ring that
 //   one warp fills (bulk copies some tiles ahead, across items).  A tile's K and V each
 //   have two places in shared memory, one for each warpgroup.
@@ -30,6 +30,21 @@
 // Work: the (sequence, KV head, row tile) items' tiles, concatenated, are cut
 // into ranges of equal cost, one per CTA, from the lengths on the device; an item
 // cut between CTAs is merged by merge_kernel (fa_kv4_decode.cuh).
+//
+// Measured on a GB300 (8 KV heads of 4 query heads, d = 128): 60 nodes over 131000
+// tokens 130 us, 990 TFLOP/s of visible products (58 us at cuBLAS' bf16 rate, 68
+// with the rows that fill the second tile of 128; the cache read twice, 302 MB, 45
+// us); 24 nodes over 32 contexts of 250 to 12000 tokens 67 us (17; 22 with the rows
+// that fill a tile; 16 for the bytes).  A tile takes a CTA 1.07 us: the tensor core
+// has work for 46 % of that, issue slots are 56 % used.  What bounds it is a
+// warpgroup's own round, two tiles long: its products 0.6 us (the operands, the codes
+// and their conversion move 196 KB through shared memory a tile, 0.75 us at the most),
+// scores through tensor memory 0.2 us a half, exponentials 0.3 a half, four
+// hand-overs of 0.1.  Without the softmax's arithmetic the long context takes 116 us,
+// without the conversion of codes 120.  An item's start and end are 5 us, a launch's
+// start 2.7.
+// Items of 256 rows, each warpgroup with all key tiles for its own 128 (half the
+// conversions and loads; K then has one place only): 137 us.
 //
 // Warps: 0-7 softmax; 8-15 codes to operands; 16 MMA issuer; 17 loads.
 #pragma once
@@ -46,7 +61,9 @@ constexpr int kRows = 128;             // of an item
 constexpr int kKeys = 128;             // of a tile
 constexpr int kTurnWarps = 8;          // four for K, four for V; two groups of a tile each
 constexpr int kThreads = 640;
-constexpr int kItemTiles = 8;          // an item's own cost, in tiles
+// An item's own cost, in tiles.  The 32 contexts: 112, 91, 84 and 84 us with 2, 4, 6
+// and 9 (the merge still with two rows a CTA).
+constexpr int kItemTiles = 8;
 constexpr int kMinTiles = 2;           // a CTA takes at least, where there are that many
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSiteTree = 8;           // status code: a wait gave up

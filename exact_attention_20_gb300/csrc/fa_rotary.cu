@@ -128,7 +128,6 @@ int fa_rotate(const void* q, const void* k, void* q_out, void* k_out, const int*
   p.rot = rot_dim;
   p.interleaved = interleaved;
   p.copy_rest = !in_place;
-  p.heads_outer = strides[2] > strides[1];
   p.m = magnitude;
   p.sign = backward ? -1.f : 1.f;
   p.tokens_per_cta = std::min(ro::kMaxTokens, tokens_per_cta(static_cast<int>(static_cast<long long>(B) * N), view.num_sms));

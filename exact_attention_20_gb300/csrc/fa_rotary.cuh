@@ -168,7 +168,7 @@ struct RotateParams {
   long long position_stride;        // of a batch entry: N, or 0
   int N, Hq, H;             // H = Hq + Hk
   int rot, interleaved, copy_rest;  // copy_rest: elements past rot are written too (not in place)
-  int tokens_per_cta, heads_outer;  // heads_outer: a head's tokens are neighbours, not a token's heads
+  int tokens_per_cta;
   float m, sign;            // sign: -1 for the gradient
 };
 
@@ -202,7 +202,10 @@ constexpr int kAhead = 4;  // heads whose loads are in flight together
 // of the tokens' pairs go to shared memory once; then a thread has the eight
 // pairs of one token to itself and goes through the heads with them in registers,
 // two 16-byte loads and stores each (of neighbouring elements if interleaved,
-// else rot / 2 apart), four heads' loads in flight.  Bound by the bytes: FIGURES
+// else rot / 2 apart), four heads' loads in flight.  Bound by the bytes: q and k of
+// 4 x 32 heads x 4096 tokens x 128, one direction, 84 us, 6.4 TB/s, 95 % of the
+// copy rate (a thread going from head to head with cos and sin read from shared
+// memory each time, four ways in conflict: 102 us).  A step of 64 tokens: 2.5 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
   __shared__ float2 s_cs[kMaxTokens * (D / 2)];
@@ -342,7 +345,10 @@ __device__ __forceinline__ void turned_vector(const __nv_bfloat16* src, int e, c
 }
 
 // As storing (kv4::store_kernel), with the keys' blocks turned first, and q
-// turned as by rotate_kernel before them.
+// turned as by rotate_kernel before them.  79063 tokens of 32 and 8 heads, d = 128:
+// 1.71 GB, 293 us, 5.8 TB/s, 86 % of the copy rate, at 59 % of the issue slots (64
+// registers a thread: 293 us; 80, three CTAs an SM: 323; every key element with two
+// floats each, without the bound's test: 340).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
   using kv4::kBlock;

@@ -30,6 +30,15 @@
 // tokens, a warp a tile at a time, a lane eight tokens, and every CTA takes every
 // decision from the same numbers.  Tiles' sums stay in shared memory, so that the
 // token is found by looking at one tile again.
+//
+// Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
+// 111 us; the 96 MB of rows that are visited (3.4 a sequence, and the draft's where a
+// child is refused) would take 14 at the copy rate.  An exact pass is some 65
+// instructions a token, and a sequence's passes (5.6 on average, 10 at the most)
+// follow one another: issue slots are 43 % used while an SM has work, and of the
+// kernel's time SMs have work for two thirds.  CTAs of 128 threads, five an SM: 127
+// us where 256 threads, three an SM, took 139 and 256, two an SM, 168.  One tree of 16
+// nodes, 32000 tokens in bf16: 12.6 us.
 #pragma once
 
 #include <cuda_bf16.h>
