@@ -10,6 +10,7 @@ turn per position, so far positions lose nothing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple
 
@@ -139,7 +140,10 @@ def _strides(name, x, shape, device):
     return (s[0], s[2], s[1]) if len(s) == 4 else (0, s[0], s[1])
 
 
-_Strides = _L * 12
+@functools.lru_cache(maxsize=1024)
+def _stride_array(*strides):
+    """The strides as the C array that fa_rotate reads."""
+    return (_L * 12)(*strides)
 
 
 def _rotate(q, k, q_out, k_out, r, positions, backward, stream):
@@ -185,7 +189,7 @@ def _rotate(q, k, q_out, k_out, r, positions, backward, stream):
                 k_out = torch.empty(kshape, dtype=torch.bfloat16, device=dev)
         rc = lib().fa_rotate(q.data_ptr(), k.data_ptr() if hk else None, q_out.data_ptr(), k_out.data_ptr() if hk else None,
                              None if positions is None else positions.data_ptr(), r.turns.data_ptr(), B, N, hq, hk, d, rot,
-                             1 if r.interleaved else 0, r.magnitude, backward, _Strides(*strides), position_stride, handle)
+                             1 if r.interleaved else 0, r.magnitude, backward, _stride_array(*strides), position_stride, handle)
         if rc != FA_OK:
             raise FAError(rc)
     if target.other is not None:
