@@ -101,6 +101,7 @@ int fa_verify_tree(const void* logits, int logits_fp32, const int* tokens, const
   if (!p.greedy) {
     p.c_hi = static_cast<float>(c);
     p.c_lo = static_cast<float>(c - static_cast<double>(p.c_hi));
+    p.span = static_cast<float>(vf::kSpan / c);
   }
   const int size = cluster_size(dev, V);
   cudaLaunchConfig_t cfg{};

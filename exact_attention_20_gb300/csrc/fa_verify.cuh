@@ -57,7 +57,8 @@ constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
 constexpr int kMaxTiles = kMaxVocab / kTile + 1;  // of a row that starts within a tile
 constexpr int kMaxCluster = 16;  // (more than 8 has to be asked for)
-constexpr float kMinLog = -60.f;                  // what is below is rounded to 0 as 2^-60 is
+constexpr float kSpan = 64.f;                     // powers of two below the maximum; what lies further is taken as 2^-64, which is rounded to 0
+constexpr float kFar = 16384.f;                   // of the maximum's power of two: above it, differences from it are taken first
 
 // 2^(k / 128) as a sum of two floats.
 __device__ const float2 kExp2[128] = {
@@ -118,6 +119,7 @@ struct Params {
   int n_nodes, V;
   long long logits_stride, draft_stride;
   float c_hi, c_lo;  // log2(e) / temperature
+  float span;        // kSpan of those
   int greedy;        // temperature 0
 };
 
@@ -130,39 +132,58 @@ __device__ __forceinline__ Pair quick_sum(float a, float b) {  // |a| >= |b|, or
   return Pair{s, __fsub_rn(b, __fsub_rn(s, a))};
 }
 
-__device__ __forceinline__ Pair two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
-  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x))};
+// What a row's weights are taken against: its maximum M.
+struct Reference {
+  float shift, low, top;  // tokens are taken as x - shift, from low (NaN, too) to top
+  int n;                // M's power of two in 128ths: bits of n / 128 + kRound
+  float rest;           // and what is left of it
+};
+
+// t + kRound is t to the nearest 128th (|t| < 2^15), which is exact.
+constexpr float kRound = 98304.f;  // 1.5 * 2^16
+
+// Far from 0 the difference to M is exact for every token that counts, near 0 it is not needed.
+__device__ __forceinline__ Reference reference(float M, const Params& p) {
+  Reference r;
+  r.shift = fabsf(M) * p.c_hi > kFar ? M : 0.f;
+  const float x = r.top = M - r.shift;
+  r.low = x - p.span;
+  const float t = __fmaf_rn(x, p.c_hi, kRound);
+  r.n = __float_as_int(t);
+  r.rest = __fmaf_rn(x, p.c_lo, __fmaf_rn(x, p.c_hi, -__fsub_rn(t, kRound)));
+  return r;
 }
 
-// exp((x - M) / temperature) for x <= M: z = (x - M) c as a sum of two floats,
-// z = n / 128 + r with |r| <= 2^-8, 2^z = 2^(n / 128) (1 + y + y^2 / 2 + ...), y = r
-// ln 2.  What the polynomial leaves out is below 2^-49.
-__device__ __forceinline__ Pair weight(float x, float M, const Params& p, const float2* table) {
-  const Pair d = two_sum(x, -M);
-  // no branch, so that a lane's eight tokens overlap: what is far below is taken as 2^-60 and rounded to 0
-  const float z0 = d.hi * p.c_hi, z = fmaxf(z0, kMinLog);
-  const float z_lo = z0 > kMinLog ? fmaf(d.hi, p.c_hi, -z) + fmaf(d.hi, p.c_lo, d.lo * p.c_hi) : 0.f;
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-  const float t = fmaf(z, 128.f, kRound);
-  const int n = __float_as_int(t) - __float_as_int(kRound);
-  const float r = fmaf(__fsub_rn(t, kRound), -1.f / 128.f, z);  // exact
-  constexpr float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
-  const float y = r * kLn2;
-  const float y_lo = fmaf(r, kLn2, -y) + fmaf(r, kLn2Lo, z_lo * kLn2);
-  const float more = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y_lo);  // 2^z / 2^(n/128) - 1 - y
-  const float2 e = table[n & 127];
-  const float q = e.x * y;
-  const Pair v = quick_sum(e.x, q + (fmaf(e.x, y, -q) + fmaf(e.x, more, e.y)));
-  const float scale = __int_as_float((127 + (n >> 7)) << 23);
-  return Pair{v.hi * scale, v.lo * scale};
+// (x + lo) scale
+struct Weight {
+  float x, lo, scale;
+  __device__ __forceinline__ Pair pair() const { return Pair{x * scale, lo * scale}; }
+};
+
+// exp((x - M) / temperature): with d a token's difference to the shift, d c = t + r
+// for t a multiple of 1 / 128 and |r| <= 2^-8, one fused product; 2^(t - M's) from the
+// table; e^y - 1 for y = (r - M's rest) ln 2 by a polynomial, which leaves out less than
+// 2^-49.  Off by about 2^-31 of the weight, from r's and y's roundings (2^-33 each) and
+// that of the product with the table's value (2^-32).
+__device__ __forceinline__ Weight weight(float x, const Reference& ref, const Params& p, const float2* table) {
+  const float d = fminf(fmaxf(__fsub_rn(x, ref.shift), ref.low), ref.top);
+  const float t = __fmaf_rn(d, p.c_hi, kRound);
+  const float r = __fmaf_rn(d, p.c_hi, -__fsub_rn(t, kRound));
+  const float y = __fadd_rn(r, __fmaf_rn(d, p.c_lo, -ref.rest));
+  constexpr float kLn2 = 0.693147180559945f;
+  const float e = __fmaf_rn(y, kLn2, __fmul_rn(__fmul_rn(y, y), __fmaf_rn(y, __fmaf_rn(y, kLn2 * kLn2 * kLn2 * kLn2 / 24,
+                                                                             kLn2 * kLn2 * kLn2 / 6), kLn2 * kLn2 / 2)));
+  const int k = __float_as_int(t) - ref.n;  // in 128ths: 0 down to -64 * 128
+  const float2 v = table[k & 127];
+  return Weight{v.x, __fmaf_rn(v.x, e, v.y), __int_as_float((k & ~127) * 65536 + 0x3f800000)};
 }
 
 // a - q T, at least 0, for T as a sum of two floats.
 __device__ __forceinline__ Pair without(const Pair& a, float q, const float2& T) {
-  const float h = q * T.x;
-  const Pair d = two_sum(a.hi, -h);
-  const Pair v = quick_sum(d.hi, d.lo + (a.lo - fmaf(q, T.y, fmaf(q, T.x, -h))));
+  const float h = __fmul_rn(q, T.x);
+  const float more = __fmaf_rn(q, T.y, __fmaf_rn(q, T.x, -h));
+  const float d = __fsub_rn(a.hi, h), err = __fsub_rn(__fsub_rn(a.hi, d), h);  // exact where something is left
+  const Pair v = quick_sum(d, __fadd_rn(err, __fsub_rn(a.lo, more)));
   return v.hi > 0.f ? v : Pair{0.f, 0.f};  // not where it is NaN
 }
 
@@ -172,13 +193,14 @@ struct Fixed {
   int hi, lo;
   __device__ __forceinline__ long long value() const { return (static_cast<long long>(hi) << 22) + lo; }
 };
-__device__ __forceinline__ Fixed fixed44(const Pair& a) {
+__device__ __forceinline__ Fixed fixed44(const Weight& w) {
   constexpr float kHi = 3.f;           // sums near it are multiples of 2^-22
   constexpr float kLo = 0x1.8p-21f;    // of 2^-44
-  const float h = __fadd_rn(a.hi, kHi);
-  const float rest = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(h, kHi)), a.lo);
+  const float h = __fmaf_rn(__fadd_rn(w.x, w.lo), w.scale, kHi);
+  const float rest = __fmaf_rn(w.lo, w.scale, __fmaf_rn(w.x, w.scale, -__fsub_rn(h, kHi)));
   return Fixed{__float_as_int(h) - __float_as_int(kHi), __float_as_int(__fadd_rn(rest, kLo)) - __float_as_int(kLo)};
 }
+__device__ __forceinline__ Fixed fixed44(const Pair& a) { return fixed44(Weight{a.hi, a.lo, 1.f}); }
 
 __device__ __forceinline__ float2 from_fixed44(long long T) {
   const float hi = __ll2float_rz(T);
@@ -236,8 +258,8 @@ struct Row {
     end = min(tiles, begin + per);
   }
   __device__ __forceinline__ int first(int tile) const { return tile * kTile - shift + static_cast<int>(threadIdx.x & 31) * 8; }
-  __device__ __forceinline__ float at(int x) const { return usable(FP32 ? __ldg(f + x) : __bfloat162float(b[x])); }
-  // Tokens x .. x + 7; -inf outside the row.
+  __device__ __forceinline__ float at(int x) const { return FP32 ? __ldg(f + x) : __bfloat162float(b[x]); }
+  // Tokens x .. x + 7, as they are; -inf outside the row.
   __device__ __forceinline__ void load(int x, float* v) const {
     if (x >= 0 && x + 8 <= V) {
       if constexpr (FP32) {
@@ -249,8 +271,6 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = usable(v[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = x + i >= 0 && x + i < V ? at(x + i) : -INFINITY;
@@ -333,6 +353,8 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
     for (int n = 0; n < kAtOnce; ++n) {
       if (t + n * kWarps < row.end) {
         row.load(row.first(t + n * kWarps), v[n]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[n][i] = usable(v[n][i]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[n][i] = -INFINITY;
@@ -384,22 +406,27 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
 
 // What is left of the weights of tokens x .. x + 7 after m drawn children.
 template <bool FP32>
-__device__ __forceinline__ void left8(const Row<FP32>& row, int x, float M, int m, int gone, const Params& p, const Shared& s,
+__device__ __forceinline__ void left8(const Row<FP32>& row, int x, const Reference& ref, int m, int gone, const Params& p, const Shared& s,
                                       Fixed* out) {
   float v[8], q[8];
   row.load(x, v);
-  if (m > 0) row.load_draft(x, q);
-  Pair a[8];
+  if (m == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = weight(v[i], M, p, s.table);
+    for (int i = 0; i < 8; ++i) out[i] = fixed44(weight(v[i], ref, p, s.table));
+  } else {
+    row.load_draft(x, q);
+    Pair a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = weight(v[i], ref, p, s.table).pair();
 #pragma unroll 1
-  for (int n = 0; n < m; ++n) {
-    const float2 T = s.T[n];
+    for (int n = 0; n < m; ++n) {
+      const float2 T = s.T[n];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = without(a[i], q[i], T);
+      for (int i = 0; i < 8; ++i) a[i] = without(a[i], q[i], T);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = fixed44(a[i]);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = fixed44(a[i]);
 #pragma unroll 1
   for (int n = 0; n < gone; ++n) {
     const int i = s.gone[n] - x;
@@ -411,13 +438,13 @@ __device__ __forceinline__ void left8(const Row<FP32>& row, int x, float M, int 
 
 // The sums of what is left: tiles', CTAs' and, returned, the row's.
 template <bool FP32>
-__device__ __forceinline__ long long row_sum(const Row<FP32>& row, float M, int m, const Params& p, Shared& s, int& phase,
+__device__ __forceinline__ long long row_sum(const Row<FP32>& row, const Reference& ref, int m, const Params& p, Shared& s, int& phase,
                                              uint32_t rank, uint32_t size) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long mine = 0;
   for (int t = row.begin + warp; t < row.end; t += kWarps) {
     Fixed w[8], part{0, 0};
-    left8(row, row.first(t), M, m, 0, p, s, w);
+    left8(row, row.first(t), ref, m, 0, p, s, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) part.hi += w[i].hi, part.lo += w[i].lo;
     part.hi = __reduce_add_sync(0xffffffffu, part.hi);
@@ -442,7 +469,7 @@ __device__ __forceinline__ long long row_sum(const Row<FP32>& row, float M, int 
 // The first token whose running sum exceeds `target` (below the sum of all), by
 // the CTA whose part it is in.
 template <bool FP32>
-__device__ __forceinline__ void find_token(const Row<FP32>& row, long long target, float M, int m, int gone, const Params& p,
+__device__ __forceinline__ void find_token(const Row<FP32>& row, long long target, const Reference& ref, int m, int gone, const Params& p,
                                            const Shared& s, uint32_t rank, int* where) {
   long long before = 0;
   for (uint32_t r = 0; r < rank; ++r) before += s.total[r];
@@ -469,7 +496,7 @@ __device__ __forceinline__ void find_token(const Row<FP32>& row, long long targe
     Fixed w[8];
     long long sum = 0;
     const int x = row.first(t0 + l);
-    left8(row, x, M, m, gone, p, s, w);
+    left8(row, x, ref, m, gone, p, s, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += w[i].value();
     long long at = before + scan(sum) - sum;
@@ -518,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
       cur = accepted;
       continue;
     }
+    const Reference ref = reference(M, p);
     int m = 0, gone = 0;
     bool exact = false;  // T and the sums in shared memory are
     bool stale = false;  // ... but not those of m
@@ -525,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     for (int j = cur + 1; j < p.n_nodes; ++j) {
       const int x = s.tokens[j];
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
-      Pair a = weight(row.at(x), M, p, s.table);
+      const Weight own = weight(row.at(x), ref, p, s.table);
       if (row.q) {
+        Pair a = own.pair();
         const float q = __ldg(row.q + x), u = s.u[j];
         for (int n = 0; n < m; ++n) a = without(a, q, s.T[n]);
         // u q T < a
@@ -539,16 +568,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         }
         if (first) {  // not accepted: from here on T is the exact one
           first = false;
-          T = row_sum(row, M, 0, p, s, phase, rank, size), exact = true;
+          T = row_sum(row, ref, 0, p, s, phase, rank, size), exact = true;
         }
         __syncthreads();
         if (threadIdx.x == 0) s.T[m] = from_fixed44(T);
         __syncthreads();
-        const long long left = row_sum(row, M, m + 1, p, s, phase, rank, size);
+        const long long left = row_sum(row, ref, m + 1, p, s, phase, rank, size);
         stale = left <= 0;
         if (!stale) T = left, ++m;
       } else {
-        long long w = fixed44(a).value();
+        long long w = fixed44(own).value();
         for (int n = 0; n < gone; ++n)
           if (s.gone[n] == x) w = 0;
         if (static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T))) < w) {
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         }
         if (first) {
           first = false;
-          T = row_sum(row, M, 0, p, s, phase, rank, size), exact = true;
+          T = row_sum(row, ref, 0, p, s, phase, rank, size), exact = true;
         }
         if (w == 0 || T - w <= 0) continue;
         T -= w;
@@ -573,10 +602,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
       }
     }
     if (accepted < 0) {
-      if (!exact) T = row_sum(row, M, 0, p, s, phase, rank, size);
-      if (stale) row_sum(row, M, m, p, s, phase, rank, size);
+      if (!exact) T = row_sum(row, ref, 0, p, s, phase, rank, size);
+      if (stale) row_sum(row, ref, m, p, s, phase, rank, size);
       const long long target = static_cast<long long>(__umul64hi(fraction64(s.u[0]), static_cast<unsigned long long>(T)));
-      find_token(row, target, M, m, gone, p, s, rank, p.next_token + seq);
+      find_token(row, target, ref, m, gone, p, s, rank, p.next_token + seq);
     }
     cur = accepted;
     __syncthreads();  // shared sums have been read
