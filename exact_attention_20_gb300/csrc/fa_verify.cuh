@@ -8,7 +8,8 @@
 //
 //     a <- max(0, a - q T),   T <- sum a,
 //
-// which is max(r - q, 0) normalised, r = a / T.  A token given (no q) loses its
+// which is max(r - q, 0) normalised, r = a / T.  A node's children are drawn from one
+// q, so after several a = max(0, w - q S) with S the sum of their T.  A token given (no q) loses its
 // w.  The next token is the first x where a(0) + ... + a(x) > u_0 T.
 //
 // A running sum over 10^5 tokens meets u_0 T next to some token's border all
@@ -51,7 +52,8 @@ namespace fa {
 namespace verify {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 5;
+constexpr int kCtasPerSm = 7;
+constexpr int kHalves = 2;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
@@ -178,10 +180,10 @@ __device__ __forceinline__ Weight weight(float x, const Reference& ref, const Pa
   return Weight{v.x, __fmaf_rn(v.x, e, v.y), __int_as_float((k & ~127) * 65536 + 0x3f800000)};
 }
 
-// a - q T, at least 0, for T as a sum of two floats.
-__device__ __forceinline__ Pair without(const Pair& a, float q, const float2& T) {
-  const float h = __fmul_rn(q, T.x);
-  const float more = __fmaf_rn(q, T.y, __fmaf_rn(q, T.x, -h));
+// a - q S, at least 0, for S as a sum of two floats.
+__device__ __forceinline__ Pair without(const Pair& a, float q, const float2& S) {
+  const float h = __fmul_rn(q, S.x);
+  const float more = __fmaf_rn(q, S.y, __fmaf_rn(q, S.x, -h));
   const float d = __fsub_rn(a.hi, h), err = __fsub_rn(__fsub_rn(a.hi, d), h);  // exact where something is left
   const Pair v = quick_sum(d, __fadd_rn(err, __fsub_rn(a.lo, more)));
   return v.hi > 0.f ? v : Pair{0.f, 0.f};  // not where it is NaN
@@ -205,6 +207,14 @@ __device__ __forceinline__ Fixed fixed44(const Pair& a) { return fixed44(Weight{
 __device__ __forceinline__ float2 from_fixed44(long long T) {
   const float hi = __ll2float_rz(T);
   return make_float2(hi * 0x1p-44f, __ll2float_rn(T - static_cast<long long>(hi)) * 0x1p-44f);
+}
+
+// Of two positive sums of two floats.
+__device__ __forceinline__ float2 plus(const float2& a, const float2& b) {
+  const bool more = a.x >= b.x;
+  const Pair s = quick_sum(more ? a.x : b.x, more ? b.x : a.x);
+  const Pair v = quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.y, b.y)));
+  return make_float2(v.hi, v.lo);
 }
 
 // u to 64 fractional bits, from [0, 1); anything else is taken as an end of it.
@@ -276,13 +286,29 @@ struct Row {
       for (int i = 0; i < 8; ++i) v[i] = x + i >= 0 && x + i < V ? at(x + i) : -INFINITY;
     }
   }
-  __device__ __forceinline__ void load_draft(int x, float* v) const {
-    if (x >= 0 && x + 8 <= V && (reinterpret_cast<uintptr_t>(q + x) & 15) == 0) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(q + x)), c = __ldg(reinterpret_cast<const float4*>(q + x) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+  // Tokens x .. x + 3, and the draft's.
+  __device__ __forceinline__ void load4(int x, float* v) const {
+    if (x >= 0 && x + 4 <= V) {
+      if constexpr (FP32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(f + x));
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(b + x));
+        v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
+        v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x + i >= 0 && x + i < V ? __ldg(q + x + i) : 0.f;
+      for (int i = 0; i < 4; ++i) v[i] = x + i >= 0 && x + i < V ? at(x + i) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void load4_draft(int x, float* v) const {
+    if (x >= 0 && x + 4 <= V && (reinterpret_cast<uintptr_t>(q + x) & 15) == 0) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(q + x));
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = x + i >= 0 && x + i < V ? __ldg(q + x + i) : 0.f;
     }
   }
 };
@@ -296,14 +322,12 @@ struct Top {
 
 struct Shared {
   float2 table[128];
-  float2 T[kMaxNodes];             // what q was multiplied with, child by child
   long long tile[kMaxTiles];       // this CTA's tiles' sums
-  long long total[kMaxCluster];    // each CTA's sum
-  long long gather[2][2][kMaxCluster];  // [exchange, by turns][value]
-  long long warp[kWarps];
+  long long gather[2][2][kMaxCluster];  // [exchange, by turns][value]; after row_sum each CTA's sum
+  long long warp[2][kWarps];       // [exchange]
   Top tops[kWarps];
   int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
-  float u[kMaxNodes];
+  float u[kMaxNodes], logit[kMaxNodes], draft[kMaxNodes];  // of the node's children: at their tokens
 };
 
 // Every CTA's two values to every CTA, in gather[phase]; whole CTA.  A buffer is
@@ -404,76 +428,69 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
   return join(top, c);
 }
 
-// What is left of the weights of tokens x .. x + 7 after m drawn children.
+// What is left of the weights of tokens x .. x + 3: less q S where `drawn`, less `gone` given ones.
 template <bool FP32>
-__device__ __forceinline__ void left8(const Row<FP32>& row, int x, const Reference& ref, int m, int gone, const Params& p, const Shared& s,
-                                      Fixed* out) {
-  float v[8], q[8];
-  row.load(x, v);
-  if (m == 0) {
+__device__ __forceinline__ void left4(const Row<FP32>& row, int x, const Reference& ref, bool drawn, const float2& S, int gone,
+                                      const Params& p, const Shared& s, Fixed* out) {
+  float v[4], q[4];
+  row.load4(x, v);
+  if (!drawn) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = fixed44(weight(v[i], ref, p, s.table));
+    for (int i = 0; i < 4; ++i) out[i] = fixed44(weight(v[i], ref, p, s.table));
   } else {
-    row.load_draft(x, q);
-    Pair a[8];
+    row.load4_draft(x, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = weight(v[i], ref, p, s.table).pair();
-#pragma unroll 1
-    for (int n = 0; n < m; ++n) {
-      const float2 T = s.T[n];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = without(a[i], q[i], T);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = fixed44(a[i]);
+    for (int i = 0; i < 4; ++i) out[i] = fixed44(without(weight(v[i], ref, p, s.table).pair(), q[i], S));
   }
 #pragma unroll 1
   for (int n = 0; n < gone; ++n) {
     const int i = s.gone[n] - x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 4; ++e)
       if (i == e) out[e] = Fixed{0, 0};
   }
 }
 
 // The sums of what is left: tiles', CTAs' and, returned, the row's.
 template <bool FP32>
-__device__ __forceinline__ long long row_sum(const Row<FP32>& row, const Reference& ref, int m, const Params& p, Shared& s, int& phase,
+__device__ __forceinline__ long long row_sum(const Row<FP32>& row, const Reference& ref, bool drawn, const float2& S, const Params& p, Shared& s, int& phase,
                                              uint32_t rank, uint32_t size) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long mine = 0;
   for (int t = row.begin + warp; t < row.end; t += kWarps) {
-    Fixed w[8], part{0, 0};
-    left8(row, row.first(t), ref, m, 0, p, s, w);
+    Fixed part{0, 0};
+#pragma unroll kHalves
+    for (int half = 0; half < 2; ++half) {
+      Fixed w[4];
+      left4(row, row.first(t) + 4 * half, ref, drawn, S, 0, p, s, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part.hi += w[i].hi, part.lo += w[i].lo;
+      for (int i = 0; i < 4; ++i) part.hi += w[i].hi, part.lo += w[i].lo;
+    }
     part.hi = __reduce_add_sync(0xffffffffu, part.hi);
     part.lo = __reduce_add_sync(0xffffffffu, part.lo);
     const long long sum = part.value();
     if (lane == 0) s.tile[t - row.begin] = sum;
     mine += sum;
   }
-  if (lane == 0) s.warp[warp] = mine;
+  if (lane == 0) s.warp[phase ^ 1][warp] = mine;
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s.warp[w];
+  for (int w = 0; w < kWarps; ++w) total += s.warp[phase ^ 1][w];
   exchange(total, 0, s, phase, rank, size);
-  if (threadIdx.x < size) s.total[threadIdx.x] = s.gather[phase][0][threadIdx.x];
   total = 0;
   for (uint32_t r = 0; r < size; ++r) total += s.gather[phase][0][r];
-  __syncthreads();
   return total;
 }
 
 // The first token whose running sum exceeds `target` (below the sum of all), by
 // the CTA whose part it is in.
 template <bool FP32>
-__device__ __forceinline__ void find_token(const Row<FP32>& row, long long target, const Reference& ref, int m, int gone, const Params& p,
-                                           const Shared& s, uint32_t rank, int* where) {
+__device__ __forceinline__ void find_token(const Row<FP32>& row, long long target, const Reference& ref, bool drawn, const float2& S, int gone, const Params& p,
+                                           const Shared& s, int phase, uint32_t rank, int* where) {
   long long before = 0;
-  for (uint32_t r = 0; r < rank; ++r) before += s.total[r];
-  if (threadIdx.x >= 32 || target < before || target >= before + s.total[rank]) return;
+  for (uint32_t r = 0; r < rank; ++r) before += s.gather[phase][0][r];
+  if (threadIdx.x >= 32 || target < before || target >= before + s.gather[phase][0][rank]) return;
   const int lane = threadIdx.x;
   auto scan = [&](long long v) {  // inclusive, over the lanes
 #pragma unroll
@@ -496,7 +513,8 @@ __device__ __forceinline__ void find_token(const Row<FP32>& row, long long targe
     Fixed w[8];
     long long sum = 0;
     const int x = row.first(t0 + l);
-    left8(row, x, ref, m, gone, p, s, w);
+    left4(row, x, ref, drawn, S, gone, p, s, w);
+    left4(row, x + 4, ref, drawn, S, gone, p, s, w + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += w[i].value();
     long long at = before + scan(sum) - sum;
@@ -533,6 +551,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     if (writer) p.path[node0 + kept] = cur;
     ++kept;
     const Row<FP32> row(p, node0 + cur, rank, size);
+    // what the children's tokens have is on its way during the pass
+    float logit = -INFINITY, draft = 0.f;
+    if (threadIdx.x < p.n_nodes && !p.greedy && s.parents[threadIdx.x] == cur) {
+      const int x = s.tokens[threadIdx.x];
+      if (x >= 0 && x < p.V) {
+        logit = row.at(x);
+        if (row.q) draft = __ldg(row.q + x);
+      }
+    }
     const Top top = row_quick(row, p, s, phase, rank, size);
     const float M = top.max;
     long long T = __float2ll_rn(top.sum * 0x1p44f);
@@ -545,19 +572,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
       cur = accepted;
       continue;
     }
+    if (threadIdx.x < p.n_nodes) s.logit[threadIdx.x] = logit, s.draft[threadIdx.x] = draft;
+    __syncthreads();
     const Reference ref = reference(M, p);
-    int m = 0, gone = 0;
+    int gone = 0;
+    bool drawn = false;               // whether S is above 0
+    float2 S = make_float2(0.f, 0.f);  // the T of all drawn children that were not accepted
     bool exact = false;  // T and the sums in shared memory are
-    bool stale = false;  // ... but not those of m
+    bool stale = false;  // ... but not those of S
     bool first = true;
     for (int j = cur + 1; j < p.n_nodes; ++j) {
       const int x = s.tokens[j];
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
-      const Weight own = weight(row.at(x), ref, p, s.table);
+      const Weight own = weight(s.logit[j], ref, p, s.table);
       if (row.q) {
         Pair a = own.pair();
-        const float q = __ldg(row.q + x), u = s.u[j];
-        for (int n = 0; n < m; ++n) a = without(a, q, s.T[n]);
+        const float q = s.draft[j], u = s.u[j];
+        if (drawn) a = without(a, q, S);
         // u q T < a
         const float2 t = from_fixed44(T);
         const float uq = u * q, uq_lo = fmaf(u, q, -uq);
@@ -568,14 +599,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         }
         if (first) {  // not accepted: from here on T is the exact one
           first = false;
-          T = row_sum(row, ref, 0, p, s, phase, rank, size), exact = true;
+          T = row_sum(row, ref, false, S, p, s, phase, rank, size), exact = true;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) s.T[m] = from_fixed44(T);
-        __syncthreads();
-        const long long left = row_sum(row, ref, m + 1, p, s, phase, rank, size);
+        const float2 more = plus(S, from_fixed44(T));
+        const long long left = row_sum(row, ref, true, more, p, s, phase, rank, size);
         stale = left <= 0;
-        if (!stale) T = left, ++m;
+        if (!stale) T = left, S = more, drawn = true;
       } else {
         long long w = fixed44(own).value();
         for (int n = 0; n < gone; ++n)
@@ -586,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         }
         if (first) {
           first = false;
-          T = row_sum(row, ref, 0, p, s, phase, rank, size), exact = true;
+          T = row_sum(row, ref, false, S, p, s, phase, rank, size), exact = true;
         }
         if (w == 0 || T - w <= 0) continue;
         T -= w;
@@ -594,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         if (threadIdx.x == 0) {
           s.gone[gone] = x;
           const int tile = (x + row.shift) / kTile;
-          s.total[tile / row.per] -= w;
+          s.gather[phase][0][tile / row.per] -= w;
           if (tile >= row.begin && tile < row.end) s.tile[tile - row.begin] -= w;
         }
         __syncthreads();
@@ -602,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
       }
     }
     if (accepted < 0) {
-      if (!exact) T = row_sum(row, ref, 0, p, s, phase, rank, size);
-      if (stale) row_sum(row, ref, m, p, s, phase, rank, size);
+      if (!exact) T = row_sum(row, ref, false, S, p, s, phase, rank, size);
+      if (stale) row_sum(row, ref, drawn, S, p, s, phase, rank, size);
       const long long target = static_cast<long long>(__umul64hi(fraction64(s.u[0]), static_cast<unsigned long long>(T)));
-      find_token(row, target, ref, m, gone, p, s, rank, p.next_token + seq);
+      find_token(row, target, ref, drawn, S, gone, p, s, phase, rank, p.next_token + seq);
     }
     cur = accepted;
     __syncthreads();  // shared sums have been read
