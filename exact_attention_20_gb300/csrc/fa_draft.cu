@@ -17,36 +17,61 @@ namespace {
 namespace vf = fa::verify;
 using namespace fa_internal;
 
-std::mutex g_mu;
-int g_cluster[kMaxDevices];  // the largest cluster of verify_kernel; 0: not asked yet
+// What a device holds of verify_kernel.
+struct Held {
+  int cluster;  // the largest cluster; 0: not asked yet
+  int wide;     // CTAs of such clusters that are on the card at once, of kThreads threads
+};
 
-// CTAs of a sequence's cluster: as many as leave each warp a tile.  Eight for 48
-// sequences, which are then all on the card at once, leave it idle behind those
-// that have done their walks: 164 us where clusters of 16 take 145 (both with 256
-// threads a CTA).
-int cluster_size(int dev, int V) {
-  int c = 0;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (g_cluster[dev] == 0) {
-      g_cluster[dev] = 8;
-      if (cudaFuncSetAttribute(vf::verify_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-          cudaFuncSetAttribute(vf::verify_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(vf::kMaxCluster);
-        cfg.blockDim = dim3(vf::kThreads);
-        int most[2] = {0, 0};
-        if (cudaOccupancyMaxPotentialClusterSize(&most[0], vf::verify_kernel<true>, &cfg) == cudaSuccess &&
-            cudaOccupancyMaxPotentialClusterSize(&most[1], vf::verify_kernel<false>, &cfg) == cudaSuccess &&
-            std::min(most[0], most[1]) >= vf::kMaxCluster)
-          g_cluster[dev] = vf::kMaxCluster;
+std::mutex g_mu;
+Held g_held[kMaxDevices];
+
+Held held(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  Held& h = g_held[dev];
+  if (h.cluster == 0) {
+    const auto a = vf::verify_kernel<true>;
+    const auto b = vf::verify_kernel<false>;
+    const bool large = cudaFuncSetAttribute(a, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                       cudaFuncSetAttribute(b, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (h.cluster = large ? vf::kMaxCluster : 8; h.cluster > 1; h.cluster /= 2) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(h.cluster);
+      cfg.blockDim = dim3(vf::kThreads);
+      cudaLaunchAttribute attr{};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = h.cluster;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n[2] = {0, 0};
+      if (cudaOccupancyMaxActiveClusters(&n[0], a, &cfg) == cudaSuccess &&
+          cudaOccupancyMaxActiveClusters(&n[1], b, &cfg) == cudaSuccess && std::min(n[0], n[1]) > 0) {
+        h.wide = std::min(n[0], n[1]) * h.cluster;
+        break;
       }
-      cudaGetLastError();  // what was refused there is no error of this call
     }
-    c = g_cluster[dev];
+    cudaGetLastError();  // what was refused there is no error of this call
   }
-  while (c > 1 && V < vf::kTile * vf::kWarps * (c - 1)) c /= 2;
-  return c;
+  return h;
+}
+
+// CTAs of a sequence's cluster, and their threads.  A walk's passes follow one another,
+// so that a sequence wants as many warps as have a tile, but sequences that wait for
+// others to end want fewer: 256 threads where all clusters are on the card at once, else
+// 128 (fp32, 128000 tokens: 1, 16 and 48 sequences 31, 53 and 80 us with 256, 39, 66 and 78
+// with 128).  Clusters of eight, not of 16, leave the card idle
+// behind the sequences that are done (48 sequences, 164 us for 145 at the time).
+void shape(const Held& h, int n_seqs, int V, int* cluster, int* threads) {
+  const int tiles = (V + vf::kTile - 1) / vf::kTile;
+  auto size = [&](int warps) {
+    int c = h.cluster;
+    while (c > 1 && tiles <= warps * (c - 1)) c /= 2;
+    return c;
+  };
+  *cluster = size(vf::kWarps);
+  *threads = vf::kThreads;
+  if (static_cast<long long>(n_seqs) * *cluster > h.wide) *threads = vf::kThreads / 2, *cluster = size(vf::kWarps / 2);
 }
 
 }  // namespace
@@ -103,10 +128,11 @@ int fa_verify_tree(const void* logits, int logits_fp32, const int* tokens, const
     p.c_lo = static_cast<float>(c - static_cast<double>(p.c_hi));
     p.span = static_cast<float>(vf::kSpan / c);
   }
-  const int size = cluster_size(dev, V);
+  int size = 0, threads = 0;
+  shape(held(dev), n_seqs, V, &size, &threads);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(n_seqs) * size);
-  cfg.blockDim = dim3(vf::kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;

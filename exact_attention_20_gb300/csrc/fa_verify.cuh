@@ -15,10 +15,9 @@
 // A running sum over 10^5 tokens meets u_0 T next to some token's border all
 // the time: with sums and exponentials in fp32 one call in a hundred would give
 // another token than the same sums in 64 bits do.  So each w is computed as a sum
-// of two floats (relative error about 2^-40: exp2 by the table-driven method, 128
-// table entries and a short polynomial, every product with its error) and rounded to
-// a multiple of 2^-44; sums of those are 64-bit integers, exact, and the same
-// however the row is cut.
+// of two floats (relative error below 2^-29: table-driven, 128 entries and a short
+// polynomial) and rounded to a multiple of 2^-44; sums of those are 64-bit integers,
+// exact, and the same however the row is cut.
 //
 // Whether a child is accepted is one comparison, which T's error of about 2^-24
 // decides otherwise once in ten million: a node's first child is judged by a T
@@ -33,13 +32,15 @@
 // token is found by looking at one tile again.
 //
 // Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
-// 111 us; the 96 MB of rows that are visited (3.4 a sequence, and the draft's where a
-// child is refused) would take 14 at the copy rate.  An exact pass is some 65
-// instructions a token, and a sequence's passes (5.6 on average, 10 at the most)
-// follow one another: issue slots are 43 % used while an SM has work, and of the
-// kernel's time SMs have work for two thirds.  CTAs of 128 threads, five an SM: 127
-// us where 256 threads, three an SM, took 139 and 256, two an SM, 168.  One tree of 16
-// nodes, 32000 tokens in bf16: 12.6 us.
+// 78 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
+// child is refused) would take 14 at the copy rate.  A quick pass is some 12
+// instructions a token, an exact one 30, or 43 with the draft's; a sequence's passes
+// (5.6 on average, 10 at the most) follow one another, 7 of them in 31 us on an idle
+// card, where each waits for its first loads, two reductions and the cluster's
+// barrier.  All 48 together use 43 % of the issue slots while an SM has work.  One tree
+// of 16 nodes, 32000 tokens in bf16: 11.9 us.  What the steps brought at 48 sequences:
+// exact weights of 60 instructions, right to 2^-40, 111 us; 30, 93; one product with
+// q for all refused children, and fewer registers, 75 to 78.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -51,9 +52,8 @@
 namespace fa {
 namespace verify {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 7;
-constexpr int kHalves = 2;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a CTA, at most
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
@@ -164,9 +164,10 @@ struct Weight {
 
 // exp((x - M) / temperature): with d a token's difference to the shift, d c = t + r
 // for t a multiple of 1 / 128 and |r| <= 2^-8, one fused product; 2^(t - M's) from the
-// table; e^y - 1 for y = (r - M's rest) ln 2 by a polynomial, which leaves out less than
-// 2^-49.  Off by about 2^-31 of the weight, from r's and y's roundings (2^-33 each) and
-// that of the product with the table's value (2^-32).
+// table; e^(y ln 2) - 1 for y = r - M's rest by a polynomial, which leaves out less than
+// 2^-45.  Off by less than 2^-29 of the weight: roundings of 2^-32 of y, of the
+// polynomial's value and of its product with the table's (2^-29.7 at the most in 8
+// million values against 64 bits).
 __device__ __forceinline__ Weight weight(float x, const Reference& ref, const Params& p, const float2* table) {
   const float d = fminf(fmaxf(__fsub_rn(x, ref.shift), ref.low), ref.top);
   const float t = __fmaf_rn(d, p.c_hi, kRound);
@@ -366,17 +367,17 @@ __device__ __forceinline__ Top join(const Top& mine, float c) {
 template <bool FP32>
 __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
                                          uint32_t size) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   constexpr int kAtOnce = 2;  // tiles whose loads are in flight together
   float best = -INFINITY, sum = 0.f;  // the sum against `best`
   int where = 0x7fffffff;
 #pragma unroll 1
-  for (int t = row.begin + warp; t < row.end; t += kAtOnce * kWarps) {
+  for (int t = row.begin + warp; t < row.end; t += kAtOnce * warps) {
     float v[kAtOnce][8];
 #pragma unroll
     for (int n = 0; n < kAtOnce; ++n) {
-      if (t + n * kWarps < row.end) {
-        row.load(row.first(t + n * kWarps), v[n]);
+      if (t + n * warps < row.end) {
+        row.load(row.first(t + n * warps), v[n]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[n][i] = usable(v[n][i]);
       } else {
@@ -393,7 +394,7 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
       if (top > best) {  // ascending tokens: the first of equals stays
         sum *= ex2_approx((best - top) * p.c_hi);
         best = top;
-        const int x = row.first(t + n * kWarps);
+        const int x = row.first(t + n * warps);
 #pragma unroll
         for (int i = 7; i >= 0; --i)
           if (v[n][i] == top) where = x + i;
@@ -416,7 +417,7 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
   Top top = join(Top{best, where, sum}, c);
   if (lane == 0) s.tops[warp] = top;
   __syncthreads();
-  top = join(lane < kWarps ? s.tops[lane] : none, c);
+  top = join(lane < warps ? s.tops[lane] : none, c);
   exchange(static_cast<long long>(static_cast<unsigned long long>(__float_as_uint(top.max)) << 32 | static_cast<uint32_t>(top.token)),
            __float_as_uint(top.sum), s, phase, rank, size);
   top = none;
@@ -455,11 +456,11 @@ __device__ __forceinline__ void left4(const Row<FP32>& row, int x, const Referen
 template <bool FP32>
 __device__ __forceinline__ long long row_sum(const Row<FP32>& row, const Reference& ref, bool drawn, const float2& S, const Params& p, Shared& s, int& phase,
                                              uint32_t rank, uint32_t size) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   long long mine = 0;
-  for (int t = row.begin + warp; t < row.end; t += kWarps) {
+  for (int t = row.begin + warp; t < row.end; t += warps) {
     Fixed part{0, 0};
-#pragma unroll kHalves
+#pragma unroll
     for (int half = 0; half < 2; ++half) {
       Fixed w[4];
       left4(row, row.first(t) + 4 * half, ref, drawn, S, 0, p, s, w);
@@ -475,8 +476,7 @@ __device__ __forceinline__ long long row_sum(const Row<FP32>& row, const Referen
   if (lane == 0) s.warp[phase ^ 1][warp] = mine;
   __syncthreads();
   long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s.warp[phase ^ 1][w];
+  for (int w = 0; w < warps; ++w) total += s.warp[phase ^ 1][w];
   exchange(total, 0, s, phase, rank, size);
   total = 0;
   for (uint32_t r = 0; r < size; ++r) total += s.gather[phase][0][r];

@@ -86,9 +86,9 @@ int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, in
  *                 -1), with next_token -1.
  *   next_token  : int32 [n_seqs]; written.  -1 where every logit of the row is -inf.
  *
- * Probabilities are taken to 2^-44 of a row's largest (exponentials right to about
- * 2^-40, sums in 64-bit integers): where a running sum passes a random number
- * hardly ever depends on roundings, and never on how the work is divided.
+ * Probabilities are taken to 2^-44 of a row's largest (exponentials right to 2^-29,
+ * sums in 64-bit integers): where a running sum passes a random number hardly
+ * ever depends on roundings, and never on how the work is divided.
  * V <= 2^18.  One launch.  Errors: FA_ERR_INVALID_ARG, FA_ERR_NULL, FA_ERR_ALIGN (each
  * pointer to its element's size), FA_ERR_ALIAS, FA_ERR_DEVICE, FA_ERR_LAUNCH.
  */
