@@ -19,10 +19,11 @@
 // polynomial) and rounded to a multiple of 2^-44; sums of those are 64-bit integers,
 // exact, and the same however the row is cut.
 //
-// Whether a child is accepted is one comparison, which T's error of about 2^-24
-// decides otherwise once in ten million: a node's first child is judged by a T
-// from one quick pass over the row, fp32 exponentials against running maxima,
-// which finds M, too.  Where that child is accepted nothing more is asked of the row.
+// Whether a child is accepted is one comparison, for which a T right to 2^-16 is
+// enough but for one child in ten thousand or so: a node's first child is judged by a
+// T from one quick pass over the row, fp32 exponentials against running maxima,
+// which finds M, too.  Where that child is surely accepted nothing more is asked of the
+// row; where it is not sure, the exact T is.
 //
 // Work: a quick pass a node; where its first child is not accepted, or there is
 // none, a pass for the exact T, and one more for each drawn child that is not
@@ -32,15 +33,15 @@
 // token is found by looking at one tile again.
 //
 // Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
-// 78 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
+// 80 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
 // child is refused) would take 14 at the copy rate.  A quick pass is some 12
 // instructions a token, an exact one 30, or 43 with the draft's; a sequence's passes
 // (5.6 on average, 10 at the most) follow one another, 7 of them in 31 us on an idle
 // card, where each waits for its first loads, two reductions and the cluster's
 // barrier.  All 48 together use 43 % of the issue slots while an SM has work.  One tree
-// of 16 nodes, 32000 tokens in bf16: 11.9 us.  What the steps brought at 48 sequences:
+// of 16 nodes, 32000 tokens in bf16: 12.1 us.  What the steps brought at 48 sequences:
 // exact weights of 60 instructions, right to 2^-40, 111 us; 30, 93; one product with
-// q for all refused children, and fewer registers, 75 to 78.
+// q for all refused children, and fewer registers, 75 to 80.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -59,6 +60,10 @@ constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
 constexpr int kMaxTiles = kMaxVocab / kTile + 1;  // of a row that starts within a tile
 constexpr int kMaxCluster = 16;  // (more than 8 has to be asked for)
+// The quick pass's sum is right to 2^-16 of it: at most 34 products with a power of two
+// right to 2^-22, the powers' arguments to 2^-23.3 of themselves (17 where all tokens of
+// a row lie there), 40 additions.
+constexpr float kQuick = 0x1p-15f;
 constexpr float kSpan = 64.f;                     // powers of two below the maximum; what lies further is taken as 2^-64, which is rounded to 0
 constexpr float kFar = 16384.f;                   // of the maximum's power of two: above it, differences from it are taken first
 
@@ -580,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     float2 S = make_float2(0.f, 0.f);  // the T of all drawn children that were not accepted
     bool exact = false;  // T and the sums in shared memory are
     bool stale = false;  // ... but not those of S
-    bool first = true;
     for (int j = cur + 1; j < p.n_nodes; ++j) {
       const int x = s.tokens[j];
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
@@ -589,17 +593,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         Pair a = own.pair();
         const float q = s.draft[j], u = s.u[j];
         if (drawn) a = without(a, q, S);
-        // u q T < a
-        const float2 t = from_fixed44(T);
-        const float uq = u * q, uq_lo = fmaf(u, q, -uq);
-        const float h = uq * t.x, l = fmaf(uq, t.x, -h) + fmaf(uq, t.y, uq_lo * t.x);
-        if ((h - a.hi) + (l - a.lo) < 0.f) {
+        // u q T - a, and whether that has its sign for any T that the quick pass may stand for
+        bool sure = true;
+        auto excess = [&]() {
+          const float2 t = from_fixed44(T);
+          const float uq = u * q, uq_lo = fmaf(u, q, -uq);
+          const float h = uq * t.x, l = fmaf(uq, t.x, -h) + fmaf(uq, t.y, uq_lo * t.x);
+          const float d = (h - a.hi) + (l - a.lo);
+          sure = exact || fabsf(d) > h * kQuick;
+          return d;
+        };
+        float d = excess();
+        if (sure && d < 0.f) {
           accepted = j;
           break;
         }
-        if (first) {  // not accepted: from here on T is the exact one
-          first = false;
+        if (!exact) {
           T = row_sum(row, ref, false, S, p, s, phase, rank, size), exact = true;
+          if (!sure && (d = excess()) < 0.f) {
+            accepted = j;
+            break;
+          }
         }
         const float2 more = plus(S, from_fixed44(T));
         const long long left = row_sum(row, ref, true, more, p, s, phase, rank, size);
@@ -609,13 +623,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         long long w = fixed44(own).value();
         for (int n = 0; n < gone; ++n)
           if (s.gone[n] == x) w = 0;
-        if (static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T))) < w) {
+        bool sure = true;
+        auto excess = [&]() {
+          const long long h = static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T)));
+          sure = exact || llabs(h - w) > static_cast<long long>(static_cast<float>(h) * kQuick) + 1;
+          return h - w;
+        };
+        long long d = excess();
+        if (sure && d < 0) {
           accepted = j;
           break;
         }
-        if (first) {
-          first = false;
+        if (!exact) {
           T = row_sum(row, ref, false, S, p, s, phase, rank, size), exact = true;
+          if (!sure && (d = excess()) < 0) {
+            accepted = j;
+            break;
+          }
         }
         if (w == 0 || T - w <= 0) continue;
         T -= w;

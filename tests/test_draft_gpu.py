@@ -642,3 +642,33 @@ def test_a_padded_batch_is_the_batch(draft, serve, nodes, hq):
         assert torch.equal(a, torch.cat([b[rows:2 * rows], b[3 * rows:4 * rows]]))
         rest = torch.cat([b[:rows], b[2 * rows:3 * rows], b[4 * rows:]])
         assert (rest == (0, -math.inf, -1, 0, -1, 0)[i]).all()
+
+
+@pytest.mark.parametrize("offset,temperature", [(3e4, 1.0), (-3e4, 1.0), (1e6, 1.0), (-1e6, 20.0), (8.0, 1e-3), (11350.0, 1.0), (-11360.0, 1.0),
+                                                (5675.0, 0.5), (1e30, 1e26), (-300.0, 1e4)])
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("fp32", [True, False])
+def test_verify_logits_far_from_zero(draft, offset, temperature, drawn, fp32):
+    # on both sides of where differences to the maximum are taken first (11356.5 temperatures)
+    logits, tokens, parents, u, probs = make_verify(103, 12, 8, 3001, drawn)
+    logits = (logits.double() * temperature + offset).to(torch.float32 if fp32 else torch.bfloat16)
+    check_verify(draft, logits, tokens, parents, u, probs, temperature)
+
+
+@pytest.mark.parametrize("V", [999, 20000, 131072])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_does_not_depend_on_how_it_is_divided(draft, V, drawn):
+    # many sequences at once (fewer threads each) and one by one; part of a wider row, whose tiles begin elsewhere
+    n, nodes = 70, 6
+    logits, tokens, parents, u, probs = make_verify(104, n, nodes, V, drawn)
+    parents = kv4.int32(parents)
+    want = draft.verify_tree(logits, tokens, parents, u, draft_probs=probs)
+    for i in range(0, n, 3):
+        one = slice(i, i + 1)
+        got = draft.verify_tree(logits[one], tokens[one], parents[one], u[one], draft_probs=None if probs is None else probs[one])
+        assert all(torch.equal(a[one], b) for a, b in zip(want, got))
+    wide = torch.full((n, nodes, V + 5), math.nan, device=DEV)
+    wide[..., 5:] = logits
+    got = draft.verify_tree(wide.view(n * nodes, V + 5)[:, 5:], tokens, parents, u,
+                            draft_probs=None if probs is None else probs.view(n * nodes, V))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
