@@ -25,6 +25,12 @@ constexpr int kMaxNodes = kv::kMaxTreeNodes;
 // 78.5, 55.5 and 52.8; one context of 20000, d = 128: 16 rows 26.5 and 23.9, 24
 // rows 26.3 and 28.8.
 constexpr int kTreeRows = 16;
+// Rows of a KV head above which it does so where that is little work: items taken
+// whole, or key tiles for no more than a CTA each.  8 KV heads, tiles against
+// kv4::decode_kernel: 12 rows over 600 tokens 13.2 and 18.2 us at d = 128, 11.7 and
+// 13.8 at d = 64; over 2000 15.4 and 18.7, 14.0 and 14.0; two contexts of 2000 17.8 and
+// 19.6, 15.5 and 14.6.  8 rows over 600 tokens 13.4 and 13.3, over 2000 15.3 and 13.6.
+constexpr int kFewRows = 8;
 // Key tiles up to which a tree's items are taken whole, one by each CTA, where
 // all are on the card at once: 16 nodes, 8 KV heads, five tiles 13.2 us and 14.4
 // in parts that are merged; six tiles 15.0 and 14.4.
@@ -149,7 +155,18 @@ DecodePlan tree_plan(int n_seqs, int nodes, int G, int Hkv, int d, int max_pages
   return pl;
 }
 
-bool tensor_tiles(bool tree, int Lq, int G) { return tree && Lq * G > kTreeRows; }
+// How a call is divided; *tiles: by the tensor core's 128-row tiles.
+DecodePlan plan(bool tree, int n_seqs, int Lq, int G, int Hkv, int d, int max_pages, int page_size, int num_sms, bool* tiles) {
+  *tiles = false;
+  if (tree && Lq * G > kFewRows) {
+    const DecodePlan pl = tree_plan(n_seqs, Lq, G, Hkv, d, max_pages, page_size, num_sms);
+    const long long keys = static_cast<long long>(max_pages) * page_size;
+    const long long work = static_cast<long long>(n_seqs) * Hkv * ((keys + kv::tree::kKeys - 1) / kv::tree::kKeys);
+    *tiles = Lq * G > kTreeRows || !pl.split || work <= num_sms;
+    if (*tiles) return pl;
+  }
+  return decode_plan(n_seqs, Lq, G, Hkv, d, max_pages, page_size, num_sms);
+}
 
 // ROWS: of a CTA.  Items of 128 rows are in few parts, so that a row's threads take
 // them one after another: with two rows a CTA, as for small items, 32 contexts of
@@ -205,13 +222,13 @@ int launch_decode(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cuda
   return pl.split ? launch_merge<D, 2>(p, pl, 8 * NT, stream) : FA_OK;
 }
 
-template <bool TREE>
-int launch_rows(const kv::DecodeParams& p, const DecodePlan& pl, int d, int dev, cudaStream_t s) {
-  if (d == 128)
-    return pl.nt == 1 ? launch_decode<128, 1, TREE>(p, pl, dev, s)
-         : pl.nt == 2 ? launch_decode<128, 2, TREE>(p, pl, dev, s) : launch_decode<128, 4, TREE>(p, pl, dev, s);
-  return pl.nt == 1 ? launch_decode<64, 1, TREE>(p, pl, dev, s)
-       : pl.nt == 2 ? launch_decode<64, 2, TREE>(p, pl, dev, s) : launch_decode<64, 4, TREE>(p, pl, dev, s);
+template <int D, bool TREE>
+int launch_rows(const kv::DecodeParams& p, const DecodePlan& pl, int dev, cudaStream_t s) {
+  if (pl.nt == 1) return launch_decode<D, 1, TREE>(p, pl, dev, s);
+  if constexpr (!TREE) {  // (more rows of a tree go to its own kernel)
+    if (pl.nt == 4) return launch_decode<D, 4, TREE>(p, pl, dev, s);
+  }
+  return launch_decode<D, 2, TREE>(p, pl, dev, s);
 }
 
 int check_decode_sizes(int n_seqs, int Lq, int Hq, int Hkv, int d, int max_pages, int page_size) {
@@ -233,8 +250,8 @@ int attention_workspace(bool tree, int n_seqs, int Lq, int Hq, int Hkv, int d, i
   fa_internal::DeviceView view;
   rc = current(&dev, &view);
   if (rc != FA_OK) return rc;
-  const auto plan = tensor_tiles(tree, Lq, Hq / Hkv) ? tree_plan : decode_plan;
-  *bytes = n_seqs == 0 ? 0 : plan(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms).bytes;
+  bool tiles = false;
+  *bytes = n_seqs == 0 ? 0 : plan(tree, n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms, &tiles).bytes;
   return FA_OK;
 }
 
@@ -277,8 +294,8 @@ int attention(bool tree, const void* q, const void* cache, const int* page_table
   fa_internal::DeviceView view;
   rc = current(&dev, &view);
   if (rc != FA_OK) return rc;
-  const bool tiles = tensor_tiles(tree, Lq, Hq / Hkv);
-  const DecodePlan pl = (tiles ? tree_plan : decode_plan)(n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms);
+  bool tiles = false;
+  const DecodePlan pl = plan(tree, n_seqs, Lq, Hq / Hkv, Hkv, d, max_pages, page_size, view.num_sms, &tiles);
   if (pl.bytes > 0 && (workspace == nullptr || workspace_bytes < pl.bytes)) return FA_ERR_SCRATCH;
   kv::DecodeParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -311,7 +328,8 @@ int attention(bool tree, const void* q, const void* cache, const int* page_table
   p.parents = parents;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (tiles) return d == 128 ? launch_tree<128>(p, pl, dev, s) : launch_tree<64>(p, pl, dev, s);
-  return tree ? launch_rows<true>(p, pl, d, dev, s) : launch_rows<false>(p, pl, d, dev, s);
+  if (tree) return d == 128 ? launch_rows<128, true>(p, pl, dev, s) : launch_rows<64, true>(p, pl, dev, s);
+  return d == 128 ? launch_rows<128, false>(p, pl, dev, s) : launch_rows<64, false>(p, pl, dev, s);
 }
 
 }  // namespace

@@ -672,3 +672,12 @@ def test_verify_does_not_depend_on_how_it_is_divided(draft, V, drawn):
     got = draft.verify_tree(wide.view(n * nodes, V + 5)[:, 5:], tokens, parents, u,
                             draft_probs=None if probs is None else probs.view(n * nodes, V))
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("nodes,hq", [(8, 1), (9, 1), (3, 4), (5, 3), (16, 1), (17, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[600, 3], [2000], [3000, 1, 0, 700, 2500, 2999, 129, 64, 4000]])
+def test_few_rows_over_little_and_much(draft, serve, nodes, hq, d, lens):
+    # on both sides of where the tensor core's tiles take over
+    parents = [ref.tree(cpu_generator(105 + i), nodes, roots=1 + i % 2) for i in range(len(lens))]
+    check_tree(draft, serve, lens, parents, hq, 1, d, 64, seed=106)
