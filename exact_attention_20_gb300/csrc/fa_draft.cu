@@ -59,7 +59,7 @@ Held held(int dev) {
 // CTAs of a sequence's cluster, and their threads.  A walk's passes follow one another,
 // so that a sequence wants as many warps as have a tile, but sequences that wait for
 // others to end want fewer: 256 threads where all clusters are on the card at once, else
-// 128 (fp32, 128000 tokens: 1, 16 and 48 sequences 31, 53 and 82 us with 256, 39, 66 and 80
+// 128 (fp32, 128000 tokens: 1, 16 and 48 sequences 30, 53 and 82 us with 256, 39, 66 and 75
 // with 128).  Clusters of eight, not of 16, leave the card idle
 // behind the sequences that are done (48 sequences, 164 us for 145 at the time).
 void shape(const Held& h, int n_seqs, int V, int* cluster, int* threads) {

@@ -61,10 +61,12 @@ constexpr int kRows = 128;             // of an item
 constexpr int kKeys = 128;             // of a tile
 constexpr int kTurnWarps = 8;          // four for K, four for V; two groups of a tile each
 constexpr int kThreads = 640;
-// An item's own cost, in tiles.  The 32 contexts: 112, 91, 84 and 84 us with 2, 4, 6
-// and 9 (the merge still with two rows a CTA).
+// An item's own cost, in tiles.  The 32 contexts: 72, 68 and 72 us with 5, 8 and 11, the
+// long one 133, 130 and 129.
 constexpr int kItemTiles = 8;
-constexpr int kMinTiles = 2;           // a CTA takes at least, where there are that many
+// A CTA takes at least, where there are that many.  16 nodes over 2000 tokens: 15.6, 16.9
+// and 20.5 us with 2, 4 and 8.
+constexpr int kMinTiles = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSiteTree = 8;           // status code: a wait gave up
 // Registers: the launch gives every thread 96 (65536 / 640, rounded down to 8).

@@ -9,8 +9,8 @@
 //     a <- max(0, a - q T),   T <- sum a,
 //
 // which is max(r - q, 0) normalised, r = a / T.  A node's children are drawn from one
-// q, so after several a = max(0, w - q S) with S the sum of their T.  A token given (no q) loses its
-// w.  The next token is the first x where a(0) + ... + a(x) > u_0 T.
+// q, so after several a = max(0, w - q S) with S the sum of their T.  A token given (no
+// q) loses its w.  The next token is the first x where a(0) + ... + a(x) > u_0 T.
 //
 // A running sum over 10^5 tokens meets u_0 T next to some token's border all
 // the time: with sums and exponentials in fp32 one call in a hundred would give
@@ -33,15 +33,16 @@
 // token is found by looking at one tile again.
 //
 // Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
-// 80 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
-// child is refused) would take 14 at the copy rate.  A quick pass is some 12
-// instructions a token, an exact one 30, or 43 with the draft's; a sequence's passes
-// (5.6 on average, 10 at the most) follow one another, 7 of them in 31 us on an idle
+// 75 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
+// child is refused) would take 14 at the copy rate.  A quick pass is some 17
+// instructions a token, an exact one 34, or 47 with the draft's; a sequence's passes
+// (5.6 on average, 10 at the most) follow one another, 7 of them in 30 us on an idle
 // card, where each waits for its first loads, two reductions and the cluster's
 // barrier.  All 48 together use 43 % of the issue slots while an SM has work.  One tree
 // of 16 nodes, 32000 tokens in bf16: 12.1 us.  What the steps brought at 48 sequences:
 // exact weights of 60 instructions, right to 2^-40, 111 us; 30, 93; one product with
-// q for all refused children, and fewer registers, 75 to 80.
+// q for all refused children, and fewer registers, 80; the quick pass's running
+// maximum without a branch 75.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -367,8 +368,8 @@ __device__ __forceinline__ Top join(const Top& mine, float c) {
   return all;
 }
 
-// The quick pass: the row's maximum and the lowest token that has it, and, unless
-// greedy, the sum of its weights to about 2^-24.
+// The quick pass: the row's maximum, and the lowest token that has it where greedy,
+// else the sum of the row's weights (kQuick).
 template <bool FP32>
 __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
                                          uint32_t size) {
@@ -396,16 +397,19 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
       top = fmax3(top, v[n][3], v[n][4]);
       top = fmax3(top, v[n][5], v[n][6]);
       top = fmaxf(top, v[n][7]);
-      if (top > best) {  // ascending tokens: the first of equals stays
-        sum *= ex2_approx((best - top) * p.c_hi);
-        best = top;
-        const int x = row.first(t + n * warps);
+      if (p.greedy) {
+        if (top > best) {  // ascending tokens: the first of equals stays
+          best = top;
+          const int x = row.first(t + n * warps);
 #pragma unroll
-        for (int i = 7; i >= 0; --i)
-          if (v[n][i] == top) where = x + i;
-      }
-      if (!p.greedy) {
-        const float shift = best == -INFINITY ? 0.f : best;
+          for (int i = 7; i >= 0; --i)
+            if (v[n][i] == top) where = x + i;
+        }
+      } else {
+        // no branch: one of a warp's lanes has a new maximum nearly every time
+        const float now = fmaxf(best, top), shift = now == -INFINITY ? 0.f : now;
+        sum *= ex2_approx((best - shift) * p.c_hi);
+        best = now;
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
