@@ -34,8 +34,8 @@
 //
 // Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
 // 75 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
-// child is refused) would take 14 at the copy rate.  A quick pass is some 17
-// instructions a token, an exact one 34, or 47 with the draft's; a sequence's passes
+// child is refused) would take 14 at the copy rate.  A quick pass is some 15
+// instructions a token, an exact one 50 with its loads and sums; a sequence's passes
 // (5.6 on average, 10 at the most) follow one another, 7 of them in 30 us on an idle
 // card, where each waits for its first loads, two reductions and the cluster's
 // barrier.  All 48 together use 43 % of the issue slots while an SM has work.  One tree
