@@ -244,8 +244,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
+// Another CTA's shared memory is there once that CTA has started, and until it ends.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  cluster_wait();
 }
 // A 64-bit store to the same place in CTA `rank`'s shared memory.
 __device__ __forceinline__ void store_to(uint32_t rank, void* where, long long v) {
@@ -369,10 +373,11 @@ __device__ __forceinline__ Top join(const Top& mine, float c) {
 }
 
 // The quick pass: the row's maximum, and the lowest token that has it where greedy,
-// else the sum of the row's weights (kQuick).
+// else the sum of the row's weights (kQuick).  `first`: the kernel's first pass, whose
+// exchange waits for the cluster's CTAs to have started, which the pass hides.
 template <bool FP32>
 __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
-                                         uint32_t size) {
+                                         uint32_t size, bool first) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   constexpr int kAtOnce = 2;  // tiles whose loads are in flight together
   float best = -INFINITY, sum = 0.f;  // the sum against `best`
@@ -427,6 +432,7 @@ __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, 
   if (lane == 0) s.tops[warp] = top;
   __syncthreads();
   top = join(lane < warps ? s.tops[lane] : none, c);
+  if (first && size > 1) cluster_wait();
   exchange(static_cast<long long>(static_cast<unsigned long long>(__float_as_uint(top.max)) << 32 | static_cast<uint32_t>(top.token)),
            __float_as_uint(top.sum), s, phase, rank, size);
   top = none;
@@ -545,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const long long seq = blockIdx.x / size, node0 = seq * p.n_nodes;
   const bool writer = rank == 0 && threadIdx.x == 0;
+  if (size > 1) cluster_started();
   if (threadIdx.x < 128) s.table[threadIdx.x] = kExp2[threadIdx.x];
   if (threadIdx.x < p.n_nodes) {
     s.parents[threadIdx.x] = p.parents[node0 + threadIdx.x];
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         if (row.q) draft = __ldg(row.q + x);
       }
     }
-    const Top top = row_quick(row, p, s, phase, rank, size);
+    const Top top = row_quick(row, p, s, phase, rank, size, kept == 1);
     const float M = top.max;
     long long T = __float2ll_rn(top.sum * 0x1p44f);
     int accepted = -1;
@@ -668,7 +675,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     __syncthreads();  // shared sums have been read
   }
   if (writer) p.n_kept[seq] = kept;
-  if (size > 1) cluster_sync();  // no CTA leaves while another may still store to it
+  if (size > 1) {
+    if (kept == 0) cluster_wait();  // no pass has
+    cluster_sync();  // no CTA leaves while another may still store to it
+  }
 }
 
 }  // namespace verify
