@@ -187,6 +187,14 @@ __device__ __forceinline__ Weight weight(float x, const Reference& ref, const Pa
   return Weight{v.x, __fmaf_rn(v.x, e, v.y), __int_as_float((k & ~127) * 65536 + 0x3f800000)};
 }
 
+// A drawn child's own, which is compared without rounding it to 2^-44: what lies further
+// below M than `low` is itself, to about 2^-16, and not 2^-64; -inf (and NaN) is 0.
+__device__ __forceinline__ Pair own_weight(float x, const Reference& ref, const Params& p, const float2* table) {
+  const float d = __fsub_rn(fmaxf(x, -INFINITY), ref.shift);
+  if (!(d < ref.low)) return weight(x, ref, p, table).pair();
+  return Pair{ex2_approx(__fsub_rn(d, ref.top) * p.c_hi), 0.f};
+}
+
 // a - q S, at least 0, for S as a sum of two floats.
 __device__ __forceinline__ Pair without(const Pair& a, float q, const float2& S) {
   const float h = __fmul_rn(q, S.x);
@@ -599,9 +607,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
     for (int j = cur + 1; j < p.n_nodes; ++j) {
       const int x = s.tokens[j];
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
-      const Weight own = weight(s.logit[j], ref, p, s.table);
       if (row.q) {
-        Pair a = own.pair();
+        Pair a = own_weight(s.logit[j], ref, p, s.table);
         const float q = s.draft[j], u = s.u[j];
         if (drawn) a = without(a, q, S);
         // u q T - a, and whether that has its sign for any T that the quick pass may stand for
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         stale = left <= 0;
         if (!stale) T = left, S = more, drawn = true;
       } else {
-        long long w = fixed44(own).value();
+        long long w = fixed44(weight(s.logit[j], ref, p, s.table)).value();
         for (int n = 0; n < gone; ++n)
           if (s.gone[n] == x) w = 0;
         bool sure = true;

@@ -31,3 +31,34 @@ def test_clusters_with_and_without_a_walk(draft, V, drawn):
     plain.check_verify(draft, logits, tokens, parents, u, probs, 1.0, range(1, n, 14))
     none = draft.verify_tree(logits, tokens, kv4.int32([[-2] * nodes] * n), u, draft_probs=probs)
     assert (none[0] == -1).all() and (none[1] == 0).all() and (none[2] == -1).all()
+
+
+@pytest.mark.parametrize("V", [300, 9000])
+@pytest.mark.parametrize("fp32", [True, False])
+def test_drawn_children_that_cannot_come(draft, V, fp32):
+    # (the child's target logit against the row's largest, its q, its number, whether it is kept): u q(x) < r(x)
+    inf, nan = float("inf"), float("nan")
+    cases = [(-inf, 0.1, 0.0, False), (nan, 0.1, 0.0, False), (-inf, 0.0, 0.9, False), (nan, 0.0, 0.9, False),
+             (-60.0, 1e-23, 0.9, False), (-60.0, 0.0, 0.9, True), (-60.0, 0.5, 0.0, True), (-40.0, 0.0, 0.9, True),
+             (-200.0, 1e-30, 0.9, False), (-1.0, 0.0, 0.9, True)]
+    n = 2 * len(cases)
+    g = kv4.generator(210)
+    logits = torch.randn((n, 3, V), generator=g, device=DEV)
+    probs = torch.full((n, 3, V), 0.4 / V, device=DEV)
+    u = torch.full((n, 3), 0.5, device=DEV)
+    x, y = 17, V - 20
+    tokens, parents = [], []
+    for i, (logit, q, number, _) in enumerate(cases * 2):
+        after = i >= len(cases)  # after a child that is refused: half of q is at it, and little of p
+        logits[i, 0, x], probs[i, 0, x] = float(logits[i, 0].max()) + logit, q
+        logits[i, 0, y], probs[i, 0, y] = -2.0, 0.5
+        u[i, 1], u[i, 2] = (0.999, number) if after else (number, 0.5)
+        tokens.append([0, y, x] if after else [0, x, -1])
+        parents.append([-1, 0, 0])
+    logits = logits.to(torch.float32 if fp32 else torch.bfloat16)
+    lengths = plain.check_verify(draft, logits, kv4.int32(tokens), parents, u, probs, 1.0)
+    assert [a == 2 for a in lengths[:len(cases)]] == [c[3] for c in cases]
+    path = draft.verify_tree(logits, kv4.int32(tokens), kv4.int32(parents), u, draft_probs=probs)[0]
+    kept = [row[1] == 2 for row in path[len(cases):].tolist()]
+    # what is left of a child is max(r - q, 0): of those with a q of their own above their r, nothing
+    assert kept == [c[3] and c[1] == 0.0 for c in cases] and not (path[len(cases):, 1] == 1).any()
