@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
       if (s.parents[j] != cur || x < 0 || x >= p.V) continue;
       if (row.q) {
         Pair a = own_weight(s.logit[j], ref, p, s.table);
-        const float q = s.draft[j], u = s.u[j];
+        const float q = s.draft[j], u = fminf(fmaxf(s.u[j], 0.f), 1.f);  // as fraction64
         if (drawn) a = without(a, q, S);
         // u q T - a, and whether that has its sign for any T that the quick pass may stand for
         bool sure = true;

@@ -73,7 +73,7 @@ int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, in
  *   tokens      : int32 [n_seqs][n_nodes].  A node whose token is outside
  *                 [0, V) is passed over; node 0's is not looked at.
  *   parents     : int32 [n_seqs][n_nodes].  A node that node 0 does not lead to is not looked at.
- *   uniforms    : fp32 [n_seqs][n_nodes], random numbers from [0, 1).
+ *   uniforms    : fp32 [n_seqs][n_nodes], random numbers from [0, 1); others are taken as its ends (NaN as 0).
  *   draft_probs : fp32 [n_seqs * n_nodes][V], rows draft_stride elements apart: row s *
  *                 n_nodes + i holds the distribution that node i's children
  *                 were drawn from (not read where it has none); or NULL.

@@ -62,3 +62,18 @@ def test_drawn_children_that_cannot_come(draft, V, fp32):
     kept = [row[1] == 2 for row in path[len(cases):].tolist()]
     # what is left of a child is max(r - q, 0): of those with a q of their own above their r, nothing
     assert kept == [c[3] and c[1] == 0.0 for c in cases] and not (path[len(cases):, 1] == 1).any()
+
+
+def test_numbers_outside_the_unit_interval_of_drawn_children(draft):
+    # they are taken as its ends, as those of given children are: below 0 and NaN as 0, from 1 on as 1
+    V = 64
+    u = torch.tensor([-1.0, float("nan"), -float("inf"), 0.0, 1.0, 7.0, float("inf")] * 3, device=DEV)
+    n = u.numel()
+    logits = torch.zeros((n, 2, V), device=DEV)
+    logits[:7, 0, 9] = -float("inf")               # a child that cannot come,
+    probs = torch.full((n, 2, V), 1.0 / V, device=DEV)
+    probs[7:14, 0, 9] = 0.5 / V                    # one that always comes,
+    probs[14:, 0, 9] = 2.0 / V                     # and one that comes below 1/2
+    numbers = torch.stack((torch.full_like(u, 0.3), u), 1)
+    kept = draft.verify_tree(logits, kv4.int32([[0, 9]] * n), kv4.int32([[-1, 0]] * n), numbers, draft_probs=probs)[1].tolist()
+    assert kept == [1] * 7 + [2] * 7 + [2, 2, 2, 2, 1, 1, 1]
