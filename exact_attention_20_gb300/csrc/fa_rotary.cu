@@ -49,23 +49,29 @@ struct Strided {
     }
     return true;
   }
-  // Its tokens' rows lie `token stride` apart throughout: one run of them, or batch entries that go on in step.
-  bool in_rows() const {
-    const long long row = (count[2] - 1) * stride[2] + d;
-    return stride[1] > 0 && row <= stride[1] && (count[0] < 2 || stride[0] % stride[1] == 0);
+  // The elements that one run of them takes of every `every`, counted from ptr: dimensions whose stride is a
+  // multiple of it fall on one another.
+  long long run(long long every) const {
+    long long e = d;
+    for (int i = 0; i < 3; ++i)
+      if (count[i] > 1 && stride[i] % every != 0) e += (count[i] - 1) * stride[i];
+    return e;
   }
 };
 
-// Whether two tensors share an element (may say so where rows interleave in ways that this does not see through).
+// Whether two tensors share an element (may say so where they interleave in ways that this does not see through).
 bool share(const Strided& a, const Strided& b) {
   if (!overlaps(a.ptr, a.bytes(), b.ptr, b.bytes())) return false;
-  // columns of the same rows, as q and k of one projection's output are
-  if (!a.in_rows() || !b.in_rows() || a.stride[1] != b.stride[1]) return true;
-  const long long s = a.stride[1] * 2;  // bytes
   const long long apart = static_cast<long long>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr));
-  const long long at = (apart % s + s) % s;
-  const long long wa = ((a.count[2] - 1) * a.stride[2] + a.d) * 2, wb = ((b.count[2] - 1) * b.stride[2] + b.d) * 2;
-  return at < wa || at + wb > s;
+  // Apart in every period of some stride's length, as columns of the same rows are (q and k of one projection's output:
+  // the token stride), or heads of the same batch entries (views of one [B, H, N, d]: the batch stride).
+  for (const Strided* t : {&a, &b})
+    for (int i = 0; i < 3; ++i) {
+      if (t->count[i] < 2 || t->stride[i] == 0) continue;
+      const long long s = t->stride[i] * 2, at = (apart % s + s) % s;  // bytes
+      if (a.run(t->stride[i]) * 2 <= at && at + b.run(t->stride[i]) * 2 <= s) return false;
+    }
+  return true;
 }
 
 }  // namespace
