@@ -77,3 +77,17 @@ def test_numbers_outside_the_unit_interval_of_drawn_children(draft):
     numbers = torch.stack((torch.full_like(u, 0.3), u), 1)
     kept = draft.verify_tree(logits, kv4.int32([[0, 9]] * n), kv4.int32([[-1, 0]] * n), numbers, draft_probs=probs)[1].tolist()
     assert kept == [1] * 7 + [2] * 7 + [2, 2, 2, 2, 1, 1, 1]
+
+
+@pytest.mark.parametrize("nodes,hq,hkv", [(4, 4, 2), (1, 8, 1), (3, 4, 2), (5, 3, 1), (16, 1, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_line_in_the_decode_kernel_is_the_newest_tokens_bit_by_bit(draft, nodes, hq, hkv, d):
+    # up to 8 rows of a KV head, and up to 16 over many contexts: the kernel that kv4_attention takes, with another mask
+    from exact_attention_20_gb300 import serve
+    lens = [700, nodes, 33 + nodes, 4000, 9001] + [3000 + 7 * i for i in range(60)] * (nodes * hq // hkv > 8)
+    cache, table, _, _ = kv4.fill(serve, lens, hkv, d, 64, 220)
+    q = torch.randn((len(lens) * nodes, hq, d), generator=kv4.generator(221), device=DEV).bfloat16()
+    line = kv4.int32([[-1] + list(range(nodes - 1))] * len(lens))
+    o, lse = draft.kv4_tree_attention(q, cache, table, kv4.int32(lens), line)
+    o2, lse2 = serve.kv4_attention(q, cache, table, kv4.int32(lens), n_queries=nodes)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
