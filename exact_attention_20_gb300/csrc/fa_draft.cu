@@ -130,6 +130,7 @@ int fa_verify_tree(const void* logits, int logits_fp32, const int* tokens, const
   }
   int size = 0, threads = 0;
   shape(held(dev), n_seqs, V, &size, &threads);
+  p.quick = vf::quick_bound(vf::lane_tiles(V, size, threads / 32));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(n_seqs) * size);
   cfg.blockDim = dim3(threads);

@@ -61,10 +61,20 @@ constexpr int kMaxVocab = 1 << 18;
 constexpr int kTile = 256;                        // tokens of a warp's step
 constexpr int kMaxTiles = kMaxVocab / kTile + 1;  // of a row that starts within a tile
 constexpr int kMaxCluster = 16;  // (more than 8 has to be asked for)
-// The quick pass's sum is right to 2^-16 of it: at most 34 products with a power of two
-// right to 2^-22, the powers' arguments to 2^-23.3 of themselves (17 where all tokens of
-// a row lie there), 40 additions.
-constexpr float kQuick = 0x1p-15f;
+// What the quick pass's sum may be off by, of it, twice over, where a lane takes `tiles` tiles.  A
+// weight is a power of two right to 2^-22 and is brought to a later maximum by at most `tiles`
+// products with such powers in the lane, each rounded to 2^-24, and three in the reductions;
+// a sum has 4 additions of a tile, one a tile and 15 of the reductions; the powers' arguments are right
+// to 2^-22.4 of themselves (17 where all tokens of a row lie there: 36 in 2^-24).  In 2^-24 that is
+// 5 (tiles + 4) + tiles + 19 + 36.  Up to 30 tiles it is 2^-15 at the most: clusters of 16 take 17.
+__host__ __device__ constexpr float quick_bound(int tiles) {
+  return 6 * tiles + 75 <= 256 ? 0x1p-15f : static_cast<float>(6 * tiles + 75) * 0x1p-23f;
+}
+// The most tiles of a lane of `warps` warps in each of `ctas`, wherever in a tile the row starts.
+__host__ __device__ constexpr int lane_tiles(int V, int ctas, int warps) {
+  const int tiles = (V + 7 + kTile - 1) / kTile, per = (tiles + ctas - 1) / ctas;
+  return (per + warps - 1) / warps;
+}
 constexpr float kSpan = 64.f;                     // powers of two below the maximum; what lies further is taken as 2^-64, which is rounded to 0
 constexpr float kFar = 16384.f;                   // of the maximum's power of two: above it, differences from it are taken first
 
@@ -128,6 +138,7 @@ struct Params {
   long long logits_stride, draft_stride;
   float c_hi, c_lo;  // log2(e) / temperature
   float span;        // kSpan of those
+  float quick;       // quick_bound of the tiles that a lane takes
   int greedy;        // temperature 0
 };
 
@@ -381,7 +392,7 @@ __device__ __forceinline__ Top join(const Top& mine, float c) {
 }
 
 // The quick pass: the row's maximum, and the lowest token that has it where greedy,
-// else the sum of the row's weights (kQuick).  `first`: the kernel's first pass, whose
+// else the sum of the row's weights (quick_bound).  `first`: the kernel's first pass, whose
 // exchange waits for the cluster's CTAs to have started, which the pass hides.
 template <bool FP32>
 __device__ __forceinline__ Top row_quick(const Row<FP32>& row, const Params& p, Shared& s, int& phase, uint32_t rank,
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
           const float uq = u * q, uq_lo = fmaf(u, q, -uq);
           const float h = uq * t.x, l = fmaf(uq, t.x, -h) + fmaf(uq, t.y, uq_lo * t.x);
           const float d = (h - a.hi) + (l - a.lo);
-          sure = exact || fabsf(d) > h * kQuick;
+          sure = exact || fabsf(d) > h * p.quick;
           return d;
         };
         float d = excess();
@@ -644,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Para
         bool sure = true;
         auto excess = [&]() {
           const long long h = static_cast<long long>(__umul64hi(fraction64(s.u[j]), static_cast<unsigned long long>(T)));
-          sure = exact || llabs(h - w) > static_cast<long long>(static_cast<float>(h) * kQuick) + 1;
+          sure = exact || llabs(h - w) > static_cast<long long>(static_cast<float>(h) * p.quick) + 1;
           return h - w;
         };
         long long d = excess();
