@@ -10,8 +10,8 @@
 // and the gradient of a by that of a' is the same with -sin.  A pair's speed is
 // a 64-bit fraction of a turn per position, so the angle of any 32-bit
 // position is one integer product, whose wrap drops whole turns and loses
-// nothing: the error is that of the speed's last bit times p, 2^-34 of a turn
-// at the most, where p times an fp32 speed would be off by 2^-24 of all the
+// nothing: the error is that of the speed's last bit times p, 2^-33 of a turn
+// at the most (a speed cut to 64 bits), where p times an fp32 speed would be off by 2^-24 of all the
 // turns made.
 //
 // Rotating alone rounds to bf16 once, and fp32 does (cos and sin to about

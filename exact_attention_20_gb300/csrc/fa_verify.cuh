@@ -29,17 +29,18 @@
 // none, a pass for the exact T, and one more for each drawn child that is not
 // accepted.  CTA r of the cluster takes the r-th part of the row's tiles of 256
 // tokens, a warp a tile at a time, a lane eight tokens, and every CTA takes every
-// decision from the same numbers.  Tiles' sums stay in shared memory, so that the
+// decision from the same numbers, which the CTAs store to one another's shared memory
+// once all have started.  Tiles' sums stay in shared memory, so that the
 // token is found by looking at one tile again.
 //
 // Measured on a GB300: 48 sequences' trees of 24 drawn nodes, 128000 tokens in fp32,
-// 75 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
+// 75 to 76 us; the 96 MB of rows that are visited (3.3 a sequence, and the draft's where a
 // child is refused) would take 14 at the copy rate.  A quick pass is some 15
 // instructions a token, an exact one 50 with its loads and sums; a sequence's passes
 // (5.6 on average, 10 at the most) follow one another, 7 of them in 30 us on an idle
 // card, where each waits for its first loads, two reductions and the cluster's
 // barrier.  All 48 together use 43 % of the issue slots while an SM has work.  One tree
-// of 16 nodes, 32000 tokens in bf16: 12.1 us.  What the steps brought at 48 sequences:
+// of 16 nodes, 32000 tokens in bf16: 12.3 us (6.0 at temperature 0).  What the steps brought at 48 sequences:
 // exact weights of 60 instructions, right to 2^-40, 111 us; 30, 93; one product with
 // q for all refused children, and fewer registers, 80; the quick pass's running
 // maximum without a branch 75.

@@ -114,7 +114,9 @@ def fa_kv4_tree_attention(q, cache, page_table, seq_lens, parents, o, lse, scale
     and values are the last ``nodes`` of seq_lens[i] positions.  q: bf16
     [sequences * nodes, Hq, d], any token stride; node i sees the context and
     its line down to itself.  A place without a node gets O = 0, LSE = -inf.
-    o: bf16 like q, lse: fp32 [Hq, sequences * nodes], contiguous.
+    o: bf16 like q, lse: fp32 [Hq, sequences * nodes], contiguous.  Small trees
+    over short contexts are quickest with a page_table not much wider than the
+    longest sequence: how a call is divided goes by its width.
     """
     if o is None or lse is None:
         raise TypeError("o and lse must be torch.Tensors")
@@ -197,7 +199,7 @@ def fa_verify_tree(logits, tokens, parents, uniforms, path, n_kept, next_token, 
     last token, decided already.  uniforms: fp32 [sequences, nodes] from [0, 1):
     node j's decides on it, node 0's draws the next token.  draft_probs: fp32
     like logits, row i what node i's children were drawn from; None: children
-    are given, not drawn.  temperature 0: the likeliest token alone.
+    are given, not drawn.  temperature, of all sequences: 0 is the likeliest token alone.
     path: int32 [sequences, nodes], the kept nodes and then -1; n_kept (node 0
     counts) and next_token: int32 [sequences].  What comes out is distributed as
     the target's own samples, whatever the draft.

@@ -37,7 +37,9 @@ extern "C" {
  *       s * n_nodes + i is node i of sequence s.
  *   o, lse : as fa_kv4_attention's.  A place without a node gets O = 0 and
  *       LSE = -inf, whatever q holds there.
- * Everything else is as for fa_kv4_attention.
+ * Everything else is as for fa_kv4_attention.  How a call is divided goes by the
+ * table's width, max_pages: small trees over short contexts are quickest (by a
+ * tenth to a fifth) under a table not much wider than the longest sequence.
  */
 int fa_kv4_tree_attention(const void* q, const void* cache, const int* page_table, const int* seq_lens,
                           const int* parents, void* o, float* lse, int n_seqs, int n_nodes, int Hq, int Hkv, int d,
@@ -77,7 +79,7 @@ int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, in
  *   draft_probs : fp32 [n_seqs * n_nodes][V], rows draft_stride elements apart: row s *
  *                 n_nodes + i holds the distribution that node i's children
  *                 were drawn from (not read where it has none); or NULL.
- *   temperature : above 0; or 0, the target's likeliest token (the lowest of equals) with
+ *   temperature : of all sequences; above 0; or 0, the target's likeliest token (the lowest of equals) with
  *                 probability 1.
  *   path        : int32 [n_seqs][n_nodes]; written: the kept nodes in order, node 0 first,
  *                 then -1.
@@ -88,7 +90,8 @@ int fa_kv4_tree_attention_workspace(int n_seqs, int n_nodes, int Hq, int Hkv, in
  *
  * Probabilities are taken to 2^-44 of a row's largest (exponentials right to 2^-29,
  * sums in 64-bit integers): where a running sum passes a random number hardly
- * ever depends on roundings, and never on how the work is divided.
+ * ever depends on roundings, and never on how the work is divided.  A drawn child's
+ * own r(x) is taken as it is down to 2^-126 of the largest, and as 0 below.
  * V <= 2^18.  One launch.  Errors: FA_ERR_INVALID_ARG, FA_ERR_NULL, FA_ERR_ALIGN (each
  * pointer to its element's size), FA_ERR_ALIAS, FA_ERR_DEVICE, FA_ERR_LAUNCH.
  */
